@@ -10,7 +10,8 @@ non-OK status raises :class:`ZppError`.
 
 The short helpers (:func:`quantize`, :func:`dequantize`, :func:`reorder`,
 :func:`dequant_reduce_requant`, :func:`dequant_reduce_average`,
-:func:`quantize_reordered`) allocate their outputs with torch on the
+:func:`quantize_reordered`, :func:`linear`, :func:`linear_grad`,
+:func:`layer_norm`, :func:`layer_norm_grad`) allocate their outputs with torch on the
 input's device and call the same entry points.
 
 Importing the package fails with ``ImportError`` when ``libzpp.so`` has not
@@ -42,9 +43,13 @@ ZPP_MAX_BLOCK = 4096
 ZPP_MAX_INPUTS = 4096
 ZPP_MAX_DIVISOR = 1 << 24
 ZPP_MAX_NUMEL = 1 << 40
+ZPP_MAX_FEATURES = 1 << 26
+ZPP_MAX_ROWS = 1 << 30
 
 EXPORTED = ("zpp_quantize_blocks", "zpp_quantize_reordered", "zpp_dequantize_blocks", "zpp_reorder_slices",
             "zpp_dequant_reduce_requant", "zpp_dequant_reduce_requant_split", "zpp_dequant_reduce_average",
+            "zpp_linear_blocks", "zpp_linear_blocks_grad", "zpp_linear_blocks_workspace", "zpp_layer_norm",
+            "zpp_layer_norm_grad", "zpp_layer_norm_grad_workspace",
             "zpp_set_pointer_checks", "zpp_status_string", "zpp_abi_version")
 
 
@@ -69,11 +74,19 @@ def _load() -> ctypes.CDLL:
         "zpp_dequant_reduce_requant": [P, I64, P, I64, I32, I32, I64, I32, P, P, I32, P, P],
         "zpp_dequant_reduce_requant_split": [P, I64, P, I64, I32, I32, I64, I32, I64, I64, P, P, P, P, I32, P],
         "zpp_dequant_reduce_average": [P, I64, P, I64, I32, I32, I64, I32, I32, P, P],
+        "zpp_linear_blocks": [P, I32, I64, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
+        "zpp_linear_blocks_grad": [P, I32, I64, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
+        "zpp_layer_norm": [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, P, I64, P, P, P],
+        "zpp_layer_norm_grad": [P, I64, P, I32, I64, I64, I64, P, I32, P, P, P, I64, P, P, P, I64, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = ctypes.c_int
+    lib.zpp_linear_blocks_workspace.argtypes = [I32, I32, I32, I64, I64, I64]
+    lib.zpp_linear_blocks_workspace.restype = I64
+    lib.zpp_layer_norm_grad_workspace.argtypes = [I64, I64]
+    lib.zpp_layer_norm_grad_workspace.restype = I64
     lib.zpp_set_pointer_checks.argtypes = [ctypes.c_int32]
     lib.zpp_set_pointer_checks.restype = ctypes.c_int32
     lib.zpp_status_string.argtypes = [ctypes.c_int]
@@ -156,6 +169,40 @@ def zpp_dequant_reduce_average(codes_in, codes_stride_bytes, scales_in, scales_s
                                block, divisor, avg_out, stream=None) -> None:
     _call("zpp_dequant_reduce_average", _ptr(codes_in), codes_stride_bytes, _ptr(scales_in), scales_stride,
           n_inputs, bits_in, numel, block, divisor, _ptr(avg_out), _stream(stream))
+
+
+def zpp_linear_blocks(x, x_dtype, x_stride, rows, codes, scales, bits, out_features, in_features, block, y, y_dtype,
+                      y_stride, workspace, workspace_bytes, stream=None) -> None:
+    _call("zpp_linear_blocks", _ptr(x), x_dtype, x_stride, rows, _ptr(codes), _ptr(scales), bits, out_features,
+          in_features, block, _ptr(y), y_dtype, y_stride, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def zpp_linear_blocks_grad(dy, dy_dtype, dy_stride, rows, codes, scales, bits, out_features, in_features, block, dx,
+                           dx_dtype, dx_stride, workspace, workspace_bytes, stream=None) -> None:
+    _call("zpp_linear_blocks_grad", _ptr(dy), dy_dtype, dy_stride, rows, _ptr(codes), _ptr(scales), bits,
+          out_features, in_features, block, _ptr(dx), dx_dtype, dx_stride, _ptr(workspace), workspace_bytes,
+          _stream(stream))
+
+
+def zpp_linear_blocks_workspace(grad, in_dtype, out_dtype, rows, out_features, in_features) -> int:
+    return int(_lib.zpp_linear_blocks_workspace(grad, in_dtype, out_dtype, rows, out_features, in_features))
+
+
+def zpp_layer_norm(x, x_dtype, x_stride, rows, width, weight, bias, w_dtype, eps, y, y_stride, mean, rstd,
+                   stream=None) -> None:
+    _call("zpp_layer_norm", _ptr(x), x_dtype, x_stride, rows, width, _ptr(weight), _ptr(bias), w_dtype, eps, _ptr(y),
+          y_stride, _ptr(mean), _ptr(rstd), _stream(stream))
+
+
+def zpp_layer_norm_grad(dy, dy_stride, x, x_dtype, x_stride, rows, width, weight, w_dtype, mean, rstd, dx, dx_stride,
+                        dweight, dbias, workspace, workspace_bytes, stream=None) -> None:
+    _call("zpp_layer_norm_grad", _ptr(dy), dy_stride, _ptr(x), x_dtype, x_stride, rows, width, _ptr(weight), w_dtype,
+          _ptr(mean), _ptr(rstd), _ptr(dx), dx_stride, _ptr(dweight), _ptr(dbias), _ptr(workspace), workspace_bytes,
+          _stream(stream))
+
+
+def zpp_layer_norm_grad_workspace(rows, width) -> int:
+    return int(_lib.zpp_layer_norm_grad_workspace(rows, width))
 
 
 def zpp_set_pointer_checks(enabled: bool) -> bool:
@@ -308,3 +355,134 @@ def dequant_reduce_average(codes_in, scales_in, n_inputs: int, bits_in: int, num
     avg = torch.empty(numel, dtype=torch.float32, device=codes_in.device)
     zpp_dequant_reduce_average(codes_in, cs, scales_in, ss, n_inputs, bits_in, numel, block, divisor, avg, stream)
     return avg
+
+
+def _rows(t, name: str):
+    """(rows, width, row stride in elements) of a tensor whose leading dimensions
+    follow one stride and whose last one is contiguous."""
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    width = t.shape[-1]
+    rows = t.numel() // width if width else 0
+    if rows <= 1:
+        if width > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+        return rows, width, width
+    if t.dim() > 2 and t.is_contiguous():
+        return rows, width, width
+    lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    if (width > 1 and t.stride(-1) != 1) or any(a[1] != b[0] * b[1] for a, b in zip(lead, lead[1:])):
+        raise ValueError(f"{name} must be rows of contiguous elements with one stride between them")
+    return rows, width, lead[-1][1]
+
+
+def _check_weight(codes, scales, bits: int, block: int, numel: int) -> None:
+    import torch
+
+    _need_contiguous(codes=codes, scales=scales)
+    if codes.element_size() != 1 or scales.dtype != torch.float32:
+        raise TypeError("codes must be bytes and scales float32")
+    if codes.numel() * 8 != numel * bits or scales.numel() * block != numel:
+        raise ValueError(f"codes and scales do not hold {numel} weights in {bits}-bit blocks of {block}")
+
+
+def _linear(grad: bool, a, codes, scales, bits, block, out_len, dtype, out, workspace, stream):
+    import torch
+
+    rows, width, stride = _rows(a, "dy" if grad else "x")
+    out_features, in_features = (width, out_len) if grad else (out_len, width)
+    _check_weight(codes, scales, bits, block, out_features * in_features)
+    if out is None:
+        out = torch.empty(*a.shape[:-1], out_len, dtype=dtype or a.dtype, device=a.device)
+    elif tuple(out.shape) != (*a.shape[:-1], out_len):
+        raise ValueError(f"out must be of shape {(*a.shape[:-1], out_len)}")
+    ostride = _rows(out, "out")[2]
+    adt, odt = _dtype_code(a), _dtype_code(out)
+    need = zpp_linear_blocks_workspace(int(grad), adt, odt, rows, out_features, in_features)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+    call = zpp_linear_blocks_grad if grad else zpp_linear_blocks
+    call(a, adt, stride, rows, codes, scales, bits, out_features, in_features, block, out, odt, ostride, workspace,
+         0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+    return out
+
+
+def linear(x, codes, scales, bits: int, block: int, out_features: int, dtype=None, out=None, workspace=None,
+           stream=None):
+    """x @ W.T for x [..., in_features] and the [out_features, in_features] weight
+    that ``quantize`` turned into codes and scales. The result is of ``dtype``
+    (x's by default), or written into ``out``. ``workspace``, if given, is a
+    device tensor of at least ``zpp_linear_blocks_workspace`` bytes; with a
+    ``stream`` that is not torch's current one, pass ``out`` and ``workspace``
+    (memory torch allocates here belongs to its current stream)."""
+    return _linear(False, x, codes, scales, bits, block, out_features, dtype, out, workspace, stream)
+
+
+def linear_grad(dy, codes, scales, bits: int, block: int, in_features: int, dtype=None, out=None, workspace=None,
+                stream=None):
+    """dy @ W: the gradient of :func:`linear` with respect to x, for dy
+    [..., out_features]. Arguments as there."""
+    return _linear(True, dy, codes, scales, bits, block, in_features, dtype, out, workspace, stream)
+
+
+def _check_norm(width: int, **vectors):
+    """The shared dtype code of the given weight-like vectors (None: left out)."""
+    code = None
+    for name, v in vectors.items():
+        if v is None:
+            continue
+        _need_contiguous(**{name: v})
+        if v.numel() != width:
+            raise ValueError(f"{name} must have {width} elements")
+        if code is not None and _dtype_code(v) != code:
+            raise TypeError("weight and bias must be of one dtype")
+        code = _dtype_code(v)
+    return code
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
+    """Layer norm over x's last dimension. Returns (y, mean, rstd): y of x's
+    shape and dtype (or ``out``), mean and rstd float32, one each per row, as
+    :func:`layer_norm_grad` takes them."""
+    import torch
+
+    rows, width, stride = _rows(x, "x")
+    wdt = _check_norm(width, weight=weight, bias=bias) or _dtype_code(x)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must be of x's shape and dtype")
+    stats = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean, rstd = stats[0], stats[1]
+    zpp_layer_norm(x, _dtype_code(x), stride, rows, width, weight, bias, wdt, eps, out, _rows(out, "out")[2], mean,
+                   rstd, stream)
+    return out, mean, rstd
+
+
+def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype=None, stream=None):
+    """Backward pass of :func:`layer_norm`. Returns (dx, dweight, dbias); the
+    last two in weight's dtype (``w_dtype``, or x's, when weight is None).
+    ``workspace``, if given, is a device tensor of at least
+    ``zpp_layer_norm_grad_workspace(rows, width)`` bytes."""
+    import torch
+
+    rows, width, stride = _rows(x, "x")
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must be of x's shape and dtype")
+    _need_contiguous(mean=mean, rstd=rstd)
+    if mean.numel() != rows or rstd.numel() != rows or mean.dtype != torch.float32 or rstd.dtype != torch.float32:
+        raise ValueError("mean and rstd must be float32, one element per row")
+    wt = weight.dtype if weight is not None else (w_dtype or x.dtype)
+    _check_norm(width, weight=weight)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must be of x's shape and dtype")
+    dw = torch.empty(width, dtype=wt, device=x.device)
+    db = torch.empty(width, dtype=wt, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(zpp_layer_norm_grad_workspace(rows, width), dtype=torch.uint8, device=x.device)
+    zpp_layer_norm_grad(dy, _rows(dy, "dy")[2], x, _dtype_code(x), stride, rows, width, weight, _dtype_code(dw), mean,
+                        rstd, out, _rows(out, "out")[2], dw, db, workspace,
+                        workspace.numel() * workspace.element_size(), stream)
+    return out, dw, db

@@ -20,8 +20,10 @@ OBJDIR = os.path.join(ROOT, "_build", "zpp")
 ARCH = os.environ.get("ZPP_OFFLOAD_ARCH", "gfx950")
 
 DRR_UNITS = [f"drr_in{i}_out{o}.hip" for i in (4, 8) for o in (0, 4, 8)]
-SOURCES = ["quantize.hip", "dequantize.hip", "reorder.hip", "drr.hip", *DRR_UNITS, "zpp_api.hip"]
-HEADERS = ["zpp_device.h", "zpp_launch.h", "drr_kernel.h"]
+LINEAR_UNITS = [f"linear_tile_{d}{b}.hip" for d in ("fwd", "grad") for b in (4, 8)] + ["linear_few.hip"]
+SOURCES = ["quantize.hip", "dequantize.hip", "reorder.hip", "drr.hip", *DRR_UNITS, "linear.hip", *LINEAR_UNITS,
+           "layer_norm.hip", "zpp_api.hip"]
+HEADERS = ["zpp_device.h", "zpp_launch.h", "drr_kernel.h", "linear_device.h", "linear_tile.h"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -60,8 +62,8 @@ def build(jobs: int | None = None) -> str:
     """Compile every source and link ``libzpp.so``. Always rebuilds."""
     os.makedirs(OBJDIR, exist_ok=True)
     jobs = jobs or max(1, min(len(SOURCES), os.cpu_count() or 1, 16))
-    # the hop-kernel units take longest: start them first
-    order = sorted(SOURCES, key=lambda f: not f.startswith("drr_in"))
+    # the units of many kernels take longest: start them first
+    order = sorted(SOURCES, key=lambda f: not f.startswith(("linear_", "layer_norm", "drr_in")))
     with ThreadPoolExecutor(jobs) as ex:
         objs = list(ex.map(_compile, order))
     tmp = LIB + f".tmp{os.getpid()}"

@@ -1,0 +1,146 @@
+// linear.hip - which kernels a linear product on block codes takes, and the
+// sum of the parts of a split contraction.
+#include <algorithm>
+
+#include "linear_device.h"
+
+namespace zpp {
+
+hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
+hipError_t launch_linear_tile_fwd4(const LinArgs &p, int mode, int mt, hipStream_t stream);
+hipError_t launch_linear_tile_fwd8(const LinArgs &p, int mode, int mt, hipStream_t stream);
+hipError_t launch_linear_tile_grad4(const LinArgs &p, int mode, int mt, hipStream_t stream);
+hipError_t launch_linear_tile_grad8(const LinArgs &p, int mode, int mt, hipStream_t stream);
+
+namespace {
+
+constexpr int64_t kCus = 256;       // MI355X
+constexpr int64_t kFewRows = 64;    // forward: at most this many rows stream the codes
+constexpr int64_t kMaxTiles = 1 << 23;  // workgroups of one launch
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+    bool few;
+    int mt;       // rows of 16 per workgroup
+    int splits;   // parts of the contraction
+    int64_t split_steps;
+    int64_t rows; // rows of one launch
+};
+
+// Rows per workgroup: 256 (128 where operands have three parts) as long as
+// that still gives every CU a tile, 64 or 16 otherwise. Where even those
+// leave CUs idle, the contraction is split over workgroups, in parts of four
+// steps or more, and a second kernel sums the parts in order.
+Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
+    Plan p{};
+    if (!grad && rows <= kFewRows) {
+        p.few = true;
+        p.splits = 1;
+        p.rows = rows;
+        return p;
+    }
+    const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
+    const int64_t col_tiles = ceil_div(len, 256), steps = ceil_div(c_len, 64);
+    const int big = in_f32 || out_f32 ? 8 : 16;
+    p.mt = rows <= 16 ? 1 : (ceil_div(rows, 16 * big) * col_tiles >= kCus * 3 / 4 ? big : 4);
+    const int64_t tiles = ceil_div(rows, 16 * p.mt) * col_tiles;
+    int64_t splits = 1;
+    if (tiles < kCus) splits = std::min({kCus / tiles, std::max<int64_t>(steps / 4, 1), INT64_C(64)});
+    p.split_steps = ceil_div(steps, splits);
+    p.splits = static_cast<int>(ceil_div(steps, p.split_steps));
+    p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
+    return p;
+}
+
+// out[r][c] = sum of the parts, in order, 4 columns a thread.
+__global__ __launch_bounds__(kBlockThreads) void linear_join_kernel(const float *__restrict__ partial, int splits,
+                                                                    int64_t rows, int64_t len, void *out,
+                                                                    int64_t ldo, int out_f32) {
+    const int64_t ldp = (len + 3) & ~INT64_C(3), per = ldp / 4;
+    const int64_t n = static_cast<int64_t>(gridDim.x) * kBlockThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlockThreads + threadIdx.x; i < rows * per; i += n) {
+        const int64_t r = i / per, c = (i - r * per) * 4;
+        f32x4 v = {0, 0, 0, 0};
+        for (int s = 0; s < splits; ++s) v += ld<f32x4>(partial + (s * rows + r) * ldp + c);
+        const bool whole = (ldo & 3) == 0 && c + 4 <= len;
+        if (out_f32) {
+            float *o = static_cast<float *>(out) + r * ldo + c;
+            if (whole) {
+                st<f32x4>(o, v);
+            } else {
+                for (int t = 0; t < 4; ++t)
+                    if (c + t < len) o[t] = v[t];
+            }
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(out) + r * ldo + c;
+            const uint32_t a = pack_rn(v[0], v[1]), b = pack_rn(v[2], v[3]);
+            if (whole) {
+                st<u32x2>(o, u32x2{a, b});
+            } else {
+                for (int t = 0; t < 4; ++t)
+                    if (c + t < len) o[t] = static_cast<uint16_t>((t < 2 ? a : b) >> (16 * (t & 1)));
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int64_t linear_workspace(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
+    if (rows == 0) return 0;
+    const Plan p = make_plan(grad, in_f32, out_f32, rows, n_out, n_in);
+    if (p.splits == 1) return 0;
+    const int64_t len = grad ? n_in : n_out;
+    return p.splits * std::min(rows, p.rows) * ((len + 3) & ~INT64_C(3)) * 4;
+}
+
+hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int64_t rows, const void *codes,
+                         const float *scales, int bits, int64_t n_out, int64_t n_in, int log2b, void *out,
+                         bool out_f32, int64_t ldo, void *workspace, hipStream_t stream) {
+    const Plan plan = make_plan(grad, in_f32, out_f32, rows, n_out, n_in);
+    const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
+    const int mode = in_f32 ? 3 : out_f32 ? 2 : (lda % 8 == 0 && c_len % 8 == 0) ? 0 : 1;
+    for (int64_t r0 = 0; r0 < rows; r0 += plan.rows) {
+        LinArgs p{};
+        p.a = static_cast<const uint8_t *>(a) + r0 * lda * (in_f32 ? 4 : 2);
+        p.lda = lda;
+        p.rows = std::min(rows - r0, plan.rows);
+        p.codes = static_cast<const uint8_t *>(codes);
+        p.scales = scales;
+        p.n_out = n_out;
+        p.n_in = n_in;
+        p.log2b = log2b;
+        p.out = static_cast<uint8_t *>(out) + r0 * ldo * (out_f32 ? 4 : 2);
+        p.ldo = ldo;
+        p.out_f32 = out_f32;
+        p.partial = static_cast<float *>(workspace);
+        p.splits = plan.splits;
+        p.split_steps = plan.split_steps;
+        hipError_t e;
+        if (plan.few) {
+            e = launch_linear_few(p, bits, in_f32, stream);
+        } else {
+            p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
+            p.col_tiles = ceil_div(len, 256);
+            if (grad)
+                e = bits == 4 ? launch_linear_tile_grad4(p, mode, plan.mt, stream)
+                              : launch_linear_tile_grad8(p, mode, plan.mt, stream);
+            else
+                e = bits == 4 ? launch_linear_tile_fwd4(p, mode, plan.mt, stream)
+                              : launch_linear_tile_fwd8(p, mode, plan.mt, stream);
+        }
+        if (e != hipSuccess) return e;
+        if (plan.splits > 1) {
+            const int64_t threads = p.rows * ((len + 3) / 4);
+            const int64_t grid = std::min<int64_t>(ceil_div(threads, kBlockThreads), 1 << 16);
+            linear_join_kernel<<<static_cast<unsigned>(grid), kBlockThreads, 0, stream>>>(
+                p.partial, p.splits, p.rows, len, p.out, ldo, out_f32);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
+}  // namespace zpp

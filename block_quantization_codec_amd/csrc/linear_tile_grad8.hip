@@ -1,0 +1,10 @@
+// The tiled products on 8-bit codes: dx = dy W.
+#include "linear_tile.h"
+
+namespace zpp {
+
+hipError_t launch_linear_tile_grad8(const LinArgs &p, int mode, int mt, hipStream_t stream) {
+    return launch_linear_tile_as<true, 8>(p, mode, mt, stream);
+}
+
+}  // namespace zpp

@@ -10,6 +10,7 @@
 // launched and every output untouched.
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/zpp.h"
 #include "zpp_device.h"
@@ -179,6 +180,72 @@ zpp_status launch_checked(Launch &&launch) {
 }
 
 int64_t code_bytes(int64_t numel, int32_t bits) { return numel * bits / 8; }
+
+bool is_dtype(int32_t t) { return t == ZPP_BF16 || t == ZPP_FP32; }
+
+int64_t dtype_bytes(int32_t t) { return t == ZPP_BF16 ? 2 : 4; }
+
+// A row stride that keeps every offset of the matrix within ZPP_MAX_NUMEL elements.
+bool is_stride(int64_t stride, int64_t rows, int64_t width) {
+    return stride >= width && stride <= ZPP_MAX_NUMEL && (rows < 2 || stride <= ZPP_MAX_NUMEL / (rows - 1));
+}
+
+// From a matrix's first element to its last.
+Range matrix(const void *p, int64_t rows, int64_t stride, int64_t width, int32_t dtype) {
+    return Range{p, p && rows > 0 ? ((rows - 1) * stride + width) * dtype_bytes(dtype) : 0};
+}
+
+bool is_linear_size(int64_t rows, int64_t n_out, int64_t n_in) {
+    return rows >= 0 && rows <= ZPP_MAX_ROWS && n_out >= 1 && n_out <= ZPP_MAX_FEATURES && n_in >= 32 &&
+           n_in <= ZPP_MAX_FEATURES && n_in % 32 == 0 && n_out <= ZPP_MAX_NUMEL / n_in;
+}
+
+bool is_norm_size(int64_t rows, int64_t width) {
+    return rows >= 0 && rows <= ZPP_MAX_ROWS && width >= 1 && width <= ZPP_MAX_FEATURES;
+}
+
+// y = x W^T, or with `grad` dx = dy W: `a` and `out` are [rows, a_len] and [rows, out_len].
+zpp_status linear(bool grad, const void *a, int32_t a_dtype, int64_t a_stride, int64_t rows, const void *codes,
+                  const float *scales, int32_t bits, int64_t n_out, int64_t n_in, int32_t block, void *out,
+                  int32_t out_dtype, int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!is_dtype(a_dtype) || !is_dtype(out_dtype)) return ZPP_ERR_ARG;
+    if (bits != 8 && bits != 4) return ZPP_ERR_ARG;
+    if (!is_linear_size(rows, n_out, n_in)) return ZPP_ERR_ARG;
+    if (!is_pow2_block(block) || n_out * n_in % block != 0) return ZPP_ERR_ARG;
+    const int64_t a_len = grad ? n_out : n_in, out_len = grad ? n_in : n_out;
+    if (!is_stride(a_stride, rows, a_len) || !is_stride(out_stride, rows, out_len)) return ZPP_ERR_ARG;
+    if (workspace_bytes < 0) return ZPP_ERR_ARG;
+    if (rows == 0) return ZPP_OK;
+    const int64_t need = zpp::linear_workspace(grad, a_dtype == ZPP_FP32, out_dtype == ZPP_FP32, rows, n_out, n_in);
+    if (workspace_bytes < need) return ZPP_ERR_ARG;
+    if (!a || !codes || !scales || !out || (need > 0 && !workspace)) return ZPP_ERR_NULL;
+    if (!aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return ZPP_ERR_ALIGN;
+    if (need > 0 && !aligned(workspace, 16)) return ZPP_ERR_ALIGN;
+    // the side of in_features moves in 16-byte pieces
+    const int64_t wide = grad ? out_stride * dtype_bytes(out_dtype) : a_stride * dtype_bytes(a_dtype);
+    if (rows > 1 && wide % 16 != 0) return ZPP_ERR_ALIGN;
+    const Range ra = matrix(a, rows, a_stride, a_len, a_dtype), rc{codes, code_bytes(n_out * n_in, bits)},
+        rs{scales, 4 * (n_out * n_in / block)}, ro = matrix(out, rows, out_stride, out_len, out_dtype),
+        rw{workspace, need};
+    for (const Range &r : {ra, rc, rs}) {
+        if (overlap(ro, r) || overlap(rw, r)) return ZPP_ERR_OVERLAP;
+    }
+    if (overlap(ro, rw)) return ZPP_ERR_OVERLAP;
+    const Range all[] = {ra, rc, rs, ro, rw};
+    if (zpp_status s = check_all(all); s != ZPP_OK) return s;
+    // one row has no stride to speak of: a well-formed one, so that the kernels' rules see whole pieces
+    if (rows == 1) {
+        if (grad)
+            out_stride = n_in;
+        else
+            a_stride = n_in;
+    }
+    return launch_checked([&] {
+        return zpp::launch_linear(grad, a, a_dtype == ZPP_FP32, a_stride, rows, codes, scales, bits, n_out, n_in,
+                   log2_of(block), out, out_dtype == ZPP_FP32, out_stride, workspace,
+                   static_cast<hipStream_t>(stream));
+    });
+}
 
 }  // namespace
 
@@ -368,6 +435,97 @@ zpp_status zpp_dequant_reduce_average(const void *codes_in, int64_t codes_stride
         return zpp::launch_drr_average(codes_in, codes_stride_bytes, scales_in, scales_stride, n_inputs, bits_in,
                    numel, log2_of(block), divisor, avg_out, static_cast<hipStream_t>(stream));
     });
+}
+
+zpp_status zpp_linear_blocks(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, const void *codes,
+                             const float *scales, int32_t bits, int64_t out_features, int64_t in_features,
+                             int32_t block, void *y, int32_t y_dtype, int64_t y_stride, void *workspace,
+                             int64_t workspace_bytes, void *stream) {
+    return linear(false, x, x_dtype, x_stride, rows, codes, scales, bits, out_features, in_features, block, y,
+                  y_dtype, y_stride, workspace, workspace_bytes, stream);
+}
+
+zpp_status zpp_linear_blocks_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, int64_t rows,
+                                  const void *codes, const float *scales, int32_t bits, int64_t out_features,
+                                  int64_t in_features, int32_t block, void *dx, int32_t dx_dtype, int64_t dx_stride,
+                                  void *workspace, int64_t workspace_bytes, void *stream) {
+    return linear(true, dy, dy_dtype, dy_stride, rows, codes, scales, bits, out_features, in_features, block, dx,
+                  dx_dtype, dx_stride, workspace, workspace_bytes, stream);
+}
+
+int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int32_t out_dtype, int64_t rows,
+                                    int64_t out_features, int64_t in_features) {
+    if (!is_dtype(in_dtype) || !is_dtype(out_dtype) || !is_linear_size(rows, out_features, in_features)) return 0;
+    return zpp::linear_workspace(grad != 0, in_dtype == ZPP_FP32, out_dtype == ZPP_FP32, rows, out_features,
+                                 in_features);
+}
+
+zpp_status zpp_layer_norm(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t width,
+                          const void *weight, const void *bias, int32_t w_dtype, float eps, void *y,
+                          int64_t y_stride, float *mean, float *rstd, void *stream) {
+    if (!is_dtype(x_dtype) || !is_dtype(w_dtype)) return ZPP_ERR_ARG;
+    if (!is_norm_size(rows, width)) return ZPP_ERR_ARG;
+    if (!is_stride(x_stride, rows, width) || !is_stride(y_stride, rows, width)) return ZPP_ERR_ARG;
+    if (!(eps >= 0.0f) || eps > 3.402823466e38f) return ZPP_ERR_ARG;
+    if (rows == 0) return ZPP_OK;
+    if (!x || !y || !mean || !rstd) return ZPP_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(y, 16)) return ZPP_ERR_ALIGN;
+    if (!aligned(mean, 4) || !aligned(rstd, 4)) return ZPP_ERR_ALIGN;
+    const Range rx = matrix(x, rows, x_stride, width, x_dtype), rw = matrix(weight, 1, width, width, w_dtype),
+        rb = matrix(bias, 1, width, width, w_dtype), ry = matrix(y, rows, y_stride, width, x_dtype),
+        rm{mean, 4 * rows}, rr{rstd, 4 * rows};
+    for (const Range &o : {ry, rm, rr}) {
+        if (overlap(o, rx) || overlap(o, rw) || overlap(o, rb)) return ZPP_ERR_OVERLAP;
+    }
+    if (overlap(ry, rm) || overlap(ry, rr) || overlap(rm, rr)) return ZPP_ERR_OVERLAP;
+    const Range all[] = {rx, rw, rb, ry, rm, rr};
+    if (zpp_status s = check_all(all); s != ZPP_OK) return s;
+    return launch_checked([&] {
+        return zpp::launch_layer_norm(x, x_dtype == ZPP_FP32, x_stride, rows, width, weight, bias,
+                   w_dtype == ZPP_FP32, eps, y, y_stride, mean, rstd, static_cast<hipStream_t>(stream));
+    });
+}
+
+zpp_status zpp_layer_norm_grad(const void *dy, int64_t dy_stride, const void *x, int32_t x_dtype, int64_t x_stride,
+                               int64_t rows, int64_t width, const void *weight, int32_t w_dtype, const float *mean,
+                               const float *rstd, void *dx, int64_t dx_stride, void *dweight, void *dbias,
+                               void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!is_dtype(x_dtype) || !is_dtype(w_dtype)) return ZPP_ERR_ARG;
+    if (!is_norm_size(rows, width)) return ZPP_ERR_ARG;
+    if (!is_stride(dy_stride, rows, width) || !is_stride(x_stride, rows, width) || !is_stride(dx_stride, rows, width))
+        return ZPP_ERR_ARG;
+    const int64_t need = zpp::layer_norm_grad_workspace(rows, width);
+    if (workspace_bytes < need) return ZPP_ERR_ARG;
+    if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return ZPP_ERR_NULL;
+    if (need > 0 && !workspace) return ZPP_ERR_NULL;
+    if (!aligned(dweight, 16) || !aligned(dbias, 16)) return ZPP_ERR_ALIGN;
+    if (rows > 0) {
+        if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(weight, 16) || !aligned(dx, 16)) return ZPP_ERR_ALIGN;
+        if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 16)) return ZPP_ERR_ALIGN;
+    }
+    const Range rd = matrix(dy, rows, dy_stride, width, x_dtype), rx = matrix(x, rows, x_stride, width, x_dtype),
+        rw = matrix(weight, rows > 0, width, width, w_dtype), rm{mean, 4 * rows}, rr{rstd, 4 * rows},
+        ro = matrix(dx, rows, dx_stride, width, x_dtype), rdw = matrix(dweight, 1, width, width, w_dtype),
+        rdb = matrix(dbias, 1, width, width, w_dtype), rws{workspace, need};
+    const Range outs[] = {ro, rdw, rdb, rws};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range &r : {rd, rx, rw, rm, rr})
+            if (overlap(outs[i], r)) return ZPP_ERR_OVERLAP;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return ZPP_ERR_OVERLAP;
+    }
+    const Range all[] = {rd, rx, rw, rm, rr, ro, rdw, rdb, rws};
+    if (zpp_status s = check_all(all); s != ZPP_OK) return s;
+    if (rows == 0 && !dweight && !dbias) return ZPP_OK;
+    return launch_checked([&] {
+        return zpp::launch_layer_norm_grad(dy, dy_stride, x, x_dtype == ZPP_FP32, x_stride, rows, width, weight,
+                   w_dtype == ZPP_FP32, mean, rstd, dx, dx_stride, dweight, dbias, workspace,
+                   static_cast<hipStream_t>(stream));
+    });
+}
+
+int64_t zpp_layer_norm_grad_workspace(int64_t rows, int64_t width) {
+    return is_norm_size(rows, width) ? zpp::layer_norm_grad_workspace(rows, width) : 0;
 }
 
 int32_t zpp_set_pointer_checks(int32_t enabled) {

@@ -7,6 +7,9 @@
  * gather-side dequantization, and the gradient path of qgZ (tensor-slice
  * reordering, one-shot 4-bit quantization, and the dequantize-reduce-
  * requantize step between the two hops of its hierarchical all-to-all).
+ * Next to it stand the operators that use those weights on the GPU that holds
+ * their codes: linear products and their input gradient straight from codes
+ * and scales, and layer norm, forward and backward.
  * It moves no data between GPUs: the caller's collectives do that.
  *
  * Conventions shared by every entry point
@@ -25,7 +28,8 @@
  *   not survive it; a rejected launch returns ZPP_ERR_LAUNCH and leaves no
  *   error pending. The hop reductions launch once per 2^29 output elements;
  *   if a later launch is rejected, the earlier ones still run, so after
- *   ZPP_ERR_LAUNCH the outputs are unspecified.
+ *   ZPP_ERR_LAUNCH the outputs are unspecified (likewise of a linear call, or
+ *   a norm's backward pass, which may take two launches or more).
  * - The caller allocates and owns every buffer; the library allocates
  *   nothing, keeps no per-call state and may be called from several threads
  *   and streams at once. Outputs must not overlap inputs or each other
@@ -78,6 +82,8 @@ extern "C" {
 #define ZPP_MAX_BLOCK 4096
 #define ZPP_MAX_INPUTS 4096
 #define ZPP_MAX_DIVISOR 16777216 /* 2^24: every divisor up to it is exact in binary32 */
+#define ZPP_MAX_FEATURES 67108864 /* 2^26: the longest row of a weight matrix or of a norm */
+#define ZPP_MAX_ROWS 1073741824  /* 2^30: the most rows of one linear or norm call */
 /* 2^40: the largest element count, input stride (bytes for codes, floats
  * for scales), and reordered buffer (elements, or bytes / 4) accepted; far
  * beyond any GPU's memory, it keeps every byte range of a call exact in
@@ -273,6 +279,113 @@ zpp_status zpp_dequant_reduce_average(const void *codes_in, int64_t codes_stride
                                       const float *scales_in, int64_t scales_stride,
                                       int32_t n_inputs, int32_t bits_in, int64_t numel,
                                       int32_t block, int32_t divisor, float *avg_out, void *stream);
+
+/*
+ * Linear products on block-quantized weights, without rebuilding the weights
+ * in memory: the receiver of the quantized all-gather [QWZ][ZPP2] multiplies
+ * by the codes it holds. The weight matrix is out_features x in_features,
+ * row-major, quantized as one flat buffer of out_features * in_features
+ * elements (as zpp_quantize_blocks writes it; blocks may straddle rows):
+ *
+ *   W[n][k] = code[n*K + k] * scales[(n*K + k) / B],   K = in_features
+ *   zpp_linear_blocks:       y[m][n]  = sum over k of x[m][k]  * W[n][k]
+ *   zpp_linear_blocks_grad:  dx[m][k] = sum over n of dy[m][n] * W[n][k]
+ *
+ * the second being the gradient of the first with respect to x. Any number
+ * of rows, from one token to a long sequence. Sums are binary32. Where input
+ * and output are both ZPP_BF16 and there are more than 64 rows, and in every
+ * bf16 gradient, the weights enter the products as bf16, exactly the values
+ * zpp_dequantize_blocks writes as ZPP_BF16; otherwise nothing is rounded below
+ * binary32 but the result.
+ *
+ *   x / dy          in   rows of in_features (dy: out_features) elements of x_dtype, 16-B aligned
+ *   x_stride        in   elements from one row to the next, >= the row's length; for x a
+ *                        multiple of 16 bytes; <= ZPP_MAX_NUMEL
+ *   rows            in   0..ZPP_MAX_ROWS; 0 is a no-op returning ZPP_OK
+ *   codes, scales   in   as zpp_quantize_blocks writes them for out_features * in_features elements
+ *   bits            in   8 or 4 (any code value is accepted)
+ *   out_features    in   1..ZPP_MAX_FEATURES
+ *   in_features     in   a multiple of 32, 32..ZPP_MAX_FEATURES
+ *   block           in   block size B; divides out_features * in_features
+ *   y / dx          out  rows of out_features (dx: in_features) elements of y_dtype, 16-B aligned;
+ *                        elements between a row's end and the next row are not written
+ *   y_stride        in   as x_stride; for dx a multiple of 16 bytes
+ *   workspace       in   workspace_bytes of memory for this call alone, 16-B aligned; NULL if 0 bytes
+ *                        are needed. Its contents are unspecified before and after.
+ *   workspace_bytes in   at least zpp_linear_blocks_workspace(...) (ZPP_ERR_ARG otherwise)
+ *   stream          in   hipStream_t
+ * A matrix with a row stride counts, for the overlap and range checks, from
+ * its first element to its last. An infinite or NaN element of x or dy makes
+ * results of its own row infinite or NaN (unspecified which), of no other row.
+ */
+zpp_status zpp_linear_blocks(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, const void *codes,
+                             const float *scales, int32_t bits, int64_t out_features, int64_t in_features,
+                             int32_t block, void *y, int32_t y_dtype, int64_t y_stride, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
+zpp_status zpp_linear_blocks_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, int64_t rows,
+                                  const void *codes, const float *scales, int32_t bits, int64_t out_features,
+                                  int64_t in_features, int32_t block, void *dx, int32_t dx_dtype, int64_t dx_stride,
+                                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that zpp_linear_blocks (grad == 0) or zpp_linear_blocks_grad
+ * (grad != 0) needs for these types and sizes: 0 in most cases, and more where
+ * few tiles of results are shared out over the GPU by splitting the sums.
+ * It depends on the arguments alone; 0 for sizes the calls refuse. */
+int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int32_t out_dtype, int64_t rows,
+                                    int64_t out_features, int64_t in_features);
+
+/*
+ * Layer norm over each row of `width` elements, as it stands before the
+ * projections of a layer:
+ *
+ *   mean = sum x / width;  rstd = 1 / sqrt(sum (x - mean)^2 / width + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ *
+ *   x         in   rows x width elements of x_dtype, 16-B aligned
+ *   x_stride  in   elements from one row to the next, width..ZPP_MAX_NUMEL
+ *   rows      in   0..ZPP_MAX_ROWS; 0 is a no-op returning ZPP_OK
+ *   width     in   1..ZPP_MAX_FEATURES
+ *   weight    in   width elements of w_dtype, 16-B aligned, or NULL (ones)
+ *   bias      in   width elements of w_dtype, 16-B aligned, or NULL (zeros)
+ *   eps       in   >= 0, finite
+ *   y         out  rows x width elements of x_dtype, 16-B aligned, y_stride between rows
+ *   mean, rstd  out  rows floats each, 4-B aligned: what the backward pass needs
+ *   stream    in   hipStream_t
+ * Everything between the loads and the stores is binary32.
+ */
+zpp_status zpp_layer_norm(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t width,
+                          const void *weight, const void *bias, int32_t w_dtype, float eps, void *y,
+                          int64_t y_stride, float *mean, float *rstd, void *stream);
+
+/*
+ * The backward pass of zpp_layer_norm: with xh = (x - mean) * rstd and
+ * g = dy * weight,
+ *
+ *   dx = rstd * (g - sum g / width - xh * sum (g * xh) / width)
+ *   dweight = sum over rows of dy * xh;   dbias = sum over rows of dy
+ *
+ * The sums over rows are binary32, in an order fixed by the sizes alone, and
+ * rounded once to w_dtype: the same inputs give the same bits.
+ *
+ *   dy, x       in   rows x width elements of x_dtype each, 16-B aligned, with their row strides
+ *   weight      in   as in zpp_layer_norm (NULL: ones)
+ *   mean, rstd  in   as zpp_layer_norm wrote them
+ *   dx          out  rows x width elements of x_dtype, 16-B aligned, dx_stride between rows
+ *   dweight     out  width elements of w_dtype, 16-B aligned, or NULL
+ *   dbias       out  width elements of w_dtype, 16-B aligned, or NULL
+ *   workspace   in   workspace_bytes of memory for this call alone, 16-B aligned (NULL if 0 bytes are needed)
+ *   workspace_bytes  in  at least zpp_layer_norm_grad_workspace(rows, width) (ZPP_ERR_ARG otherwise)
+ *   stream      in   hipStream_t
+ * With rows == 0, dweight and dbias are set to zero (the empty sum).
+ */
+zpp_status zpp_layer_norm_grad(const void *dy, int64_t dy_stride, const void *x, int32_t x_dtype, int64_t x_stride,
+                               int64_t rows, int64_t width, const void *weight, int32_t w_dtype, const float *mean,
+                               const float *rstd, void *dx, int64_t dx_stride, void *dweight, void *dbias,
+                               void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace zpp_layer_norm_grad needs; 0 for sizes it refuses. */
+int64_t zpp_layer_norm_grad_workspace(int64_t rows, int64_t width);
 
 /*
  * Switch the library's HIP-runtime pointer checks on (enabled != 0, the
