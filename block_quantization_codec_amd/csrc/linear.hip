@@ -7,6 +7,7 @@
 namespace zpp {
 
 hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
+hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
 hipError_t launch_linear_tile_fwd4(const LinArgs &p, int mode, int mt, hipStream_t stream);
 hipError_t launch_linear_tile_fwd8(const LinArgs &p, int mode, int mt, hipStream_t stream);
 hipError_t launch_linear_tile_grad4(const LinArgs &p, int mode, int mt, hipStream_t stream);
@@ -15,13 +16,17 @@ hipError_t launch_linear_tile_grad8(const LinArgs &p, int mode, int mt, hipStrea
 namespace {
 
 constexpr int64_t kCus = 256;       // MI355X
-constexpr int64_t kFewRows = 64;    // forward: at most this many rows stream the codes
+constexpr int64_t kFewRows = 4;     // forward: at most this many rows stream the codes, x in registers,
+constexpr int64_t kMidRows = 64;    // and this many with x in LDS
+constexpr int64_t kMidGroups = 512;  // workgroups the middle kernel's contraction is split for
 constexpr int64_t kMaxTiles = 1 << 23;  // workgroups of one launch
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+enum class Way { few, mid, tile };
+
 struct Plan {
-    bool few;
+    Way way;
     int mt;       // rows of 16 per workgroup
     int splits;   // parts of the contraction
     int64_t split_steps;
@@ -34,12 +39,21 @@ struct Plan {
 // steps or more, and a second kernel sums the parts in order.
 Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
     Plan p{};
-    if (!grad && rows <= kFewRows) {
-        p.few = true;
-        p.splits = 1;
+    if (!grad && rows <= kMidRows) {
         p.rows = rows;
+        if (rows <= kFewRows) {
+            p.way = Way::few;
+            p.splits = 1;
+            return p;
+        }
+        p.way = Way::mid;
+        const int64_t steps = ceil_div(n_in, 128 * kMidChunks), tiles = ceil_div(n_out, 64 * kMidTiles);
+        const int64_t splits = std::max<int64_t>(std::min(kMidGroups / tiles, steps / 4), 1);
+        p.split_steps = ceil_div(steps, splits);
+        p.splits = static_cast<int>(ceil_div(steps, p.split_steps));
         return p;
     }
+    p.way = Way::tile;
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     const int64_t col_tiles = ceil_div(len, 256), steps = ceil_div(c_len, 64);
     const int big = in_f32 || out_f32 ? 8 : 16;
@@ -118,8 +132,11 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
         p.splits = plan.splits;
         p.split_steps = plan.split_steps;
         hipError_t e;
-        if (plan.few) {
+        if (plan.way == Way::few) {
             e = launch_linear_few(p, bits, in_f32, stream);
+        } else if (plan.way == Way::mid) {
+            p.col_tiles = ceil_div(n_out, 64 * kMidTiles);
+            e = launch_linear_mid(p, bits, in_f32, stream);
         } else {
             p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
             p.col_tiles = ceil_div(len, 256);

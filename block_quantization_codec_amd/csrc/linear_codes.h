@@ -1,0 +1,217 @@
+// linear_codes.h - codes read exactly, for the products that multiply by the
+// codes themselves and apply the scales to sums (few rows of activations).
+//
+//   y[m][n] = sum over chunks of k of s[n, chunk] * sum_k x[m][k] code[n][k]
+//
+// Codes are exact in bf16, so the inner sums have no rounding but the binary32
+// accumulation, and the scale multiplies each chunk's sum in binary32.
+//
+// A wave reads NT tiles of 16 output features, U chunks of 128 indices at a
+// time. WIDE: every chunk lies in one block (block >= 128 and in_features a
+// multiple of 128), so a lane takes 16-byte pieces and each feature one scale
+// a chunk. Otherwise blocks may end at any multiple of 32: lanes take 8
+// neighbouring codes of each 32 and there is a scale for each 32.
+#pragma once
+
+#include "linear_device.h"
+
+namespace zpp {
+
+constexpr int kChunk = 128;
+
+// 4-bit codes become bf16 in pairs by bit operations alone: bf16 holds 16 + u
+// exactly for u = 0..15, with u in its upper mantissa bits, so code + 24 is
+// the code's nibble with its top bit flipped, shifted into place under the
+// exponent of 16. The sum starts from -24 times the sum of x, which the matrix
+// instruction makes itself from a constant operand: about one instruction a
+// code in place of two, and all of it exact but the binary32 sums (whose terms
+// are up to 4 times larger for it). A dword's nibbles come out as pairs
+// (p, p + 4), so x is dealt in that order too.
+constexpr uint32_t kBiasPair = 0xC1C0C1C0u;  // -24, -24 in bf16
+
+__device__ __forceinline__ uint32_t code4_pair(uint32_t w, int p) {
+    const uint32_t at = p == 0 ? w << 3 : w >> (4 * p - 3);
+    return ((at & 0x00780078u) ^ 0x00400040u) | 0x41804180u;
+}
+
+// One scale a lane, of row (lane & 15) and of the quarter's chunk, to four
+// scales of the row, the same in all quarters.
+__device__ __forceinline__ void spread(float v, float (&s)[4]) {
+    const auto h = __builtin_amdgcn_permlane16_swap(as_u(v), as_u(v), false, false);  // quarters 0 0 2 2, 1 1 3 3
+    const auto a = __builtin_amdgcn_permlane32_swap(h[0], h[0], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(h[1], h[1], false, false);
+    s[0] = as_f(a[0]), s[1] = as_f(b[0]), s[2] = as_f(a[1]), s[3] = as_f(b[1]);
+}
+
+// 8 activations (as loaded: 16 bytes of bf16, 32 of binary32) as bf16 parts, in
+// the order of the codes' pairs.
+template <int BITS, int PA>
+__device__ __forceinline__ void deal(const u32x4 (&v)[PA == 3 ? 2 : 1], u32x4 (&x)[PA]) {
+    if constexpr (PA == 3) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = BITS == 4 ? j : 2 * j, f = BITS == 4 ? j + 4 : 2 * j + 1;
+            uint32_t w[3];
+            to_parts<3>(as_f(v[e / 4][e % 4]), as_f(v[f / 4][f % 4]), w);
+#pragma unroll
+            for (int a = 0; a < 3; ++a) x[a][j] = w[a];
+        }
+    } else if constexpr (BITS == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[0][j] = __builtin_amdgcn_perm(v[0][2 + j / 2], v[0][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+    } else {
+        x[0] = v[0];
+    }
+}
+
+template <int BITS, int NT, int U, bool WIDE>
+struct CodeStream {
+    static constexpr int kUnit = WIDE ? 7 : 5;    // log2 of the indices of one scale
+    static constexpr int kS = WIDE ? (U + 3) / 4 : U;  // loads of scales, four a load
+    static constexpr int kW = BITS == 4 ? 4 : 8;  // dwords of a chunk's codes
+
+    // What stays the same over the chunks. Bases are the same in every lane of
+    // the wave; lanes add 32-bit offsets.
+    struct At {
+        const uint8_t *codes;
+        const float *scales;
+        uint32_t code[NT], unit[NT];
+        int shift;
+    };
+
+    // For the wave's features n0 .. n0 + 16 NT - 1 (n0 < out_features).
+    static __device__ __forceinline__ At place(const LinArgs &p, int64_t n0) {
+        const int lane = threadIdx.x & (kWave - 1), q = lane >> 4;
+        At a;
+        const int64_t units = p.n_in >> kUnit, first = n0 * units;
+        a.shift = p.log2b - kUnit;
+        a.codes = p.codes + n0 * p.n_in * BITS / 8;
+        a.scales = p.scales + (first >> a.shift);
+        const uint32_t rem = static_cast<uint32_t>(first & ((INT64_C(1) << a.shift) - 1));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t n =
+                static_cast<uint32_t>(min(static_cast<int64_t>(t * 16 + (lane & 15)), p.n_out - 1 - n0));
+            // 16 bytes a quarter in each 64-byte run; 8 codes a quarter of each 32. Up to 32 rows of 2^26 codes.
+            static_assert(NT <= 2, "offsets are 32-bit");
+            a.code[t] = n * static_cast<uint32_t>(p.n_in * BITS / 8) + q * (WIDE ? 16 : BITS);
+            a.unit[t] = rem + n * static_cast<uint32_t>(units);
+        }
+        return a;
+    }
+
+    // Where in a chunk the lane's 8 indices of instruction s begin.
+    static __device__ __forceinline__ uint32_t index(uint32_t q, uint32_t s) {
+        if constexpr (!WIDE) return s * 32 + q * 8;
+        return BITS == 4 ? q * 32 + s * 8 : (s >> 1) * 64 + q * 16 + (s & 1) * 8;
+    }
+
+    // U chunks of one wave, as loaded.
+    struct Chunks {
+        uint32_t w[U][NT][kW];
+        float s[kS][NT];
+    };
+
+    // A chunk, or 32-index step of one, past the end is the last one again;
+    // scales() gives it a scale of zero.
+    static __device__ __forceinline__ void load(const LinArgs &p, const At &a, int64_t k0, Chunks &c) {
+        const uint32_t q = (threadIdx.x & (kWave - 1)) >> 4;
+        const uint32_t n_in = static_cast<uint32_t>(p.n_in), k = static_cast<uint32_t>(k0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (WIDE) {
+                const uint8_t *codes = a.codes + static_cast<int64_t>(min(k + u * kChunk, n_in - kChunk)) * BITS / 8;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int h = 0; h < BITS / 4; ++h) {
+                        const u32x4 v = ld<u32x4>(codes + 64 * h + a.code[t]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c.w[u][t][4 * h + i] = v[i];
+                    }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint8_t *codes =
+                        a.codes + static_cast<int64_t>(min(k + u * kChunk + s * 32, n_in - 32)) * BITS / 8;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if constexpr (BITS == 4) {
+                            c.w[u][t][s] = ld<uint32_t>(codes + a.code[t]);
+                        } else {
+                            const u32x2 v = ld<u32x2>(codes + a.code[t]);
+                            c.w[u][t][2 * s] = v[0], c.w[u][t][2 * s + 1] = v[1];
+                        }
+                    }
+                }
+            }
+        }
+        // each quarter loads another chunk's scales (WIDE), or another 32-index step's
+#pragma unroll
+        for (int i = 0; i < kS; ++i) {
+            const uint32_t unit = min((k >> kUnit) + i * 4 + q, (n_in >> kUnit) - 1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) c.s[i][t] = a.scales[(a.unit[t] + unit) >> a.shift];
+        }
+    }
+
+    // The scales of the chunks' units, in every quarter.
+    static __device__ __forceinline__ void scales(const LinArgs &p, int64_t k0, const Chunks &c,
+                                                  float (&scale)[kS][NT][4]) {
+        const uint32_t left = k0 < p.n_in ? static_cast<uint32_t>(p.n_in - k0) >> kUnit : 0;
+#pragma unroll
+        for (int i = 0; i < kS; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                spread(c.s[i][t], scale[i][t]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) scale[i][t][u] = i * 4 + u < left ? scale[i][t][u] : 0.0f;
+            }
+    }
+
+    // acc += chunk u's products with the activations a[m][s] of its four instructions.
+    template <int PA, int MT>
+    static __device__ __forceinline__ void chunk(const Chunks &c, int u, const u32x4 (&a)[MT][4][PA],
+                                                 const float (&scale)[kS][NT][4], f32x4 (&acc)[NT][MT]) {
+        const f32x4 zero = {0, 0, 0, 0};
+        const u32x4 pair[1] = {u32x4{kBiasPair, kBiasPair, kBiasPair, kBiasPair}};
+        f32x4 bias[MT][WIDE ? 1 : 4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                f32x4 &o = bias[m][WIDE ? 0 : s];
+                if (!WIDE || s == 0) o = zero;
+                if constexpr (BITS == 4) o = mfma_parts<PA, 1>(a[m][s], pair, o);
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            f32x4 sum[MT];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                u32x4 b[1];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (BITS == 4) {
+                        b[0][j] = code4_pair(c.w[u][t][s], j);
+                    } else {
+                        const uint32_t w = c.w[u][t][2 * s + j / 2];
+                        b[0][j] = pack_hi(code_f32<8>(w, 2 * (j % 2)), code_f32<8>(w, 2 * (j % 2) + 1));
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    sum[m] = mfma_parts<PA, 1>(a[m][s], b, WIDE && s > 0 ? sum[m] : bias[m][WIDE ? 0 : s]);
+                    if (!WIDE || s == 3) {
+                        const float f = WIDE ? scale[u / 4][t][u % 4] : scale[u][t][s];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[t][m][i] = __builtin_fmaf(sum[m][i], f, acc[t][m][i]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+}  // namespace zpp

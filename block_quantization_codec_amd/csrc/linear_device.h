@@ -79,6 +79,10 @@ __device__ __forceinline__ f32x4 mfma_parts(const u32x4 (&a)[PA], const u32x4 (&
     return c;
 }
 
+// linear_mid.hip's shape: tiles of 16 features a wave, chunks of 128 indices a step.
+constexpr int kMidTiles = 2;
+constexpr int kMidChunks = 2;
+
 // One product's operands, as the host describes them. a is [rows, C] with C
 // the contraction length (in for the product, out for its gradient); the
 // result is [rows, L].

@@ -1,195 +1,135 @@
-// linear_few.hip - y = x W^T on block codes for few rows of x (decoding): a
-// stream over the codes.
-//
-//   y[m][n] = sum over chunks of k of s[n, chunk] * sum_k x[m][k] code[n][k]
-//
-// The codes are exact in bf16, so the inner sums have no rounding but the
-// binary32 accumulation, and the scale multiplies each chunk's sum in
-// binary32. binary32 activations go through the matrix instructions as three
-// bf16 parts (exactly).
+// linear_few.hip - y = x W^T on block codes for one to four rows of x
+// (decoding): a stream over the codes.
 //
 // Every code is read once from HBM by one wave, 16 bytes a lane, and used for
-// up to 16*MT rows; with one row the matrix instruction still costs less than
-// multiply-adds would: the conversion to bf16 pairs is about 1.6 instructions
-// a code for any number of rows. A wave has NT tiles of 16 output features;
-// the WK waves of a workgroup take chunks of 128 indices in turn and join
+// all rows; even with one row the matrix instruction costs less than
+// multiply-adds would: about one instruction a code makes 4-bit codes bf16
+// pairs, for any number of rows. A wave has NT tiles of 16 output features;
+// the WK waves of a workgroup take U chunks of 128 indices in turn and join
 // their sums in LDS at the end, in wave order.
-//
-// WIDE: every 128-index chunk lies in one block (block >= 128 and in_features
-// a multiple of 128), so a lane takes 32 neighbouring codes and one scale a
-// chunk. Otherwise blocks may end at any multiple of 32: lanes take 8
-// neighbouring codes of each 32 and a scale for each 32.
-#include "linear_device.h"
+#include "linear_codes.h"
 
 namespace zpp {
 namespace {
 
-constexpr int kChunk = 128;
+// A row's lane i takes lane (i + c) mod 16's value.
+template <int C>
+__device__ __forceinline__ uint32_t rotate(uint32_t v) {
+    if constexpr (C % 16 == 0) return v;
+    return dpp_u32<0x120 + (16 - C % 16) % 16>(v);
+}
 
-template <int BITS, int PA, int NT, int MT, bool WIDE>
+template <int C, int PA>
+__device__ __forceinline__ void rotate_parts(const u32x4 (&v)[PA], u32x4 (&o)[PA]) {
+#pragma unroll
+    for (int a = 0; a < PA; ++a)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[a][j] = rotate<C>(v[a][j]);
+}
+
+// RM is the number of rows of x that lie in one operand (a power of two below
+// 16): the lanes of a quarter load 16 / RM operands' pieces at once, and each
+// operand is a rotation of them.
+template <int BITS, int PA, int NT, int RM, int U, bool WIDE>
 struct Few {
-    // One chunk of one wave, as loaded.
-    struct Chunk {
-        uint32_t w[NT][BITS == 4 ? 4 : 8];
-        float s[NT][WIDE ? 1 : 4];
-        u32x4 x[MT][4][PA == 3 ? 2 : 1];
-    };
+    using C = CodeStream<BITS, NT, U, WIDE>;
+    static constexpr int kPer = 16 / RM;                  // operands of one load of x
+    static constexpr int kX = (4 * U + kPer - 1) / kPer;  // loads of x
+    using Raw = u32x4[kX][PA == 3 ? 2 : 1];
 
-    static __device__ __forceinline__ void load(const LinArgs &p, int64_t n0, int64_t kc, Chunk &c) {
-        const int lane = threadIdx.x & (kWave - 1), q = lane >> 4;
+    // Operand i = l * kPer + (lane & 15) / RM is instruction i % 4 of chunk i / 4.
+    static __device__ __forceinline__ void load_x(const LinArgs &p, const uint8_t *row, int64_t k0, Raw &x) {
+        const uint32_t lane = threadIdx.x & (kWave - 1), q = lane >> 4, j = lane & 15;
+        const uint32_t n_in = static_cast<uint32_t>(p.n_in), k = static_cast<uint32_t>(k0);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int64_t n = min(n0 + t * 16 + (lane & 15), p.n_out - 1);
-            const int64_t row = n * p.n_in;
-            if constexpr (WIDE) {
-                const bool ok = kc < p.n_in;
-                const int64_t e = row + (ok ? kc : 0) + q * 32;
+        for (int l = 0; l < kX; ++l) {
+            const uint32_t i = l * kPer + j / RM, u = i / 4, s = i % 4;
+            const uint32_t at = k + u * kChunk + C::index(q, s);
+            // past the end the codes are the last ones again, with scales of zero: any x of the row will do
+            const uint8_t *from = row + min(at, n_in - 8) * (PA == 3 ? 4 : 2);
 #pragma unroll
-                for (int h = 0; h < BITS / 4; ++h) {
-                    const u32x4 v = ld_stream<u32x4>(p.codes + e * BITS / 8 + 16 * h);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) c.w[t][4 * h + i] = v[i];
-                }
-                const float sc = p.scales[e >> p.log2b];
-                c.s[t][0] = ok ? sc : 0.0f;
-            } else {
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int64_t k = kc + s * 32;
-                    const bool ok = k < p.n_in;
-                    const int64_t e = row + (ok ? k : 0) + q * 8;
-                    if constexpr (BITS == 4) {
-                        c.w[t][s] = ld<uint32_t>(p.codes + e / 2);
-                    } else {
-                        const u32x2 v = ld<u32x2>(p.codes + e);
-                        c.w[t][2 * s] = v[0], c.w[t][2 * s + 1] = v[1];
-                    }
-                    const float sc = p.scales[e >> p.log2b];
-                    c.s[t][s] = ok ? sc : 0.0f;
-                }
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int64_t row = min(static_cast<int64_t>(m * 16 + (lane & 15)), p.rows - 1);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int64_t k = kc + (WIDE ? q * 32 + s * 8 : s * 32 + q * 8);
-                const bool ok = k < p.n_in;
-                const uint8_t *at = static_cast<const uint8_t *>(p.a) + (row * p.lda + (ok ? k : 0)) * (PA == 3 ? 4 : 2);
-#pragma unroll
-                for (int h = 0; h < (PA == 3 ? 2 : 1); ++h) {
-                    const u32x4 v = ld<u32x4>(at + 16 * h);
-                    c.x[m][s][h] = ok ? v : u32x4{0, 0, 0, 0};
-                }
-            }
+            for (int h = 0; h < (PA == 3 ? 2 : 1); ++h) x[l][h] = ld<u32x4>(from + 16 * h);
         }
     }
 
-    static __device__ __forceinline__ void use(const Chunk &c, f32x4 (&acc)[NT][MT]) {
-        f32x4 sum[NT][MT];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            u32x4 x[MT][PA];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if constexpr (PA == 1) {
-                    x[m][0] = c.x[m][s][0];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[3];
-                        to_parts<3>(as_f(c.x[m][s][j / 2][2 * (j % 2)]), as_f(c.x[m][s][j / 2][2 * (j % 2) + 1]), w);
-#pragma unroll
-                        for (int a = 0; a < 3; ++a) x[m][a][j] = w[a];
-                    }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                u32x4 b[1];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    constexpr int per = 32 / BITS;
-                    const int i = 8 * s + 2 * j;
-                    b[0][j] = pack_hi(code_f32<BITS>(c.w[t][i / per], i % per),
-                                      code_f32<BITS>(c.w[t][(i + 1) / per], (i + 1) % per));
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const bool first = !WIDE || s == 0;
-                    sum[t][m] = mfma_parts<PA, 1>(x[m], b, first ? f32x4{0, 0, 0, 0} : sum[t][m]);
-                    if (!WIDE || s == 3) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[t][m][i] = __builtin_fmaf(sum[t][m][i], c.s[t][WIDE ? 0 : s], acc[t][m][i]);
-                    }
-                }
-            }
-        }
+    template <int I>
+    static __device__ __forceinline__ void use_from(const u32x4 (&x)[kX][PA], const typename C::Chunks &c,
+                                                    const float (&scale)[C::kS][NT][4], f32x4 (&acc)[NT][1]) {
+        u32x4 a[1][4][PA];
+        rotate_parts<I % kPer * RM, PA>(x[I / kPer], a[0][0]);
+        rotate_parts<(I + 1) % kPer * RM, PA>(x[(I + 1) / kPer], a[0][1]);
+        rotate_parts<(I + 2) % kPer * RM, PA>(x[(I + 2) / kPer], a[0][2]);
+        rotate_parts<(I + 3) % kPer * RM, PA>(x[(I + 3) / kPer], a[0][3]);
+        C::template chunk<PA, 1>(c, I / 4, a, scale, acc);
+        if constexpr (I + 4 < 4 * U) use_from<I + 4>(x, c, scale, acc);
     }
 };
 
-template <int BITS, int PA, int NT, int MT, bool WIDE, int WK, int U>
+template <int BITS, int PA, int NT, int RM, int U, bool WIDE, int WK>
 __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
-    using F = Few<BITS, PA, NT, MT, WIDE>;
-    constexpr int kSums = NT * MT * 256;  // of one wave
-    __shared__ float sums[WK][kSums];
+    using F = Few<BITS, PA, NT, RM, U, WIDE>;
+    using C = typename F::C;
+    __shared__ float sums[WK][NT * 256];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     const int64_t n0 = xcd_block(blockIdx.x, gridDim.x) * (16 * NT);
+    const typename C::At at = C::place(p, n0);
+    const uint8_t *row = static_cast<const uint8_t *>(p.a) +
+                         min(static_cast<int64_t>(lane % RM), p.rows - 1) * p.lda * (PA == 3 ? 4 : 2);
 
-    f32x4 acc[NT][MT];
+    f32x4 acc[NT][1];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < NT; ++t) acc[t][0] = f32x4{0, 0, 0, 0};
 
-    const int64_t chunks = (p.n_in + kChunk - 1) / kChunk;
-    for (int64_t i = w; i < chunks; i += U * WK) {
-        typename F::Chunk c[U];
+    // a wave's U chunks are neighbours: their codes fill whole cache lines
+    for (int64_t k = static_cast<int64_t>(w) * U * kChunk; k < p.n_in; k += U * WK * kChunk) {
+        typename C::Chunks c;
+        typename F::Raw raw;
+        C::load(p, at, k, c);
+        F::load_x(p, row, k, raw);
+        float scale[C::kS][NT][4];
+        C::scales(p, k, c, scale);
+        u32x4 x[F::kX][PA];
 #pragma unroll
-        for (int u = 0; u < U; ++u) F::load(p, n0, (i + u * WK) * kChunk, c[u]);  // past the end: zeros
-#pragma unroll
-        for (int u = 0; u < U; ++u) F::use(c[u], acc);
+        for (int l = 0; l < F::kX; ++l) deal<BITS, PA>(raw[l], x[l]);
+        F::template use_from<0>(x, c, scale, acc);
     }
 
+    // rows 0..3 of a sum are its quarter 0's
+    if (lane < 16) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sums[w][((t * MT + m) * 4 + i) * 64 + lane] = acc[t][m][i];
+            for (int i = 0; i < 4; ++i) sums[w][(t * 4 + i) * 16 + lane] = acc[t][0][i];
+    }
     __syncthreads();
-    for (int o = threadIdx.x; o < kSums; o += WK * kWave) {
-        const int l = o & 63, i = o >> 6 & 3, m = (o >> 8) % MT, t = (o >> 8) / MT;
-        const int64_t row = m * 16 + 4 * (l >> 4) + i, col = n0 + t * 16 + (l & 15);
-        if (row >= p.rows || col >= p.n_out) continue;
+    for (int o = threadIdx.x; o < NT * 64; o += WK * kWave) {
+        const int64_t row_out = o >> 4 & 3, col = n0 + (o >> 6) * 16 + (o & 15);
+        if (row_out >= p.rows || col >= p.n_out) continue;
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < WK; ++k) v += sums[k][o];
-        v *= kCodeScale<BITS>;
         if (p.out_f32)
-            static_cast<float *>(p.out)[row * p.ldo + col] = v;
+            static_cast<float *>(p.out)[row_out * p.ldo + col] = v;
         else
-            static_cast<uint16_t *>(p.out)[row * p.ldo + col] = static_cast<uint16_t>(pack_rn(v, 0.0f));
+            static_cast<uint16_t *>(p.out)[row_out * p.ldo + col] = static_cast<uint16_t>(pack_rn(v, 0.0f));
     }
 }
 
-template <int BITS, int PA, int NT, int MT, int WK, int U>
+template <int BITS, int PA, int NT, int RM, int U, int WK>
 hipError_t launch_as(const LinArgs &p, bool wide, hipStream_t stream) {
     const unsigned grid = static_cast<unsigned>((p.n_out + 16 * NT - 1) / (16 * NT));
     if (wide)
-        linear_few_kernel<BITS, PA, NT, MT, true, WK, U><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, true, WK><<<grid, WK * kWave, 0, stream>>>(p);
     else
-        linear_few_kernel<BITS, PA, NT, MT, false, WK, U><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, false, WK><<<grid, WK * kWave, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <int BITS, int PA>
 hipError_t launch_rows(const LinArgs &p, bool wide, hipStream_t stream) {
-    if (p.rows <= 16) return launch_as<BITS, PA, 2, 1, 8, PA == 1 ? 2 : 1>(p, wide, stream);
-    if (p.rows <= 32) return launch_as<BITS, PA, 2, 2, 8, 1>(p, wide, stream);
-    return launch_as<BITS, PA, 2, 4, 4, 1>(p, wide, stream);
+    if (p.rows == 1) return launch_as<BITS, PA, 1, 1, 4, 8>(p, wide, stream);
+    if (p.rows == 2) return launch_as<BITS, PA, 1, 2, 4, 8>(p, wide, stream);
+    return launch_as<BITS, PA, 1, 4, 4, 8>(p, wide, stream);
 }
 
 }  // namespace
