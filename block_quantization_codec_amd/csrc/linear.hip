@@ -9,9 +9,13 @@ namespace zpp {
 hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
 hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
 hipError_t launch_linear_tile_fwd4(const LinArgs &p, int mode, int mt, hipStream_t stream);
+hipError_t launch_linear_big_fwd4(const LinArgs &p, int mt, hipStream_t stream);
 hipError_t launch_linear_tile_fwd8(const LinArgs &p, int mode, int mt, hipStream_t stream);
+hipError_t launch_linear_big_fwd8(const LinArgs &p, int mt, hipStream_t stream);
 hipError_t launch_linear_tile_grad4(const LinArgs &p, int mode, int mt, hipStream_t stream);
+hipError_t launch_linear_big_grad4(const LinArgs &p, int mt, hipStream_t stream);
 hipError_t launch_linear_tile_grad8(const LinArgs &p, int mode, int mt, hipStream_t stream);
+hipError_t launch_linear_big_grad8(const LinArgs &p, int mt, hipStream_t stream);
 
 namespace {
 
@@ -140,7 +144,13 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
         } else {
             p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
             p.col_tiles = ceil_div(len, 256);
-            if (grad)
+            if (mode == 0 && grad)
+                e = bits == 4 ? launch_linear_big_grad4(p, plan.mt, stream)
+                              : launch_linear_big_grad8(p, plan.mt, stream);
+            else if (mode == 0)
+                e = bits == 4 ? launch_linear_big_fwd4(p, plan.mt, stream)
+                              : launch_linear_big_fwd8(p, plan.mt, stream);
+            else if (grad)
                 e = bits == 4 ? launch_linear_tile_grad4(p, mode, plan.mt, stream)
                               : launch_linear_tile_grad8(p, mode, plan.mt, stream);
             else

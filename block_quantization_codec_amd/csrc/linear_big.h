@@ -1,0 +1,324 @@
+// linear_big.h - the tiled products of linear_tile.h for bf16 to bf16 with
+// activations in whole 16-byte pieces: the same tiles and layouts, pipelined.
+//
+// A step is 64 contraction indices, in two halves of 32 (one matrix
+// instruction deep). With 256 rows a wave has the SIMD to itself (256 sums a
+// lane), so nothing but its own instructions hides a wait, and everything is
+// asked for early:
+//   - activations go straight to LDS, two steps ahead (three buffers);
+//   - codes and scales are loaded a step before they are converted;
+//   - each half converts the next half's B operands between its matrix
+//     instructions, 16 / MT dwords after each row of tiles;
+//   - A operands are read from LDS three rows of tiles ahead, across the ends
+//     of halves and steps: the one barrier of a step stands in its middle,
+//     after which the next step's activations can be read.
+// What is left over of the contraction, less than 64 indices, is one more
+// step, guarded and not pipelined.
+#pragma once
+
+#include "linear_tile.h"
+
+namespace zpp {
+
+template <bool GRAD, int BITS, int MT>
+struct LinBig {
+    using Tile = LinTile<GRAD, BITS, 1, 1, MT, true>;
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kBytes = Tile::kPlane;
+    static constexpr int kGroups = (2 * MT + 3) / 4;  // 8-row groups of activations a wave stages
+    static constexpr int kAhead = MT >= 4 ? 3 : 0;    // rows of tiles that A is read ahead
+    static constexpr int kRing = MT >= 4 ? 4 : 1;
+
+    // Codes of 16 indices of a lane's 4 columns; scales of the 4 columns (y),
+    // or of index (lane & 15) in both 32-column halves (dx).
+    struct Raw {
+        uint32_t w[GRAD ? 16 : (BITS == 4 ? 8 : 16)];
+        float s[GRAD ? 2 : 4];
+    };
+
+    // Bases are the same in every lane of a wave; lanes add 32-bit offsets.
+    // Scales are counted in units of 32 weights, relative to a base.
+    struct At {
+        const uint8_t *a[kGroups];  // the lane's own: activations may have any row stride
+        const uint8_t *codes;
+        uint32_t code[GRAD ? 1 : 4], unit[GRAD ? 1 : 4];
+        int64_t first;  // the base's unit: of the wave's first row (y), of its first column (dx)
+        int64_t units;  // of a row
+        uint32_t half;  // dx: from the first 32 columns' unit to the second's (0 at the end)
+        int shift;
+    };
+
+    static __device__ __forceinline__ At place(const LinArgs &p, int64_t m0, int64_t wave_col) {
+        const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
+        const uint32_t q = lane >> 4, j = lane & 15;
+        At at;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int r = (i * 4 + w) * 8 + (lane >> 3), c = (lane & 7) ^ (r & 7);
+            at.a[i] = static_cast<const uint8_t *>(p.a) + min(m0 + r, p.rows - 1) * p.lda * 2 + c * 16;
+        }
+        at.shift = p.log2b - 5;
+        at.units = p.n_in >> 5;
+        at.half = 0;
+        if constexpr (GRAD) {
+            const int64_t c0 = wave_col < p.n_in ? wave_col : 0;
+            const uint32_t col = static_cast<uint32_t>(min(static_cast<int64_t>(j * 4), p.n_in - 4 - c0));
+            at.codes = p.codes + c0 * BITS / 8;
+            at.code[0] = (q * 16 * static_cast<uint32_t>(p.n_in / 4) + col / 4) * (BITS / 2);
+            at.first = c0 >> 5;
+            at.half = at.first + 1 < at.units ? 1 : 0;
+            at.unit[0] = (q * 16 + j) * static_cast<uint32_t>(at.units);
+        } else {
+            const int64_t n0 = min(wave_col, p.n_out - 1);
+            at.codes = p.codes + n0 * p.n_in * BITS / 8;
+            at.first = n0 * at.units;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t n = static_cast<uint32_t>(min(static_cast<int64_t>(j * 4 + t), p.n_out - 1 - n0));
+                at.code[t] = n * static_cast<uint32_t>(p.n_in * BITS / 8) + q * (2 * BITS);
+                at.unit[t] = n * static_cast<uint32_t>(at.units) + (q >> 1);
+            }
+        }
+        return at;
+    }
+
+    static __device__ __forceinline__ void stage(const At &at, int64_t step, uint8_t *tile) {
+        const int w = wave_in_block();
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int g = i * 4 + w;
+            if (2 * MT % 4 != 0 && g >= 2 * MT) break;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(at.a[i] + step * 128),
+                                             (__attribute__((address_space(3))) void *)(tile + g * 1024), 16, 0, 0);
+        }
+    }
+
+    // A whole step's codes and scales.
+    static __device__ __forceinline__ void load(const LinArgs &p, const At &at, int64_t step, Raw &r) {
+        if constexpr (GRAD) {
+            const uint8_t *codes = at.codes + step * 64 * (p.n_in * BITS / 8);
+            const int64_t row = p.n_in * BITS / 8;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if constexpr (BITS == 4)
+                    r.w[i] = ld<uint16_t>(codes + i * row + at.code[0]);
+                else
+                    r.w[i] = ld<uint32_t>(codes + i * row + at.code[0]);
+            }
+            const int64_t first = step * 64 * at.units + at.first;
+            const float *scales = p.scales + (first >> at.shift);
+            const uint32_t rem = static_cast<uint32_t>(first & ((INT64_C(1) << at.shift) - 1));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) r.s[h] = scales[(at.unit[0] + rem + h * at.half) >> at.shift];
+        } else {
+            const uint8_t *codes = at.codes + step * (8 * BITS);
+            const int64_t first = at.first + step * 2;
+            const float *scales = p.scales + (first >> at.shift);
+            const uint32_t rem = static_cast<uint32_t>(first & ((INT64_C(1) << at.shift) - 1));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if constexpr (BITS == 4) {
+                    const u32x2 v = ld<u32x2>(codes + at.code[t]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) r.w[2 * t + i] = v[i];
+                } else {
+                    const u32x4 v = ld<u32x4>(codes + at.code[t]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r.w[4 * t + i] = v[i];
+                }
+                r.s[t] = scales[(at.unit[t] + rem) >> at.shift];
+            }
+        }
+    }
+
+    // The guarded last step: indices past the end read valid codes (their activations are zeros).
+    static __device__ __forceinline__ void load_last(const LinArgs &p, int64_t wave_col, int64_t c0, Raw &r) {
+        const int lane = threadIdx.x & (kWave - 1);
+        const int64_t q = lane >> 4, j = lane & 15;
+        if constexpr (GRAD) {
+            const int64_t col = wave_col < p.n_in ? wave_col : 0, k = min(col + j * 4, p.n_in - 4);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int64_t e = min(c0 + q * 16 + i, p.n_out - 1) * p.n_in + k;
+                r.w[i] = BITS == 4 ? static_cast<uint32_t>(ld<uint16_t>(p.codes + e / 2)) : ld<uint32_t>(p.codes + e);
+            }
+            const int64_t row = min(c0 + q * 16 + j, p.n_out - 1) * p.n_in;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) r.s[h] = p.scales[(row + min(col + 32 * h, p.n_in - 32)) >> p.log2b];
+        } else {
+            const int64_t k = min(c0 + q * 16, p.n_in - 16);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int64_t e = min(wave_col + j * 4 + t, p.n_out - 1) * p.n_in + k;
+#pragma unroll
+                for (int i = 0; i < BITS / 2; ++i) r.w[BITS / 2 * t + i] = ld<uint32_t>(p.codes + e * BITS / 8 + 4 * i);
+                r.s[t] = p.scales[e >> p.log2b];
+            }
+        }
+    }
+
+    // The scale of index I of the lane's 16, in the lane's own half of the columns.
+    template <int I>
+    static __device__ __forceinline__ float row_scale(const Raw &r) {
+        const float lo = as_f(dpp_u32<0x150 + I>(as_u(r.s[0]))), hi = as_f(dpp_u32<0x150 + I>(as_u(r.s[1])));
+        return (threadIdx.x & 8) ? hi : lo;
+    }
+
+    // Dword X of the 16 that half H's four B operands have: (X / 4, X % 4) is
+    // (dword, tile) in the gradient, so that an index's scale is fetched once,
+    // and (tile, dword) otherwise.
+    template <int H, int X>
+    static __device__ __forceinline__ void convert(const Raw &r, u32x4 (&b)[4]) {
+        constexpr int t = GRAD ? X % 4 : X / 4, d = GRAD ? X / 4 : X % 4, i = 8 * H + 2 * d;
+        if constexpr (GRAD) {
+            b[t][d] = pack_rn(code_f32<BITS>(r.w[i], t) * row_scale<i>(r),
+                              code_f32<BITS>(r.w[i + 1], t) * row_scale<i + 1>(r));
+        } else {
+            constexpr int per = 32 / BITS, at = t * (16 / per);
+            b[t][d] = pack_rn(code_f32<BITS>(r.w[at + i / per], i % per) * r.s[t],
+                              code_f32<BITS>(r.w[at + (i + 1) / per], (i + 1) % per) * r.s[t]);
+        }
+    }
+
+    template <int H, int X, int END>
+    static __device__ __forceinline__ void convert_range(const Raw &r, u32x4 (&b)[4]) {
+        if constexpr (X < END) {
+            convert<H, X>(r, b);
+            convert_range<H, X + 1, END>(r, b);
+        }
+    }
+
+    static __device__ __forceinline__ u32x4 read_a(const uint8_t *at, int m) {
+        return *reinterpret_cast<const u32x4 *>(at + m * 2048);
+    }
+
+    // Rows of tiles M.. of a half: products with b, and the next half's operands
+    // bn from raw. `here` and `then` are where the lane's A operands of this half
+    // and of the next one lie.
+    template <int HN, int M>
+    static __device__ __forceinline__ void rows_from(const uint8_t *here, const uint8_t *then, const u32x4 (&b)[4],
+                                                     const Raw &raw, u32x4 (&bn)[4], u32x4 (&a)[kRing],
+                                                     f32x4 (&acc)[MT][4]) {
+        if constexpr (kAhead == 0)
+            a[0] = read_a(here, M);
+        else if constexpr (M + kAhead < MT)
+            a[(M + kAhead) % kRing] = read_a(here, M + kAhead);
+        else
+            a[(M + kAhead) % kRing] = read_a(then, M + kAhead - MT);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[M][t] = mfma16(a[M % kRing], b[t], acc[M][t]);
+        convert_range<HN, 16 * M / MT, 16 * (M + 1) / MT>(raw, bn);
+        if constexpr (M + 1 < MT) rows_from<HN, M + 1>(here, then, b, raw, bn, a, acc);
+    }
+};
+
+template <bool GRAD, int BITS, int MT>
+__global__ __launch_bounds__(kBlockThreads, MT == 16 ? 1 : 2) void linear_big_kernel(LinArgs p) {
+    using L = LinBig<GRAD, BITS, MT>;
+    __shared__ __attribute__((aligned(128))) uint8_t tiles[3][L::kBytes];
+
+    const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
+    const int q = lane >> 4;
+    const int64_t c_len = GRAD ? p.n_out : p.n_in, len = GRAD ? p.n_in : p.n_out;
+    const LinPlace at_tile = lin_place(p, L::kRows);
+    const int64_t m0 = at_tile.m0, wave_col = at_tile.col0 + w * 64, col = wave_col + (lane & 15) * 4;
+    const typename L::At at = L::place(p, m0, wave_col);
+
+    const int64_t full = c_len / kStep;  // whole steps; what is left over is the last split's
+    const int64_t s0 = at_tile.split * p.split_steps, s1 = min(full, s0 + p.split_steps);
+    const bool rest = c_len % kStep != 0 && at_tile.split == p.splits - 1;
+
+    f32x4 acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
+
+    const int a0 = lds_piece(lane & 15, q * 2), a1 = lds_piece(lane & 15, q * 2 + 1);  // of halves 0 and 1
+    u32x4 a[L::kRing], b0[4], b1[4];
+
+    if (s0 < s1) {
+        typename L::Raw r0, r1;
+        // steps past the end are the last one again: their data are not used
+        auto clamp = [&](int64_t i) { return min(i, s1 - 1); };
+        L::stage(at, s0, tiles[0]);
+        L::stage(at, clamp(s0 + 1), tiles[1]);
+        L::load(p, at, s0, r0);
+        L::load(p, at, clamp(s0 + 1), r1);
+        L::template convert_range<0, 0, 16>(r0, b0);
+        wait_loads();
+        __syncthreads();
+        const uint8_t *t0 = tiles[0], *t1 = tiles[1], *t2 = tiles[2];  // this step's, the next one's, the one after
+        if constexpr (L::kAhead > 0) {
+#pragma unroll
+            for (int m = 0; m < L::kAhead; ++m) a[m] = L::read_a(t0 + a0, m);
+        }
+        auto step = [&](int64_t i, typename L::Raw &now, const typename L::Raw &next) {
+            L::template rows_from<1, 0>(t0 + a0, t0 + a1, b0, now, b1, a, acc);
+            // Every wave's share of the next step's activations has landed once all
+            // are past the barrier, and no wave reads the step before this one any more.
+            wait_loads();
+            __syncthreads();
+            L::stage(at, clamp(i + 2), const_cast<uint8_t *>(t2));
+            L::load(p, at, clamp(i + 2), now);
+            L::template rows_from<0, 0>(t0 + a1, t1 + a0, b1, next, b0, a, acc);
+            const uint8_t *t = t0;
+            t0 = t1, t1 = t2, t2 = t;
+        };
+        for (int64_t i = s0; i < s1; i += 2) {
+            step(i, r0, r1);
+            if (i + 1 < s1)
+                step(i + 1, r1, r0);
+            else
+                wait_loads();  // so that no way into the loop has codes pending, and its start waits for none
+        }
+        wait_loads();
+    }
+
+    if (rest) {
+        typename L::Raw r;
+        __syncthreads();
+        L::Tile::stage_async(p, m0, full * kStep, c_len, tiles[0]);
+        L::load_last(p, wave_col, full * kStep, r);
+        L::template convert_range<0, 0, 16>(r, b0);
+        L::template convert_range<1, 0, 16>(r, b1);
+        wait_loads();
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const u32x4 x = L::read_a(tiles[0] + a0, m), y = L::read_a(tiles[0] + a1, m);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[m][t] = mfma16(y, b1[t], mfma16(x, b0[t], acc[m][t]));
+        }
+    }
+
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = m0 + m * 16 + 4 * q + i;
+            if (row >= p.rows) continue;
+            float v[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v[t] = acc[m][t][i] * kCodeScale<BITS>;
+            L::Tile::store4(p, len, row, col, v, at_tile.split);
+        }
+    }
+}
+
+template <bool GRAD, int BITS, int MT>
+hipError_t launch_linear_big_one(const LinArgs &p, hipStream_t stream) {
+    const int64_t grid = p.row_tiles * p.col_tiles * p.splits;
+    linear_big_kernel<GRAD, BITS, MT><<<static_cast<unsigned>(grid), kBlockThreads, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <bool GRAD, int BITS>
+hipError_t launch_linear_big_as(const LinArgs &p, int mt, hipStream_t stream) {
+    if (mt == 16) return launch_linear_big_one<GRAD, BITS, 16>(p, stream);
+    if (mt == 8) return launch_linear_big_one<GRAD, BITS, 8>(p, stream);
+    if (mt == 4) return launch_linear_big_one<GRAD, BITS, 4>(p, stream);
+    return launch_linear_big_one<GRAD, BITS, 1>(p, stream);
+}
+
+}  // namespace zpp

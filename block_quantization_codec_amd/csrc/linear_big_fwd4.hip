@@ -1,0 +1,10 @@
+// The pipelined tiled products on 4-bit codes: y = x W^T.
+#include "linear_big.h"
+
+namespace zpp {
+
+hipError_t launch_linear_big_fwd4(const LinArgs &p, int mt, hipStream_t stream) {
+    return launch_linear_big_as<false, 4>(p, mt, stream);
+}
+
+}  // namespace zpp

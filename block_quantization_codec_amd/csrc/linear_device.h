@@ -83,6 +83,14 @@ __device__ __forceinline__ f32x4 mfma_parts(const u32x4 (&a)[PA], const u32x4 (&
 constexpr int kMidTiles = 2;
 constexpr int kMidChunks = 2;
 
+// Waits for all of this wave's loads, those into LDS among them, in a form the
+// compiler counts too (it then waits for none of them again).
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), nothing else
+    asm volatile("" ::: "memory");
+}
+
 // One product's operands, as the host describes them. a is [rows, C] with C
 // the contraction length (in for the product, out for its gradient); the
 // result is [rows, L].

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
     land(0);
     int cur = 0;
     for (int64_t k = k0; k < k1; k += kAll, cur ^= 1) {
-        if constexpr (ASYNC) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if constexpr (ASYNC) wait_loads();
         __syncthreads();
         typename C::Chunks next;
         const bool more = k + kAll < k1;

@@ -43,6 +43,23 @@ __device__ __attribute__((aligned(16))) const uint32_t g_lin_zeros[4] = {0, 0, 0
 // Byte offset of 16-byte piece c of row r in a tile of 128-byte rows.
 __device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
+// The tile a workgroup computes. An XCD takes a contiguous run of tiles; 8
+// rows of tiles run down before the next column, so that the 32 tiles an XCD
+// works on at once share both activations and codes in its L2.
+struct LinPlace {
+    int64_t split, m0, col0;
+};
+
+__device__ __forceinline__ LinPlace lin_place(const LinArgs &p, int rows) {
+    const int64_t id = xcd_block(blockIdx.x, gridDim.x);
+    const int64_t tiles_all = p.row_tiles * p.col_tiles;
+    const int64_t split = id / tiles_all, tid = id % tiles_all;
+    const int64_t g = tid / (8 * p.col_tiles);
+    const int64_t in_g = min(INT64_C(8), p.row_tiles - g * 8);
+    const int64_t at = tid - g * 8 * p.col_tiles;
+    return LinPlace{split, (g * 8 + at % in_g) * rows, (at / in_g) * kTileCols};
+}
+
 template <bool GRAD, int BITS, int PA, int PB, int MT, bool ASYNC>
 struct LinTile {
     static constexpr int kRows = 16 * MT;
@@ -230,17 +247,9 @@ __global__ __launch_bounds__(kBlockThreads, 1) void linear_tile_kernel(LinArgs p
     const int q = lane >> 4;
     const int64_t c_len = GRAD ? p.n_out : p.n_in, len = GRAD ? p.n_in : p.n_out;
 
-    // An XCD takes a contiguous run of tiles; 8 rows of tiles run down before
-    // the next column, so that the 32 tiles an XCD works on at once share
-    // both activations and codes in its L2.
-    const int64_t id = xcd_block(blockIdx.x, gridDim.x);
-    const int64_t tiles_all = p.row_tiles * p.col_tiles;
-    const int64_t split = id / tiles_all, tid = id % tiles_all;
-    const int64_t g = tid / (8 * p.col_tiles);
-    const int64_t in_g = min(INT64_C(8), p.row_tiles - g * 8);
-    const int64_t at = tid - g * 8 * p.col_tiles;
-    const int64_t m0 = (g * 8 + at % in_g) * T::kRows;
-    const int64_t col = (at / in_g) * kTileCols + w * 64 + (lane & 15) * 4;
+    const LinPlace place = lin_place(p, T::kRows);
+    const int64_t split = place.split, m0 = place.m0;
+    const int64_t col = place.col0 + w * 64 + (lane & 15) * 4;
 
     const int64_t steps = (c_len + kStep - 1) / kStep;
     const int64_t s0 = split * p.split_steps, s1 = min(steps, s0 + p.split_steps);
@@ -272,7 +281,7 @@ __global__ __launch_bounds__(kBlockThreads, 1) void linear_tile_kernel(LinArgs p
 #pragma unroll
             for (int d = 0; d < 4; ++d) T::convert(raw, s, t, d, b[s][t]);
     T::load_raw(p, col, q, (s0 + 1) * kStep, raw);  // past the end: zeros
-    if constexpr (ASYNC) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if constexpr (ASYNC) wait_loads();
     __syncthreads();
 
     for (int64_t i = s0; i < s1; ++i) {
@@ -315,7 +324,7 @@ __global__ __launch_bounds__(kBlockThreads, 1) void linear_tile_kernel(LinArgs p
 #pragma unroll
                 for (int x = 0; x < PB; ++x) b[s][t][x] = bn[s][t][x];
         // this wave's loads into LDS have landed; after the barrier every wave's have
-        if constexpr (ASYNC) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if constexpr (ASYNC) wait_loads();
         __syncthreads();
     }
 
@@ -340,32 +349,28 @@ hipError_t launch_linear_tile_one(const LinArgs &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The kernels of one direction and code width: mode 0 is bf16 to bf16 with
-// activations that allow 16-byte pieces, 1 the same with any others, 2 bf16
-// to binary32, 3 binary32 activations. mt is the plan's.
+// The kernels of one direction and code width: mode 1 is bf16 to bf16 with
+// activations that are not whole 16-byte pieces (only the gradient's can be),
+// 2 bf16 to binary32, 3 binary32 activations. mt is the plan's.
 template <bool GRAD, int BITS>
 hipError_t launch_linear_tile_as(const LinArgs &p, int mode, int mt, hipStream_t stream) {
-    switch (mode) {
-    case 0:
-        if (mt == 16) return launch_linear_tile_one<GRAD, BITS, 1, 1, 16, true>(p, stream);
-        if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 1, 4, true>(p, stream);
-        return launch_linear_tile_one<GRAD, BITS, 1, 1, 1, true>(p, stream);
-    case 1:
-        if constexpr (GRAD) {  // in_features and its stride are whole pieces: only the gradient needs it
-            if (mt == 16) return launch_linear_tile_one<GRAD, BITS, 1, 1, 16, false>(p, stream);
-            if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 1, 4, false>(p, stream);
-            return launch_linear_tile_one<GRAD, BITS, 1, 1, 1, false>(p, stream);
-        }
-        return hipErrorInvalidValue;
-    case 2:
-        if (mt == 8) return launch_linear_tile_one<GRAD, BITS, 1, 3, 8, false>(p, stream);
-        if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 3, 4, false>(p, stream);
-        return launch_linear_tile_one<GRAD, BITS, 1, 3, 1, false>(p, stream);
-    default:
+    if (mode == 3) {
         if (mt == 8) return launch_linear_tile_one<GRAD, BITS, 3, 3, 8, false>(p, stream);
         if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 3, 3, 4, false>(p, stream);
         return launch_linear_tile_one<GRAD, BITS, 3, 3, 1, false>(p, stream);
     }
+    if (mode == 2) {
+        if (mt == 8) return launch_linear_tile_one<GRAD, BITS, 1, 3, 8, false>(p, stream);
+        if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 3, 4, false>(p, stream);
+        return launch_linear_tile_one<GRAD, BITS, 1, 3, 1, false>(p, stream);
+    }
+    if constexpr (GRAD) {
+        if (mt == 16) return launch_linear_tile_one<GRAD, BITS, 1, 1, 16, false>(p, stream);
+        if (mt == 8) return launch_linear_tile_one<GRAD, BITS, 1, 1, 8, false>(p, stream);
+        if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 1, 4, false>(p, stream);
+        return launch_linear_tile_one<GRAD, BITS, 1, 1, 1, false>(p, stream);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace zpp
