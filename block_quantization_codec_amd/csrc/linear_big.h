@@ -12,22 +12,65 @@
 //   - A operands are read from LDS three rows of tiles ahead, across the ends
 //     of halves and steps: the one barrier of a step stands in its middle,
 //     after which the next step's activations can be read.
-// What is left over of the contraction, less than 64 indices, is one more
-// step, guarded and not pipelined.
+// The pipeline takes pairs of steps; what is left over of the contraction, less
+// than 128 indices, follows in guarded steps that are not pipelined.
 #pragma once
+
+#include <type_traits>
 
 #include "linear_tile.h"
 
 namespace zpp {
 
+// acc += A B. PIN keeps the sums in accumulation registers: 256 of them leave
+// the compiler's allocator none to move one through, and it then moves them
+// through the others and memory. The instruction is written out for that, so
+// the compiler does not know that operands written by ordinary instructions
+// have to be two wait states old: operands_ready() stands before every run of
+// these, and within a run nothing but LDS reads (which are waited for) writes
+// an operand.
+template <bool PIN>
+__device__ __forceinline__ void mfma(u32x4 a, u32x4 b, f32x4 &acc) {
+    if constexpr (PIN)
+        asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    else
+        acc = mfma16(a, b, acc);
+}
+
+template <bool PIN>
+__device__ __forceinline__ void operands_ready() {
+    if constexpr (PIN) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 1");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// After the last mfma<true>: the wait states before ordinary instructions may
+// read the sums.
+template <bool PIN>
+__device__ __forceinline__ void settle(f32x4 &acc) {
+    if constexpr (PIN) asm volatile("s_nop 15\n\ts_nop 3" : "+a"(acc));
+}
+
+// A barrier that waits for no memory operation of the wave's own: neither the
+// loads nor the LDS reads under way have to be over for what it keeps apart.
+__device__ __forceinline__ void barrier_only() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <bool GRAD, int BITS, int MT>
 struct LinBig {
+    static constexpr bool kPin = MT == 16;
     using Tile = LinTile<GRAD, BITS, 1, 1, MT, true>;
     static constexpr int kRows = 16 * MT;
     static constexpr int kBytes = Tile::kPlane;
     static constexpr int kGroups = (2 * MT + 3) / 4;  // 8-row groups of activations a wave stages
-    static constexpr int kAhead = MT >= 4 ? 3 : 0;    // rows of tiles that A is read ahead
-    static constexpr int kRing = MT >= 4 ? 4 : 1;
+    static constexpr int kAhead = MT >= 16 ? 7 : MT >= 4 ? 3 : 0;  // rows of tiles that A is read ahead
+    static constexpr int kRing = MT >= 16 ? 8 : MT >= 4 ? 4 : 1;
+    static constexpr int kBufs = MT >= 8 ? 4 : 3;
 
     // Codes of 16 indices of a lane's 4 columns; scales of the 4 columns (y),
     // or of index (lane & 15) in both 32-column halves (dx).
@@ -82,10 +125,12 @@ struct LinBig {
         return at;
     }
 
+    // Groups I .. END - 1 of a whole step's activations.
+    template <int I, int END>
     static __device__ __forceinline__ void stage(const At &at, int64_t step, uint8_t *tile) {
         const int w = wave_in_block();
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
+        for (int i = I; i < END; ++i) {
             const int g = i * 4 + w;
             if (2 * MT % 4 != 0 && g >= 2 * MT) break;
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(at.a[i] + step * 128),
@@ -93,45 +138,67 @@ struct LinBig {
         }
     }
 
-    // A whole step's codes and scales.
-    static __device__ __forceinline__ void load(const LinArgs &p, const At &at, int64_t step, Raw &r) {
-        if constexpr (GRAD) {
-            const uint8_t *codes = at.codes + step * 64 * (p.n_in * BITS / 8);
-            const int64_t row = p.n_in * BITS / 8;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if constexpr (BITS == 4)
-                    r.w[i] = ld<uint16_t>(codes + i * row + at.code[0]);
-                else
-                    r.w[i] = ld<uint32_t>(codes + i * row + at.code[0]);
-            }
-            const int64_t first = step * 64 * at.units + at.first;
-            const float *scales = p.scales + (first >> at.shift);
-            const uint32_t rem = static_cast<uint32_t>(first & ((INT64_C(1) << at.shift) - 1));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) r.s[h] = scales[(at.unit[0] + rem + h * at.half) >> at.shift];
+    // Where a whole step's codes and scales begin.
+    struct From {
+        const uint8_t *codes;
+        const float *scales;
+        uint32_t rem;
+    };
+    static __device__ __forceinline__ From from(const LinArgs &p, const At &at, int64_t step) {
+        const int64_t first = at.first + (GRAD ? step * 64 * at.units : step * 2);
+        return From{at.codes + (GRAD ? step * 64 * (p.n_in * BITS / 8) : step * (8 * BITS)),
+                    p.scales + (first >> at.shift),
+                    static_cast<uint32_t>(first & ((INT64_C(1) << at.shift) - 1))};
+    }
+
+    // The loads of a step's codes and scales, in the order in which the
+    // conversion is done with the registers they go to.
+    static constexpr int kLoads = GRAD ? 18 : 8;
+    template <int I>
+    static __device__ __forceinline__ void load_one(const LinArgs &p, const At &at, const From &f, Raw &r) {
+        if constexpr (GRAD && I < 16) {
+            const uint8_t *codes = f.codes + I * (p.n_in * BITS / 8);
+            if constexpr (BITS == 4)
+                r.w[I] = ld<uint16_t>(codes + at.code[0]);
+            else
+                r.w[I] = ld<uint32_t>(codes + at.code[0]);
+        } else if constexpr (GRAD) {
+            r.s[I - 16] = f.scales[(at.unit[0] + f.rem + (I - 16) * at.half) >> at.shift];
         } else {
-            const uint8_t *codes = at.codes + step * (8 * BITS);
-            const int64_t first = at.first + step * 2;
-            const float *scales = p.scales + (first >> at.shift);
-            const uint32_t rem = static_cast<uint32_t>(first & ((INT64_C(1) << at.shift) - 1));
+            constexpr int t = I / 2;
+            if constexpr (I % 2 == 1) {
+                r.s[t] = f.scales[(at.unit[t] + f.rem) >> at.shift];
+            } else if constexpr (BITS == 4) {
+                const u32x2 v = ld<u32x2>(f.codes + at.code[t]);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if constexpr (BITS == 4) {
-                    const u32x2 v = ld<u32x2>(codes + at.code[t]);
+                for (int i = 0; i < 2; ++i) r.w[2 * t + i] = v[i];
+            } else {
+                const u32x4 v = ld<u32x4>(f.codes + at.code[t]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) r.w[2 * t + i] = v[i];
-                } else {
-                    const u32x4 v = ld<u32x4>(codes + at.code[t]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r.w[4 * t + i] = v[i];
-                }
-                r.s[t] = scales[(at.unit[t] + rem) >> at.shift];
+                for (int i = 0; i < 4; ++i) r.w[4 * t + i] = v[i];
             }
         }
     }
+    template <int I, int END>
+    static __device__ __forceinline__ void load_range(const LinArgs &p, const At &at, const From &f, Raw &r) {
+        if constexpr (I < END) {
+            load_one<I>(p, at, f, r);
+            load_range<I + 1, END>(p, at, f, r);
+        }
+    }
 
-    // The guarded last step: indices past the end read valid codes (their activations are zeros).
+    // The first half of a step converts the second half of its codes; after a
+    // register's last use there the step after next is loaded into it. How many
+    // of the loads may stand before row of tiles m, and not all at its start:
+    // four waves' loads at once hold up all of them.
+    static constexpr int loads_before(int m) {
+        const int done = 16 * m / MT / 4;  // fours of dwords converted
+        if (m < 0) return 0;
+        const int free = GRAD ? 8 + 2 * done : 2 * done, share = kLoads * (m + 1) / MT;
+        return m >= MT ? kLoads : free < share ? free : share;
+    }
+
+    // A guarded step: indices past the end read valid codes (their activations are zeros).
     static __device__ __forceinline__ void load_last(const LinArgs &p, int64_t wave_col, int64_t c0, Raw &r) {
         const int lane = threadIdx.x & (kWave - 1);
         const int64_t q = lane >> 4, j = lane & 15;
@@ -164,58 +231,110 @@ struct LinBig {
         return (threadIdx.x & 8) ? hi : lo;
     }
 
-    // Dword X of the 16 that half H's four B operands have: (X / 4, X % 4) is
-    // (dword, tile) in the gradient, so that an index's scale is fetched once,
-    // and (tile, dword) otherwise.
+    // Dword X of the 16 that half H's four B operands have, in three pieces that
+    // go between matrix instructions: codes to binary32, times the scale, packed.
+    // (X / 4, X % 4) is (dword, tile) in the gradient, so that an index's scale
+    // is fetched once for four dwords, and (tile, dword) otherwise.
+    struct Part {
+        float f[2];
+    };
     template <int H, int X>
-    static __device__ __forceinline__ void convert(const Raw &r, u32x4 (&b)[4]) {
+    static __device__ __forceinline__ void widen(const Raw &r, Part &f, float (&scale)[2]) {
         constexpr int t = GRAD ? X % 4 : X / 4, d = GRAD ? X / 4 : X % 4, i = 8 * H + 2 * d;
         if constexpr (GRAD) {
-            b[t][d] = pack_rn(code_f32<BITS>(r.w[i], t) * row_scale<i>(r),
-                              code_f32<BITS>(r.w[i + 1], t) * row_scale<i + 1>(r));
+            f.f[0] = code_f32<BITS>(r.w[i], t);
+            f.f[1] = code_f32<BITS>(r.w[i + 1], t);
+            if constexpr (t == 0) scale[0] = row_scale<i>(r), scale[1] = row_scale<i + 1>(r);
         } else {
             constexpr int per = 32 / BITS, at = t * (16 / per);
-            b[t][d] = pack_rn(code_f32<BITS>(r.w[at + i / per], i % per) * r.s[t],
-                              code_f32<BITS>(r.w[at + (i + 1) / per], (i + 1) % per) * r.s[t]);
+            f.f[0] = code_f32<BITS>(r.w[at + i / per], i % per);
+            f.f[1] = code_f32<BITS>(r.w[at + (i + 1) / per], (i + 1) % per);
+            scale[0] = scale[1] = r.s[t];
         }
+    }
+    template <int X>
+    static __device__ __forceinline__ void pack(const Part &f, u32x4 (&b)[4]) {
+        constexpr int t = GRAD ? X % 4 : X / 4, d = GRAD ? X / 4 : X % 4;
+        b[t][d] = pack_rn(f.f[0], f.f[1]);
     }
 
     template <int H, int X, int END>
-    static __device__ __forceinline__ void convert_range(const Raw &r, u32x4 (&b)[4]) {
+    static __device__ __forceinline__ void convert_range(const Raw &r, u32x4 (&b)[4], float (&scale)[2]) {
         if constexpr (X < END) {
-            convert<H, X>(r, b);
-            convert_range<H, X + 1, END>(r, b);
+            Part f;
+            widen<H, X>(r, f, scale);
+            f.f[0] *= scale[0], f.f[1] *= scale[1];
+            pack<X>(f, b);
+            convert_range<H, X + 1, END>(r, b, scale);
         }
+    }
+    template <int H>
+    static __device__ __forceinline__ void convert_all(const Raw &r, u32x4 (&b)[4]) {
+        float scale[2];
+        convert_range<H, 0, 16>(r, b, scale);
     }
 
     static __device__ __forceinline__ u32x4 read_a(const uint8_t *at, int m) {
         return *reinterpret_cast<const u32x4 *>(at + m * 2048);
     }
 
+    // Piece P of row M's share of the conversion.
+    template <int HN, int P, int X, int END>
+    static __device__ __forceinline__ void piece(const Raw &raw, u32x4 (&bn)[4], Part (&f)[16 / MT],
+                                                 float (&scale)[16 / MT][2]) {
+        if constexpr (X < END) {
+            constexpr int i = X % (16 / MT);
+            if constexpr (P == 0) {
+                if constexpr (GRAD && X % 4 != 0 && i != 0) scale[i][0] = scale[i - 1][0], scale[i][1] = scale[i - 1][1];
+                widen<HN, X>(raw, f[i], scale[i]);
+            } else if constexpr (P == 1) {
+                f[i].f[0] *= scale[i][0], f[i].f[1] *= scale[i][1];
+            } else {
+                pack<X>(f[i], bn);
+            }
+            piece<HN, P, X + 1, END>(raw, bn, f, scale);
+        }
+    }
+
     // Rows of tiles M.. of a half: products with b, and the next half's operands
     // bn from raw. `here` and `then` are where the lane's A operands of this half
-    // and of the next one lie.
-    template <int HN, int M>
+    // and of the next one lie. The order is fixed as written: a matrix
+    // instruction keeps its unit for 16 cycles and the issue for 4, so each is
+    // followed by about two instructions of the conversion.
+    // `before(m)` makes the loads that stand before row m.
+    template <int HN, int M, class F>
     static __device__ __forceinline__ void rows_from(const uint8_t *here, const uint8_t *then, const u32x4 (&b)[4],
                                                      const Raw &raw, u32x4 (&bn)[4], u32x4 (&a)[kRing],
-                                                     f32x4 (&acc)[MT][4]) {
+                                                     float (&scale)[16 / MT][2], f32x4 (&acc)[MT][4], F &&before) {
+        constexpr int x0 = 16 * M / MT, x1 = 16 * (M + 1) / MT;
+        Part f[16 / MT];
+        if constexpr (M == 0) operands_ready<kPin>();
         if constexpr (kAhead == 0)
             a[0] = read_a(here, M);
         else if constexpr (M + kAhead < MT)
             a[(M + kAhead) % kRing] = read_a(here, M + kAhead);
         else
             a[(M + kAhead) % kRing] = read_a(then, M + kAhead - MT);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[M][t] = mfma16(a[M % kRing], b[t], acc[M][t]);
-        convert_range<HN, 16 * M / MT, 16 * (M + 1) / MT>(raw, bn);
-        if constexpr (M + 1 < MT) rows_from<HN, M + 1>(here, then, b, raw, bn, a, acc);
+        before(std::integral_constant<int, M>{});
+        mfma<kPin>(a[M % kRing], b[0], acc[M][0]);
+        piece<HN, 0, x0, x1>(raw, bn, f, scale);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma<kPin>(a[M % kRing], b[1], acc[M][1]);
+        piece<HN, 1, x0, x1>(raw, bn, f, scale);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma<kPin>(a[M % kRing], b[2], acc[M][2]);
+        piece<HN, 2, x0, x1>(raw, bn, f, scale);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma<kPin>(a[M % kRing], b[3], acc[M][3]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (M + 1 < MT) rows_from<HN, M + 1>(here, then, b, raw, bn, a, scale, acc, before);
     }
 };
 
 template <bool GRAD, int BITS, int MT>
 __global__ __launch_bounds__(kBlockThreads, MT == 16 ? 1 : 2) void linear_big_kernel(LinArgs p) {
     using L = LinBig<GRAD, BITS, MT>;
-    __shared__ __attribute__((aligned(128))) uint8_t tiles[3][L::kBytes];
+    __shared__ __attribute__((aligned(128))) uint8_t tiles[L::kBufs][L::kBytes];
 
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     const int q = lane >> 4;
@@ -224,9 +343,10 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 ? 1 : 2) void linear_big_ke
     const int64_t m0 = at_tile.m0, wave_col = at_tile.col0 + w * 64, col = wave_col + (lane & 15) * 4;
     const typename L::At at = L::place(p, m0, wave_col);
 
-    const int64_t full = c_len / kStep;  // whole steps; what is left over is the last split's
-    const int64_t s0 = at_tile.split * p.split_steps, s1 = min(full, s0 + p.split_steps);
-    const bool rest = c_len % kStep != 0 && at_tile.split == p.splits - 1;
+    // The split's indices: an even number of whole steps in the pipeline, then the rest.
+    const int64_t s0 = at_tile.split * p.split_steps;
+    const int64_t c1 = min(c_len, (s0 + p.split_steps) * kStep);
+    const int64_t s1 = s0 + ((c1 / kStep - s0) & ~INT64_C(1));
 
     f32x4 acc[MT][4];
 #pragma unroll
@@ -239,61 +359,83 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 ? 1 : 2) void linear_big_ke
 
     if (s0 < s1) {
         typename L::Raw r0, r1;
+        float scale[16 / MT][2];
         // steps past the end are the last one again: their data are not used
         auto clamp = [&](int64_t i) { return min(i, s1 - 1); };
-        L::stage(at, s0, tiles[0]);
-        L::stage(at, clamp(s0 + 1), tiles[1]);
-        L::load(p, at, s0, r0);
-        L::load(p, at, clamp(s0 + 1), r1);
-        L::template convert_range<0, 0, 16>(r0, b0);
+        constexpr int G = L::kGroups, N = L::kLoads;
+        L::template stage<0, G>(at, s0, tiles[0]);
+        L::template stage<0, G>(at, clamp(s0 + 1), tiles[1]);
+        if (L::kBufs > 3) L::template stage<0, G>(at, clamp(s0 + 2), tiles[2]);
+        L::template load_range<0, N>(p, at, L::from(p, at, s0), r0);
+        L::template load_range<0, N>(p, at, L::from(p, at, clamp(s0 + 1)), r1);
+        L::template convert_all<0>(r0, b0);
         wait_loads();
         __syncthreads();
-        const uint8_t *t0 = tiles[0], *t1 = tiles[1], *t2 = tiles[2];  // this step's, the next one's, the one after
+        // this step's, the next one's, and so on
+        const uint8_t *t0 = tiles[0], *t1 = tiles[1], *t2 = tiles[2], *t3 = tiles[L::kBufs - 1];
         if constexpr (L::kAhead > 0) {
 #pragma unroll
             for (int m = 0; m < L::kAhead; ++m) a[m] = L::read_a(t0 + a0, m);
         }
         auto step = [&](int64_t i, typename L::Raw &now, const typename L::Raw &next) {
-            L::template rows_from<1, 0>(t0 + a0, t0 + a1, b0, now, b1, a, acc);
+            const typename L::From f = L::from(p, at, clamp(i + 2));
+            auto load = [&](auto m) {
+                L::template load_range<L::loads_before(m.value - 1), L::loads_before(m.value)>(p, at, f, now);
+            };
+            L::template rows_from<1, 0>(t0 + a0, t0 + a1, b0, now, b1, a, scale, acc, load);
+            load(std::integral_constant<int, MT>{});
             // Every wave's share of the next step's activations has landed once all
-            // are past the barrier, and no wave reads the step before this one any more.
-            wait_loads();
-            __syncthreads();
-            L::stage(at, clamp(i + 2), const_cast<uint8_t *>(t2));
-            L::load(p, at, clamp(i + 2), now);
-            L::template rows_from<0, 0>(t0 + a1, t1 + a0, b1, next, b0, a, acc);
+            // are past the barrier, and no wave reads the step before this one any
+            // more. Newer than that share are, with four buffers, the share of the
+            // step after and twice four loads of codes or more; with three, four.
+            wait_loads<L::kBufs == 4 ? G + 8 : 4>();
+            barrier_only();
+            uint8_t *to = const_cast<uint8_t *>(L::kBufs == 4 ? t3 : t2);
+            auto stage = [&](auto m) {
+                L::template stage<G * m.value / MT, G *(m.value + 1) / MT>(at, clamp(i + L::kBufs - 1), to);
+            };
+            L::template rows_from<0, 0>(t0 + a1, t1 + a0, b1, next, b0, a, scale, acc, stage);
             const uint8_t *t = t0;
-            t0 = t1, t1 = t2, t2 = t;
+            t0 = t1, t1 = t2;
+            if (L::kBufs == 4)
+                t2 = t3, t3 = t;
+            else
+                t2 = t;
         };
         for (int64_t i = s0; i < s1; i += 2) {
             step(i, r0, r1);
-            if (i + 1 < s1)
-                step(i + 1, r1, r0);
-            else
-                wait_loads();  // so that no way into the loop has codes pending, and its start waits for none
+            step(i + 1, r1, r0);
         }
         wait_loads();
     }
 
-    if (rest) {
+    auto guarded = [&](int64_t c) {
+        if (c >= c1) return;
         typename L::Raw r;
         __syncthreads();
-        L::Tile::stage_async(p, m0, full * kStep, c_len, tiles[0]);
-        L::load_last(p, wave_col, full * kStep, r);
-        L::template convert_range<0, 0, 16>(r, b0);
-        L::template convert_range<1, 0, 16>(r, b1);
+        L::Tile::stage_async(p, m0, c, c_len, tiles[0]);
+        L::load_last(p, wave_col, c, r);
+        L::template convert_all<0>(r, b0);
+        L::template convert_all<1>(r, b1);
         wait_loads();
         __syncthreads();
+        operands_ready<L::kPin>();
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const u32x4 x = L::read_a(tiles[0] + a0, m), y = L::read_a(tiles[0] + a1, m);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc[m][t] = mfma16(y, b1[t], mfma16(x, b0[t], acc[m][t]));
+            for (int t = 0; t < 4; ++t) mfma<L::kPin>(x, b0[t], acc[m][t]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) mfma<L::kPin>(y, b1[t], acc[m][t]);
         }
-    }
+    };
+    guarded(s1 * kStep);
+    guarded(s1 * kStep + kStep);
 
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) settle<L::kPin>(acc[m][t]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t row = m0 + m * 16 + 4 * q + i;

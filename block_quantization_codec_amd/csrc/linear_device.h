@@ -83,11 +83,13 @@ __device__ __forceinline__ f32x4 mfma_parts(const u32x4 (&a)[PA], const u32x4 (&
 constexpr int kMidTiles = 2;
 constexpr int kMidChunks = 2;
 
-// Waits for all of this wave's loads, those into LDS among them, in a form the
-// compiler counts too (it then waits for none of them again).
+// Waits for this wave's loads, those into LDS among them, all but the last N, in
+// a form the compiler counts too (it then waits for none of them again).
+template <int N = 0>
 __device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "the counter has 6 bits, the upper 2 apart");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), nothing else
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);  // vmcnt(N), nothing else
     asm volatile("" ::: "memory");
 }
 

@@ -51,13 +51,15 @@ struct LinPlace {
 };
 
 __device__ __forceinline__ LinPlace lin_place(const LinArgs &p, int rows) {
-    const int64_t id = xcd_block(blockIdx.x, gridDim.x);
-    const int64_t tiles_all = p.row_tiles * p.col_tiles;
-    const int64_t split = id / tiles_all, tid = id % tiles_all;
-    const int64_t g = tid / (8 * p.col_tiles);
-    const int64_t in_g = min(INT64_C(8), p.row_tiles - g * 8);
-    const int64_t at = tid - g * 8 * p.col_tiles;
-    return LinPlace{split, (g * 8 + at % in_g) * rows, (at / in_g) * kTileCols};
+    // A launch has fewer than 2^24 workgroups. Divisions leave their results in
+    // vector registers; read back, they and all that follows from them are scalar.
+    auto div = [](uint32_t a, uint32_t b) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(a / b)); };
+    const uint32_t id = static_cast<uint32_t>(xcd_block(blockIdx.x, gridDim.x));
+    const uint32_t row_tiles = static_cast<uint32_t>(p.row_tiles), col_tiles = static_cast<uint32_t>(p.col_tiles);
+    const uint32_t split = div(id, row_tiles * col_tiles), tile = id - split * (row_tiles * col_tiles);
+    const uint32_t g = div(tile, 8 * col_tiles), in_g = min(8u, row_tiles - g * 8), at = tile - g * 8 * col_tiles;
+    const uint32_t col = div(at, in_g), row = g * 8 + (at - col * in_g);
+    return LinPlace{split, static_cast<int64_t>(row) * rows, static_cast<int64_t>(col) * kTileCols};
 }
 
 template <bool GRAD, int BITS, int PA, int PB, int MT, bool ASYNC>
