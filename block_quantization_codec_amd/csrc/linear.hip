@@ -1,13 +1,15 @@
 // linear.hip - which kernels a linear product on block codes takes, and the
 // sum of the parts of a split contraction.
 #include <algorithm>
+#include <cmath>
 
+#include "../../include/zpp.h"
 #include "linear_device.h"
 
 namespace zpp {
 
 hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
-hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
+hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream);
 hipError_t launch_linear_tile_fwd4(const LinArgs &p, int mode, int mt, hipStream_t stream);
 hipError_t launch_linear_big_fwd4(const LinArgs &p, int mt, hipStream_t stream);
 hipError_t launch_linear_tile_fwd8(const LinArgs &p, int mode, int mt, hipStream_t stream);
@@ -23,6 +25,7 @@ constexpr int64_t kCus = 256;       // MI355X
 constexpr int64_t kFewRows = 4;     // forward: at most this many rows stream the codes, x in registers,
 constexpr int64_t kMidRows = 64;    // and this many with x in LDS
 constexpr int64_t kMidGroups = 512;  // workgroups the middle kernel's contraction is split for
+constexpr int64_t kMaxBigStride = INT64_C(1) << 22;  // elements: a tile's offsets of linear_big.h are 32-bit
 constexpr int64_t kMaxTiles = 1 << 23;  // workgroups of one launch
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -37,36 +40,71 @@ struct Plan {
     int64_t rows; // rows of one launch
 };
 
-// Rows per workgroup: 256 (128 where operands have three parts) as long as
-// that still gives every CU a tile, 64 or 16 otherwise. Where even those
-// leave CUs idle, the contraction is split over workgroups, in parts of four
-// steps or more, and a second kernel sums the parts in order.
+// What a tiled call takes, in microseconds, with workgroups of mt rows of 16
+// and the contraction in `splits` parts: rounds of workgroups over the CUs
+// times steps times a step's time, and, if split, the writing, reading and
+// joining of the parts (5.5 bytes a nanosecond and 7 us). A step takes, with
+// the operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured
+// at 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
+double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, int64_t split_steps) {
+    static constexpr double step_us[3][4] = {{0.92, 1.05, 1.08, 1.60}, {1.90, 2.30, 3.20, 0}, {2.10, 3.30, 5.00, 0}};
+    const int i = mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3;
+    const double tiles = static_cast<double>(ceil_div(rows, 16 * mt) * ceil_div(len, 256) * splits);
+    double rounds = std::max(tiles / kCus, 1.0);
+    if (parts > 0 || mt == 16) rounds = std::ceil(rounds);  // one workgroup a CU; otherwise they overlap
+    double t = rounds * static_cast<double>(split_steps) * step_us[parts][i];
+    if (splits > 1) t += 7.0 + static_cast<double>(splits * rows * len) * 8 / 5.5e6;
+    return t;
+}
+
+// The way of the least time. Measured on the way: 128 rows of 8192 x 8192 int4,
+// 39 us as 128-row tiles in 8 parts (41 estimated) against 48 as 256-row tiles
+// in 8, 50 as 64-row tiles in 4 and 135 or more unsplit; 1024 rows, 132 us as
+// 256-row tiles in 2 (133) against 146 as 128-row tiles unsplit (142).
+//
+// A product to binary32 (or from it) multiplies by the exact codes at any
+// number of rows: one part of the weights in place of three. 333 rows of 11008
+// x 4096 int8: 86 us so, 155 with three parts in tiles. From 128 rows of binary32 on, the tiles are faster (1024 rows of
+// 8192 x 8192 int4: 643 us against 829).
 Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
     Plan p{};
-    if (!grad && rows <= kMidRows) {
+    if (!grad && rows <= kFewRows) {
+        p.way = Way::few;
         p.rows = rows;
-        if (rows <= kFewRows) {
-            p.way = Way::few;
-            p.splits = 1;
-            return p;
-        }
+        p.splits = 1;
+        return p;
+    }
+    if (!grad && rows <= (in_f32 ? 2 * kMidRows : out_f32 ? ZPP_MAX_ROWS : kMidRows)) {
         p.way = Way::mid;
-        const int64_t steps = ceil_div(n_in, 128 * kMidChunks), tiles = ceil_div(n_out, 64 * kMidTiles);
+        p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+        const int64_t steps = ceil_div(n_in, 128 * kMidChunks), col_tiles = ceil_div(n_out, 64 * kMidTiles);
+        const int64_t tiles = col_tiles * ceil_div(rows, 16 * p.mt);
         const int64_t splits = std::max<int64_t>(std::min(kMidGroups / tiles, steps / 4), 1);
         p.split_steps = ceil_div(steps, splits);
         p.splits = static_cast<int>(ceil_div(steps, p.split_steps));
+        p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
         return p;
     }
     p.way = Way::tile;
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     const int64_t col_tiles = ceil_div(len, 256), steps = ceil_div(c_len, 64);
-    const int big = in_f32 || out_f32 ? 8 : 16;
-    p.mt = rows <= 16 ? 1 : (ceil_div(rows, 16 * big) * col_tiles >= kCus * 3 / 4 ? big : 4);
-    const int64_t tiles = ceil_div(rows, 16 * p.mt) * col_tiles;
-    int64_t splits = 1;
-    if (tiles < kCus) splits = std::min({kCus / tiles, std::max<int64_t>(steps / 4, 1), INT64_C(64)});
-    p.split_steps = ceil_div(steps, splits);
-    p.splits = static_cast<int>(ceil_div(steps, p.split_steps));
+    const int parts = in_f32 ? 2 : out_f32 ? 1 : 0;
+    double least = 0;
+    for (const int mt : {16, 8, 4, 1}) {
+        if (mt == 16 && parts > 0) continue;
+        for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            if (want > 1 && want > steps / 3) break;
+            // the pipeline takes steps in pairs
+            const int64_t each = want == 1 ? steps : ceil_div(ceil_div(steps, want), 2) * 2, n = ceil_div(steps, each);
+            const double t = tile_time(parts, mt, n, rows, len, each);
+            if (p.mt == 0 || t < least) {
+                least = t;
+                p.mt = mt;
+                p.splits = static_cast<int>(n);
+                p.split_steps = each;
+            }
+        }
+    }
     p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
     return p;
 }
@@ -118,7 +156,7 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
                          bool out_f32, int64_t ldo, void *workspace, hipStream_t stream) {
     const Plan plan = make_plan(grad, in_f32, out_f32, rows, n_out, n_in);
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
-    const int mode = in_f32 ? 3 : out_f32 ? 2 : (lda % 8 == 0 && c_len % 8 == 0) ? 0 : 1;
+    const int mode = in_f32 ? 3 : out_f32 ? 2 : (lda % 8 == 0 && c_len % 8 == 0 && lda <= kMaxBigStride) ? 0 : 1;
     for (int64_t r0 = 0; r0 < rows; r0 += plan.rows) {
         LinArgs p{};
         p.a = static_cast<const uint8_t *>(a) + r0 * lda * (in_f32 ? 4 : 2);
@@ -139,8 +177,9 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
         if (plan.way == Way::few) {
             e = launch_linear_few(p, bits, in_f32, stream);
         } else if (plan.way == Way::mid) {
+            p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
             p.col_tiles = ceil_div(n_out, 64 * kMidTiles);
-            e = launch_linear_mid(p, bits, in_f32, stream);
+            e = launch_linear_mid(p, bits, in_f32, plan.mt, stream);
         } else {
             p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
             p.col_tiles = ceil_div(len, 256);

@@ -63,7 +63,7 @@ __device__ __forceinline__ void barrier_only() {
 
 template <bool GRAD, int BITS, int MT>
 struct LinBig {
-    static constexpr bool kPin = MT == 16;
+    static constexpr bool kPin = MT >= 4;
     using Tile = LinTile<GRAD, BITS, 1, 1, MT, true>;
     static constexpr int kRows = 16 * MT;
     static constexpr int kBytes = Tile::kPlane;
@@ -82,7 +82,8 @@ struct LinBig {
     // Bases are the same in every lane of a wave; lanes add 32-bit offsets.
     // Scales are counted in units of 32 weights, relative to a base.
     struct At {
-        const uint8_t *a[kGroups];  // the lane's own: activations may have any row stride
+        const uint8_t *a;  // activations from the tile's first row on
+        uint32_t piece[kGroups];
         const uint8_t *codes;
         uint32_t code[GRAD ? 1 : 4], unit[GRAD ? 1 : 4];
         int64_t first;  // the base's unit: of the wave's first row (y), of its first column (dx)
@@ -95,10 +96,11 @@ struct LinBig {
         const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
         const uint32_t q = lane >> 4, j = lane & 15;
         At at;
+        at.a = static_cast<const uint8_t *>(p.a) + m0 * p.lda * 2;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int r = (i * 4 + w) * 8 + (lane >> 3), c = (lane & 7) ^ (r & 7);
-            at.a[i] = static_cast<const uint8_t *>(p.a) + min(m0 + r, p.rows - 1) * p.lda * 2 + c * 16;
+            at.piece[i] = static_cast<uint32_t>(min(static_cast<int64_t>(r), p.rows - 1 - m0) * p.lda * 2) + c * 16;
         }
         at.shift = p.log2b - 5;
         at.units = p.n_in >> 5;
@@ -128,14 +130,21 @@ struct LinBig {
     // Groups I .. END - 1 of a whole step's activations.
     template <int I, int END>
     static __device__ __forceinline__ void stage(const At &at, int64_t step, uint8_t *tile) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        // A buffer load: its scalar offset takes the step, so that no lane computes
+        // an address, and it counts as a global load alone. Offsets are 32-bit; the
+        // plan sends longer row strides elsewhere. 0x27000: plain 32-bit data.
+        const __amdgpu_buffer_rsrc_t from =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(at.a), 0, 0xFFFFFFFFu, 0x27000);
         const int w = wave_in_block();
 #pragma unroll
         for (int i = I; i < END; ++i) {
             const int g = i * 4 + w;
             if (2 * MT % 4 != 0 && g >= 2 * MT) break;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(at.a[i] + step * 128),
-                                             (__attribute__((address_space(3))) void *)(tile + g * 1024), 16, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)(tile + g * 1024),
+                                                     16, at.piece[i], static_cast<int>(step * 128), 0, 0);
         }
+#endif
     }
 
     // Where a whole step's codes and scales begin.
@@ -340,7 +349,7 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 ? 1 : 2) void linear_big_ke
     const int q = lane >> 4;
     const int64_t c_len = GRAD ? p.n_out : p.n_in, len = GRAD ? p.n_in : p.n_out;
     const LinPlace at_tile = lin_place(p, L::kRows);
-    const int64_t m0 = at_tile.m0, wave_col = at_tile.col0 + w * 64, col = wave_col + (lane & 15) * 4;
+    const int64_t m0 = at_tile.m0, wave_col = at_tile.col * kTileCols + w * 64, col = wave_col + (lane & 15) * 4;
     const typename L::At at = L::place(p, m0, wave_col);
 
     // The split's indices: an even number of whole steps in the pipeline, then the rest.

@@ -1,5 +1,6 @@
-// linear_mid.hip - y = x W^T on block codes for up to 64 rows of x: the stream
-// over the codes of linear_few.hip, with the activations in LDS.
+// linear_mid.hip - y = x W^T on block codes for up to 64 rows of x, and for any
+// number where x or y is binary32: the stream over the codes of
+// linear_few.hip, with the activations in LDS.
 //
 // With more than a few rows, every wave reading x for itself takes as much of
 // the path from L2 as the codes do (measured at 16 rows: a third more time).
@@ -23,9 +24,9 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
 
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     const uint32_t q = lane >> 4;
-    const int64_t id = xcd_block(blockIdx.x, gridDim.x);
-    const int64_t split = id / p.col_tiles;
-    const int64_t n0 = ((id % p.col_tiles) * 4 + w) * (16 * NT);
+    const LinPlace place = lin_place(p, T::kRows);
+    const int64_t split = place.split, m0 = place.m0;
+    const int64_t n0 = (place.col * 4 + w) * (16 * NT);
     // a wave past the last feature works on it, and stores nothing
     const typename C::At at = C::place(p, min(n0, p.n_out - 1));
     const bool vec = (p.lda & 3) == 0;
@@ -45,9 +46,9 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
 #pragma unroll
         for (int h = 0; h < 2 * U; ++h) {
             if constexpr (ASYNC)
-                T::stage_async(p, 0, k + h * 64, p.n_in, tiles[buf][h]);
+                T::stage_async(p, m0, k + h * 64, p.n_in, tiles[buf][h]);
             else
-                T::stage_load(p, 0, k + h * 64, p.n_in, vec, held[h]);
+                T::stage_load(p, m0, k + h * 64, p.n_in, vec, held[h]);
         }
     };
     auto land = [&](int buf) {
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t row = m * 16 + 4 * q + i;
+                const int64_t row = m0 + m * 16 + 4 * q + i;
                 if (row >= p.rows || col >= p.n_out) continue;
                 const float v = acc[t][m][i];
                 if (p.splits > 1)
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
 template <int BITS, int PA, int MT>
 hipError_t launch_as(const LinArgs &p, bool wide, hipStream_t stream) {
     constexpr int U = PA == 1 ? kMidChunks : 1;  // three parts of 64 rows fill LDS as they are
-    const unsigned grid = static_cast<unsigned>(p.col_tiles * p.splits);
+    const unsigned grid = static_cast<unsigned>(p.row_tiles * p.col_tiles * p.splits);
     if (wide)
         linear_mid_kernel<BITS, PA, kMidTiles, MT, U, true><<<grid, kBlockThreads, 0, stream>>>(p);
     else
@@ -136,18 +137,18 @@ hipError_t launch_as(const LinArgs &p, bool wide, hipStream_t stream) {
 }
 
 template <int BITS, int PA>
-hipError_t launch_rows(const LinArgs &p, bool wide, hipStream_t stream) {
-    if (p.rows <= 16) return launch_as<BITS, PA, 1>(p, wide, stream);
-    if (p.rows <= 32) return launch_as<BITS, PA, 2>(p, wide, stream);
+hipError_t launch_rows(const LinArgs &p, bool wide, int mt, hipStream_t stream) {
+    if (mt == 1) return launch_as<BITS, PA, 1>(p, wide, stream);
+    if (mt == 2) return launch_as<BITS, PA, 2>(p, wide, stream);
     return launch_as<BITS, PA, 4>(p, wide, stream);
 }
 
 }  // namespace
 
-hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, hipStream_t stream) {
+hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream) {
     const bool wide = p.log2b >= 7 && p.n_in % kChunk == 0;
-    if (bits == 4) return a_f32 ? launch_rows<4, 3>(p, wide, stream) : launch_rows<4, 1>(p, wide, stream);
-    return a_f32 ? launch_rows<8, 3>(p, wide, stream) : launch_rows<8, 1>(p, wide, stream);
+    if (bits == 4) return a_f32 ? launch_rows<4, 3>(p, wide, mt, stream) : launch_rows<4, 1>(p, wide, mt, stream);
+    return a_f32 ? launch_rows<8, 3>(p, wide, mt, stream) : launch_rows<8, 1>(p, wide, mt, stream);
 }
 
 }  // namespace zpp

@@ -47,7 +47,7 @@ __device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ 
 // rows of tiles run down before the next column, so that the 32 tiles an XCD
 // works on at once share both activations and codes in its L2.
 struct LinPlace {
-    int64_t split, m0, col0;
+    int64_t split, m0, col;
 };
 
 __device__ __forceinline__ LinPlace lin_place(const LinArgs &p, int rows) {
@@ -59,7 +59,7 @@ __device__ __forceinline__ LinPlace lin_place(const LinArgs &p, int rows) {
     const uint32_t split = div(id, row_tiles * col_tiles), tile = id - split * (row_tiles * col_tiles);
     const uint32_t g = div(tile, 8 * col_tiles), in_g = min(8u, row_tiles - g * 8), at = tile - g * 8 * col_tiles;
     const uint32_t col = div(at, in_g), row = g * 8 + (at - col * in_g);
-    return LinPlace{split, static_cast<int64_t>(row) * rows, static_cast<int64_t>(col) * kTileCols};
+    return LinPlace{split, static_cast<int64_t>(row) * rows, col};
 }
 
 template <bool GRAD, int BITS, int PA, int PB, int MT, bool ASYNC>
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kBlockThreads, 1) void linear_tile_kernel(LinArgs p
 
     const LinPlace place = lin_place(p, T::kRows);
     const int64_t split = place.split, m0 = place.m0;
-    const int64_t col = place.col0 + w * 64 + (lane & 15) * 4;
+    const int64_t col = place.col * kTileCols + w * 64 + (lane & 15) * 4;
 
     const int64_t steps = (c_len + kStep - 1) / kStep;
     const int64_t s0 = split * p.split_steps, s1 = min(steps, s0 + p.split_steps);
@@ -351,9 +351,10 @@ hipError_t launch_linear_tile_one(const LinArgs &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The kernels of one direction and code width: mode 1 is bf16 to bf16 with
-// activations that are not whole 16-byte pieces (only the gradient's can be),
-// 2 bf16 to binary32, 3 binary32 activations. mt is the plan's.
+// The kernels of one direction and code width: mode 1 is bf16 to bf16 where
+// linear_big.h cannot (activations that are not whole 16-byte pieces, which
+// only the gradient's can be, or row strides past 32-bit offsets), 2 bf16 to
+// binary32, 3 binary32 activations. mt is the plan's.
 template <bool GRAD, int BITS>
 hipError_t launch_linear_tile_as(const LinArgs &p, int mode, int mt, hipStream_t stream) {
     if (mode == 3) {
@@ -366,13 +367,10 @@ hipError_t launch_linear_tile_as(const LinArgs &p, int mode, int mt, hipStream_t
         if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 3, 4, false>(p, stream);
         return launch_linear_tile_one<GRAD, BITS, 1, 3, 1, false>(p, stream);
     }
-    if constexpr (GRAD) {
-        if (mt == 16) return launch_linear_tile_one<GRAD, BITS, 1, 1, 16, false>(p, stream);
-        if (mt == 8) return launch_linear_tile_one<GRAD, BITS, 1, 1, 8, false>(p, stream);
-        if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 1, 4, false>(p, stream);
-        return launch_linear_tile_one<GRAD, BITS, 1, 1, 1, false>(p, stream);
-    }
-    return hipErrorInvalidValue;
+    if (mt == 16) return launch_linear_tile_one<GRAD, BITS, 1, 1, 16, false>(p, stream);
+    if (mt == 8) return launch_linear_tile_one<GRAD, BITS, 1, 1, 8, false>(p, stream);
+    if (mt == 4) return launch_linear_tile_one<GRAD, BITS, 1, 1, 4, false>(p, stream);
+    return launch_linear_tile_one<GRAD, BITS, 1, 1, 1, false>(p, stream);
 }
 
 }  // namespace zpp
