@@ -7,15 +7,15 @@
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 //
 // Both are streams: one read of every input and one write of every output.
-// A unit of T threads (a wave, 4 or 16 of them, by the row's width) holds a
-// whole row in registers, up to 32 elements a thread, so the variance is the
-// sum of squared differences from the mean already known (no cancellation)
-// and nothing is read twice. Units walk over the rows, keeping the weights,
+// A unit of T threads (a wave to 16 of them, by the row's width) holds a whole
+// row in registers, up to 32 elements a thread, so the variance is the sum of
+// squared differences from the mean already known (no cancellation) and
+// nothing is read twice; the next row is on its way meanwhile. Units walk over the rows, keeping the weights,
 // and in the backward pass their share of dw and db, in registers; the units'
 // shares go to the workspace and a second kernel sums them in unit order, so
 // the result does not change from run to run. Rows wider than 32,768 elements
-// are read again for each sum instead (LONG); their shares are summed in the
-// workspace itself.
+// (16,384 backward) are read again for each sum instead; their shares are
+// summed in the workspace itself.
 //
 // All sums are binary32. Rows whose elements lie on 16-byte pieces move as
 // such (V elements each); any others element by element, still contiguous
@@ -29,8 +29,6 @@ namespace zpp {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kHeld = 32;  // elements of a row a thread holds
 
 __device__ __forceinline__ float add_dpp(float v, uint32_t o) { return v + as_f(o); }
 
@@ -134,47 +132,85 @@ struct NormArgs {
     int64_t units;
 };
 
-// The columns a thread of a unit holds: chunk i is V elements at (i T + thread) V.
-template <int T, int V>
-__device__ __forceinline__ int64_t column(int i) {
-    return (static_cast<int64_t>(i) * T + threadIdx.x % T) * V;
-}
+// What a thread holds of a row, as loaded: N chunks of V elements, chunk i at
+// column (i T + thread) V. Rows are loaded one ahead, so they stay packed.
+template <bool F32, int V, int T, int N>
+struct Held {
+    static constexpr int kW = F32 ? V : (V + 1) / 2;  // dwords of a chunk
+    uint32_t w[N][kW];
 
-template <bool F32, int V, int T>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(NormArgs p) {
-    constexpr int kThreads = T < 256 ? 256 : T, kUnits = kThreads / T, kN = kHeld / V;
+    static __device__ __forceinline__ int64_t column(int i) {
+        return (static_cast<int64_t>(i) * T + threadIdx.x % T) * V;
+    }
+
+    // Columns past the width are zeros.
+    __device__ __forceinline__ void load(const void *base, int64_t e, int64_t width) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t c = column(i);
+#pragma unroll
+            for (int j = 0; j < kW; ++j) w[i][j] = 0;
+            if (c >= width) continue;
+            if constexpr (V == 1) {
+                w[i][0] = F32 ? static_cast<const uint32_t *>(base)[e + c] : static_cast<const uint16_t *>(base)[e + c];
+            } else {
+                const u32x4 v = ld<u32x4>(static_cast<const uint8_t *>(base) + (e + c) * (F32 ? 4 : 2));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[i][j] = v[j];
+            }
+        }
+    }
+
+    __device__ __forceinline__ float at(int i, int j) const {
+        if constexpr (F32)
+            return as_f(w[i][j]);
+        else
+            return V == 1 || j % 2 == 0 ? bf16_lo(w[i][j / 2]) : bf16_hi(w[i][j / 2]);
+    }
+};
+
+constexpr int group(int T) { return T < 256 ? 256 : T; }  // threads of a workgroup
+
+// HOLD: the weights stay in registers over the rows (else they are read again for each).
+template <bool F32, int V, int T, int N, bool HOLD>
+__global__ __launch_bounds__(group(T)) void norm_kernel(NormArgs p) {
+    using H = Held<F32, V, T, N>;
+    constexpr int kUnits = group(T) / T;
     __shared__ float lds[T > kWave ? 2 * (T / kWave) : 1];
     int turn = 0;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kUnits + (kUnits > 1 ? wave_in_block() : 0);
+    if (kUnits > 1 && unit >= p.rows) return;
     const float inv = 1.0f / static_cast<float>(p.width);
-    float w[kN][V], b[kN][V];
+    float w[HOLD ? N : 1][V], b[HOLD ? N : 1][V];
+    H x, next;
+    next.load(p.x, unit * p.x_stride, p.width);
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int64_t c = min(column<T, V>(i) + j, p.width - 1);
-            w[i][j] = load_w(p.weight, p.w_f32, c, 1.0f);
-            b[i][j] = load_w(p.bias, p.w_f32, c, 0.0f);
-        }
+            for (int j = 0; j < V; ++j) {
+                const int64_t c = min(H::column(i) + j, p.width - 1);
+                w[i][j] = load_w(p.weight, p.w_f32, c, 1.0f);
+                b[i][j] = load_w(p.bias, p.w_f32, c, 0.0f);
+            }
+    }
     for (int64_t r = unit; r < p.rows; r += p.units) {
-        float x[kN][V], s[1] = {0.0f};
+        if constexpr (!HOLD) asm volatile("" ::: "memory");  // the weights' loads stay in the loop
+        x = next;
+        if (r + p.units < p.rows) next.load(p.x, (r + p.units) * p.x_stride, p.width);
+        float s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int64_t c = column<T, V>(i);
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[i][j] = 0.0f;
-            if (c < p.width) load_v<F32, V>(p.x, r * p.x_stride + c, x[i]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[0] += x[i][j];
-        }
+            for (int j = 0; j < V; ++j) s[0] += x.at(i, j);
         unit_sum<T>(s, lds, turn);
         const float mean = s[0] * inv;
         s[0] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float d = column<T, V>(i) < p.width ? x[i][j] - mean : 0.0f;
+                const float d = H::column(i) < p.width ? x.at(i, j) - mean : 0.0f;
                 s[0] = __builtin_fmaf(d, d, s[0]);
             }
         unit_sum<T>(s, lds, turn);
@@ -184,102 +220,120 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(NormArgs p) {
             p.rstd[r] = rstd;
         }
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int64_t c = column<T, V>(i);
+        for (int i = 0; i < N; ++i) {
+            const int64_t c = H::column(i);
             if (c >= p.width) continue;
             float y[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = __builtin_fmaf((x[i][j] - mean) * rstd, w[i][j], b[i][j]);
+            for (int j = 0; j < V; ++j) {
+                const float wj = HOLD ? w[HOLD ? i : 0][j] : load_w(p.weight, p.w_f32, c + j, 1.0f);
+                const float bj = HOLD ? b[HOLD ? i : 0][j] : load_w(p.bias, p.w_f32, c + j, 0.0f);
+                y[j] = __builtin_fmaf((x.at(i, j) - mean) * rstd, wj, bj);
+            }
             store_v<F32, V>(p.y, r * p.y_stride + c, y);
         }
     }
 }
 
-template <bool F32, int V, int T>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(NormArgs p) {
-    constexpr int kThreads = T < 256 ? 256 : T, kUnits = kThreads / T, kN = kHeld / V;
+// AHEAD: the next row's loads are made before this row's sums; a workgroup of
+// 16 waves has too few registers a lane for that.
+template <bool F32, int V, int T, int N, bool AHEAD>
+__global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
+    using H = Held<F32, V, T, N>;
+    constexpr int kUnits = group(T) / T;
     __shared__ float lds[T > kWave ? 2 * 2 * (T / kWave) : 1];
     int turn = 0;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kUnits + (kUnits > 1 ? wave_in_block() : 0);
     if (kUnits > 1 && unit >= p.units) return;
     const float inv = 1.0f / static_cast<float>(p.width);
-    float dw[kN][V], db[kN][V];
+    float w[N][V], dw[N][V], db[N][V];
+    H x, dy, next_x, next_dy;
+    float mean, rstd, next_mean, next_rstd;
+    auto fetch = [&](int64_t r) {
+        next_x.load(p.x, r * p.x_stride, p.width);
+        next_dy.load(p.dy, r * p.dy_stride, p.width);
+        next_mean = p.mean[r], next_rstd = p.rstd[r];
+    };
+    if constexpr (AHEAD) fetch(unit);
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = 0.0f;
-    for (int64_t r = unit; r < p.rows; r += p.units) {
-        float xh[kN][V], dy[kN][V], s[2] = {0.0f, 0.0f};
-        const float mean = p.mean[r], rstd = p.rstd[r];
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int64_t c = column<T, V>(i);
-#pragma unroll
-            for (int j = 0; j < V; ++j) xh[i][j] = dy[i][j] = 0.0f;
-            if (c < p.width) {
-                load_v<F32, V>(p.x, r * p.x_stride + c, xh[i]);
-                load_v<F32, V>(p.dy, r * p.dy_stride + c, dy[i]);
-            }
+        for (int j = 0; j < V; ++j) {
+            w[i][j] = load_w(p.weight, p.w_f32, min(H::column(i) + j, p.width - 1), 1.0f);
+            dw[i][j] = db[i][j] = 0.0f;
         }
+    for (int64_t r = unit; r < p.rows; r += p.units) {
+        if constexpr (!AHEAD) fetch(r);
+        x = next_x, dy = next_dy, mean = next_mean, rstd = next_rstd;
+        if (AHEAD && r + p.units < p.rows) fetch(r + p.units);
+        // columns past the width have dy = 0: they add nothing (x = 0 there, so xh is finite as mean and rstd are)
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int64_t c = column<T, V>(i);
-            if (c >= p.width) continue;
+        for (int i = 0; i < N; ++i) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                xh[i][j] = (xh[i][j] - mean) * rstd;
-                dw[i][j] = __builtin_fmaf(dy[i][j], xh[i][j], dw[i][j]);
-                db[i][j] += dy[i][j];
-                dy[i][j] *= load_w(p.weight, p.w_f32, c + j, 1.0f);
-                s[0] += dy[i][j];
-                s[1] = __builtin_fmaf(dy[i][j], xh[i][j], s[1]);
+                const float xh = (x.at(i, j) - mean) * rstd, d = dy.at(i, j), g = d * w[i][j];
+                dw[i][j] = __builtin_fmaf(d, xh, dw[i][j]);
+                db[i][j] += d;
+                s[0] += g;
+                s[1] = __builtin_fmaf(g, H::column(i) < p.width ? xh : 0.0f, s[1]);
             }
         }
         unit_sum<T>(s, lds, turn);
         const float m0 = s[0] * inv, m1 = s[1] * inv;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int64_t c = column<T, V>(i);
+        for (int i = 0; i < N; ++i) {
+            const int64_t c = H::column(i);
             if (c >= p.width) continue;
             float dx[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) dx[j] = (dy[i][j] - m0 - xh[i][j] * m1) * rstd;
+            for (int j = 0; j < V; ++j) {
+                const float xh = (x.at(i, j) - mean) * rstd;
+                dx[j] = (dy.at(i, j) * w[i][j] - m0 - xh * m1) * rstd;
+            }
             store_v<F32, V>(p.y, r * p.y_stride + c, dx);
         }
     }
     float *mine = p.partial + unit * 2 * p.width;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const int64_t c = column<T, V>(i);
+    for (int i = 0; i < N; ++i) {
+        const int64_t c = H::column(i);
         if (c >= p.width) continue;
+        if constexpr (V > 1) {  // the width is a multiple of V, so both shares are 16-byte aligned
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            mine[c + j] = dw[i][j];
-            mine[p.width + c + j] = db[i][j];
+            for (int j = 0; j < V; j += 4) {
+                st<f32x4>(mine + c + j, f32x4{dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]});
+                st<f32x4>(mine + p.width + c + j, f32x4{db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]});
+            }
+        } else {
+            mine[c] = dw[i][0];
+            mine[p.width + c] = db[i][0];
         }
     }
 }
 
 constexpr int kLong = 1024;  // threads of a unit for rows beyond the registers
 
-template <bool F32>
+template <bool F32, int V>
 __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs p) {
     __shared__ float lds[2 * (kLong / kWave)];
     int turn = 0;
     const float inv = 1.0f / static_cast<float>(p.width);
     for (int64_t r = blockIdx.x; r < p.rows; r += p.units) {
         const int64_t x0 = r * p.x_stride, y0 = r * p.y_stride;
-        float s[1] = {0.0f}, v;
-        for (int64_t c = threadIdx.x; c < p.width; c += kLong) {
-            load_v<F32, 1>(p.x, x0 + c, &v);
-            s[0] += v;
+        float s[1] = {0.0f}, v[V];
+        for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
+            load_v<F32, V>(p.x, x0 + c, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[0] += v[j];
         }
         unit_sum<kLong>(s, lds, turn);
         const float mean = s[0] * inv;
         s[0] = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.width; c += kLong) {
-            load_v<F32, 1>(p.x, x0 + c, &v);
-            s[0] = __builtin_fmaf(v - mean, v - mean, s[0]);
+        for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
+            load_v<F32, V>(p.x, x0 + c, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[0] = __builtin_fmaf(v[j] - mean, v[j] - mean, s[0]);
         }
         unit_sum<kLong>(s, lds, turn);
         const float rstd = 1.0f / __builtin_sqrtf(s[0] * inv + p.eps);
@@ -287,16 +341,18 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs p) {
             p.mean[r] = mean;
             p.rstd[r] = rstd;
         }
-        for (int64_t c = threadIdx.x; c < p.width; c += kLong) {
-            load_v<F32, 1>(p.x, x0 + c, &v);
-            v = __builtin_fmaf((v - mean) * rstd, load_w(p.weight, p.w_f32, c, 1.0f),
-                               load_w(p.bias, p.w_f32, c, 0.0f));
-            store_v<F32, 1>(p.y, y0 + c, &v);
+        for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
+            load_v<F32, V>(p.x, x0 + c, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] = __builtin_fmaf((v[j] - mean) * rstd, load_w(p.weight, p.w_f32, c + j, 1.0f),
+                                      load_w(p.bias, p.w_f32, c + j, 0.0f));
+            store_v<F32, V>(p.y, y0 + c, v);
         }
     }
 }
 
-template <bool F32>
+template <bool F32, int V>
 __global__ __launch_bounds__(kLong) void norm_grad_long_kernel(NormArgs p) {
     __shared__ float lds[2 * 2 * (kLong / kWave)];
     int turn = 0;
@@ -306,26 +362,32 @@ __global__ __launch_bounds__(kLong) void norm_grad_long_kernel(NormArgs p) {
         const int64_t x0 = r * p.x_stride, d0 = r * p.dy_stride, y0 = r * p.y_stride;
         const float mean = p.mean[r], rstd = p.rstd[r];
         const bool first = r == static_cast<int64_t>(blockIdx.x);
-        float s[2] = {0.0f, 0.0f}, x, dy;
-        for (int64_t c = threadIdx.x; c < p.width; c += kLong) {
-            load_v<F32, 1>(p.x, x0 + c, &x);
-            load_v<F32, 1>(p.dy, d0 + c, &dy);
-            x = (x - mean) * rstd;
-            // a thread's columns of the unit's shares are its own
-            mine[c] = __builtin_fmaf(dy, x, first ? 0.0f : mine[c]);
-            mine[p.width + c] = dy + (first ? 0.0f : mine[p.width + c]);
-            dy *= load_w(p.weight, p.w_f32, c, 1.0f);
-            s[0] += dy;
-            s[1] = __builtin_fmaf(dy, x, s[1]);
+        float s[2] = {0.0f, 0.0f}, x[V], dy[V];
+        for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
+            load_v<F32, V>(p.x, x0 + c, x);
+            load_v<F32, V>(p.dy, d0 + c, dy);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                x[j] = (x[j] - mean) * rstd;
+                // a thread's columns of the unit's shares are its own
+                mine[c + j] = __builtin_fmaf(dy[j], x[j], first ? 0.0f : mine[c + j]);
+                mine[p.width + c + j] = dy[j] + (first ? 0.0f : mine[p.width + c + j]);
+                dy[j] *= load_w(p.weight, p.w_f32, c + j, 1.0f);
+                s[0] += dy[j];
+                s[1] = __builtin_fmaf(dy[j], x[j], s[1]);
+            }
         }
         unit_sum<kLong>(s, lds, turn);
         const float m0 = s[0] * inv, m1 = s[1] * inv;
-        for (int64_t c = threadIdx.x; c < p.width; c += kLong) {
-            load_v<F32, 1>(p.x, x0 + c, &x);
-            load_v<F32, 1>(p.dy, d0 + c, &dy);
-            dy *= load_w(p.weight, p.w_f32, c, 1.0f);
-            x = (dy - m0 - (x - mean) * rstd * m1) * rstd;
-            store_v<F32, 1>(p.y, y0 + c, &x);
+        for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
+            load_v<F32, V>(p.x, x0 + c, x);
+            load_v<F32, V>(p.dy, d0 + c, dy);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                dy[j] *= load_w(p.weight, p.w_f32, c + j, 1.0f);
+                x[j] = (dy[j] - m0 - (x[j] - mean) * rstd * m1) * rstd;
+            }
+            store_v<F32, V>(p.y, y0 + c, x);
         }
     }
 }
@@ -356,44 +418,76 @@ __global__ __launch_bounds__(kBlockThreads) void norm_join_kernel(const float *_
         static_cast<uint16_t *>(o)[c] = static_cast<uint16_t>(pack_bf16x2(s, 0.0f));
 }
 
-// No rows: dw and db are zero.
-constexpr int64_t kMaxUnits = 512;
+constexpr int64_t kMaxHeld = 32768, kMaxGradHeld = 16384;  // widest rows in registers
 
-// Threads of a unit: as few as hold the row.
-int unit_threads(int64_t width) { return width <= 64 * kHeld ? 64 : width <= 256 * kHeld ? 256 : 1024; }
-
+// Units of the backward pass: two workgroups a CU, so that one's loads run
+// under the other's sums; every unit more is two rows of binary32 sums to write
+// and read again.
 int64_t grad_units(int64_t rows, int64_t width) {
-    const int64_t most = width > 1024 * kHeld ? 256 : unit_threads(width) == 1024 ? 256 : kMaxUnits;
-    return std::min(rows, most);
+    if (width > kMaxGradHeld) return std::min<int64_t>(rows, 256);
+    if (width <= 512) return std::min<int64_t>(rows, 2048);
+    return std::min<int64_t>(rows, 512);
 }
 
+// Threads of a unit and elements a thread holds: as few as hold the row.
 template <bool F32, int V>
 hipError_t launch_norm(NormArgs p, hipStream_t stream) {
-    const int t = unit_threads(p.width);
-    p.units = std::min<int64_t>(p.rows, t == 64 ? 8192 : t == 256 ? 2048 : 512);
-    const unsigned grid = static_cast<unsigned>(t == 64 ? (p.units + 3) / 4 : p.units);
-    if (t == 64) {
-        p.units = grid * 4;
-        norm_kernel<F32, V, 64><<<grid, 256, 0, stream>>>(p);
-    } else if (t == 256) {
-        norm_kernel<F32, V, 256><<<grid, 256, 0, stream>>>(p);
-    } else {
-        norm_kernel<F32, V, 1024><<<grid, 1024, 0, stream>>>(p);
-    }
+    const int64_t h = p.width;
+    auto go = [&](auto kernel, int units_of_group, int threads, int64_t most) {
+        p.units = std::min<int64_t>((p.rows + units_of_group - 1) / units_of_group, most / units_of_group) * units_of_group;
+        kernel<<<static_cast<unsigned>(p.units / units_of_group), threads, 0, stream>>>(p);
+    };
+    if (h <= 512)
+        go(norm_kernel<F32, V, 64, 8 / V, true>, 4, 256, 8192);
+    else if (h <= 2048)
+        go(norm_kernel<F32, V, 256, 8 / V, true>, 1, 256, 2048);
+    else if (h <= 4096)
+        go(norm_kernel<F32, V, 256, 16 / V, true>, 1, 256, 2048);
+    else if (h <= 8192)
+        go(norm_kernel<F32, V, 256, 32 / V, true>, 1, 256, 1024);
+    else if (h <= 16384)
+        go(norm_kernel<F32, V, 1024, 16 / V, true>, 1, 1024, 512);
+    else
+        go(norm_kernel<F32, V, 1024, 32 / V, false>, 1, 1024, 512);
     return hipGetLastError();
 }
 
 template <bool F32, int V>
 hipError_t launch_norm_grad(const NormArgs &p, hipStream_t stream) {
-    const int t = unit_threads(p.width);
-    const unsigned grid = static_cast<unsigned>(t == 64 ? (p.units + 3) / 4 : p.units);
-    if (t == 64)
-        norm_grad_kernel<F32, V, 64><<<grid, 256, 0, stream>>>(p);
-    else if (t == 256)
-        norm_grad_kernel<F32, V, 256><<<grid, 256, 0, stream>>>(p);
+    const int64_t h = p.width;
+    const unsigned n = static_cast<unsigned>(p.units);
+    if (h <= 512)
+        norm_grad_kernel<F32, V, 64, 8 / V, true><<<(n + 3) / 4, 256, 0, stream>>>(p);
+    else if (h <= 2048)
+        norm_grad_kernel<F32, V, 256, 8 / V, true><<<n, 256, 0, stream>>>(p);
+    else if (h <= 4096)
+        norm_grad_kernel<F32, V, 256, 16 / V, true><<<n, 256, 0, stream>>>(p);
+    else if (h <= 8192)
+        norm_grad_kernel<F32, V, 512, 16 / V, true><<<n, 512, 0, stream>>>(p);
     else
-        norm_grad_kernel<F32, V, 1024><<<grid, 1024, 0, stream>>>(p);
+        norm_grad_kernel<F32, V, 1024, 16 / V, false><<<n, 1024, 0, stream>>>(p);
     return hipGetLastError();
+}
+
+// V elements of a row at a time where they lie on 16-byte pieces, one otherwise.
+template <bool F32, int V>
+hipError_t launch_norm_any(NormArgs p, bool grad, hipStream_t stream) {
+    if (p.width <= (grad ? kMaxGradHeld : kMaxHeld))
+        return grad ? launch_norm_grad<F32, V>(p, stream) : launch_norm<F32, V>(p, stream);
+    if (!grad) p.units = std::min<int64_t>(p.rows, 512);
+    const unsigned n = static_cast<unsigned>(p.units);
+    if (grad)
+        norm_grad_long_kernel<F32, V><<<n, kLong, 0, stream>>>(p);
+    else
+        norm_long_kernel<F32, V><<<n, kLong, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_typed(const NormArgs &p, bool grad, bool f32, hipStream_t stream) {
+    const int v = f32 ? 4 : 8;
+    const bool vec = p.width % v == 0 && p.x_stride % v == 0 && p.y_stride % v == 0 && p.dy_stride % v == 0;
+    if (f32) return vec ? launch_norm_any<true, 4>(p, grad, stream) : launch_norm_any<true, 1>(p, grad, stream);
+    return vec ? launch_norm_any<false, 8>(p, grad, stream) : launch_norm_any<false, 1>(p, grad, stream);
 }
 
 }  // namespace
@@ -405,18 +499,7 @@ hipError_t launch_layer_norm(const void *x, bool f32, int64_t x_stride, int64_t 
     p.x = x, p.x_stride = x_stride, p.rows = rows, p.width = width;
     p.weight = weight, p.bias = bias, p.w_f32 = w_f32, p.eps = eps;
     p.y = y, p.y_stride = y_stride, p.mean = mean, p.rstd = rstd;
-    if (width > 1024 * kHeld) {
-        p.units = std::min<int64_t>(rows, 512);
-        if (f32)
-            norm_long_kernel<true><<<static_cast<unsigned>(p.units), kLong, 0, stream>>>(p);
-        else
-            norm_long_kernel<false><<<static_cast<unsigned>(p.units), kLong, 0, stream>>>(p);
-        return hipGetLastError();
-    }
-    const int v = f32 ? 4 : 8;
-    const bool vec = width % v == 0 && x_stride % v == 0 && y_stride % v == 0;
-    if (f32) return vec ? launch_norm<true, 4>(p, stream) : launch_norm<true, 1>(p, stream);
-    return vec ? launch_norm<false, 8>(p, stream) : launch_norm<false, 1>(p, stream);
+    return launch_norm_typed(p, false, f32, stream);
 }
 
 int64_t layer_norm_grad_workspace(int64_t rows, int64_t width) { return grad_units(rows, width) * 2 * width * 4; }
@@ -432,23 +515,11 @@ hipError_t launch_layer_norm_grad(const void *dy, int64_t dy_stride, const void 
     p.mean = const_cast<float *>(mean), p.rstd = const_cast<float *>(rstd);
     p.partial = static_cast<float *>(workspace);
     p.units = grad_units(rows, width);
-    hipError_t e = hipSuccess;
     if (rows > 0) {
-        const int v = f32 ? 4 : 8;
-        const bool vec = width % v == 0 && x_stride % v == 0 && dy_stride % v == 0 && dx_stride % v == 0;
-        if (width > 1024 * kHeld) {
-            if (f32)
-                norm_grad_long_kernel<true><<<static_cast<unsigned>(p.units), kLong, 0, stream>>>(p);
-            else
-                norm_grad_long_kernel<false><<<static_cast<unsigned>(p.units), kLong, 0, stream>>>(p);
-            e = hipGetLastError();
-        } else if (f32) {
-            e = vec ? launch_norm_grad<true, 4>(p, stream) : launch_norm_grad<true, 1>(p, stream);
-        } else {
-            e = vec ? launch_norm_grad<false, 8>(p, stream) : launch_norm_grad<false, 1>(p, stream);
-        }
+        if (const hipError_t e = launch_norm_typed(p, true, f32, stream); e != hipSuccess) return e;
     }
-    if (e != hipSuccess || (!dweight && !dbias)) return e;
+    if (!dweight && !dbias) return hipSuccess;
+    // no rows, no units: the sums are zero
     norm_join_kernel<<<static_cast<unsigned>((2 * width + 31) / 32), kBlockThreads, 0, stream>>>(
         p.partial, p.units, width, dweight, dbias, w_f32);
     return hipGetLastError();
