@@ -14,8 +14,8 @@
 // and in the backward pass their share of dw and db, in registers; the units'
 // shares go to the workspace and a second kernel sums them in unit order, so
 // the result does not change from run to run. Rows wider than 32,768 elements
-// (16,384 backward) are read again for each sum instead; their shares are
-// summed in the workspace itself.
+// (16,384 backward) are read again for each sum instead, and the backward pass
+// takes two kernels, one along the rows and one down the columns.
 //
 // All sums are binary32. Rows whose elements lie on 16-byte pieces move as
 // such (V elements each); any others element by element, still contiguous
@@ -110,10 +110,26 @@ __device__ __forceinline__ void store_v(void *base, int64_t e, const float *f) {
     }
 }
 
-// One element of a weight vector of either type; missing ones are `none`.
-__device__ __forceinline__ float load_w(const void *w, bool f32, int64_t e, float none) {
-    if (!w) return none;
-    return f32 ? static_cast<const float *>(w)[e] : bf16_lo(static_cast<const uint16_t *>(w)[e]);
+// V elements of a weight vector of either type from column c on (a multiple of
+// V within the width); a missing vector's are `none`.
+template <int V>
+__device__ __forceinline__ void load_w(const void *w, bool f32, int64_t c, float none, float (&o)[V]) {
+    if (!w) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = none;
+    } else if (f32) {
+        if constexpr (V == 1) {
+            o[0] = static_cast<const float *>(w)[c];
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; j += 4) load_v<true, 4>(w, c + j, o + j);
+        }
+    } else if constexpr (V == 4) {
+        const u32x2 v = ld<u32x2>(static_cast<const uint16_t *>(w) + c);
+        o[0] = bf16_lo(v[0]), o[1] = bf16_hi(v[0]), o[2] = bf16_lo(v[1]), o[3] = bf16_hi(v[1]);
+    } else {
+        load_v<false, V>(w, c, o);
+    }
 }
 
 struct NormArgs {
@@ -130,6 +146,7 @@ struct NormArgs {
     float *mean, *rstd;
     float *partial;  // [units][2][width]: each unit's share of dw and db
     int64_t units;
+    float *sums;     // backward pass of long rows: each row's two means
 };
 
 // What a thread holds of a row, as loaded: N chunks of V elements, chunk i at
@@ -186,13 +203,11 @@ __global__ __launch_bounds__(group(T)) void norm_kernel(NormArgs p) {
     next.load(p.x, unit * p.x_stride, p.width);
     if constexpr (HOLD) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int64_t c = min(H::column(i) + j, p.width - 1);
-                w[i][j] = load_w(p.weight, p.w_f32, c, 1.0f);
-                b[i][j] = load_w(p.bias, p.w_f32, c, 0.0f);
-            }
+        for (int i = 0; i < N; ++i) {
+            const int64_t c = min(H::column(i), p.width - V);
+            load_w<V>(p.weight, p.w_f32, c, 1.0f, w[i]);
+            load_w<V>(p.bias, p.w_f32, c, 0.0f, b[i]);
+        }
     }
     for (int64_t r = unit; r < p.rows; r += p.units) {
         if constexpr (!HOLD) asm volatile("" ::: "memory");  // the weights' loads stay in the loop
@@ -224,12 +239,14 @@ __global__ __launch_bounds__(group(T)) void norm_kernel(NormArgs p) {
             const int64_t c = H::column(i);
             if (c >= p.width) continue;
             float y[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float wj = HOLD ? w[HOLD ? i : 0][j] : load_w(p.weight, p.w_f32, c + j, 1.0f);
-                const float bj = HOLD ? b[HOLD ? i : 0][j] : load_w(p.bias, p.w_f32, c + j, 0.0f);
-                y[j] = __builtin_fmaf((x.at(i, j) - mean) * rstd, wj, bj);
+            constexpr int one = HOLD ? 1 : 0;
+            if constexpr (!HOLD) {
+                load_w<V>(p.weight, p.w_f32, c, 1.0f, w[0]);
+                load_w<V>(p.bias, p.w_f32, c, 0.0f, b[0]);
             }
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                y[j] = __builtin_fmaf((x.at(i, j) - mean) * rstd, w[one * i][j], b[one * i][j]);
             store_v<F32, V>(p.y, r * p.y_stride + c, y);
         }
     }
@@ -244,7 +261,7 @@ __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
     __shared__ float lds[T > kWave ? 2 * 2 * (T / kWave) : 1];
     int turn = 0;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kUnits + (kUnits > 1 ? wave_in_block() : 0);
-    if (kUnits > 1 && unit >= p.units) return;
+    const int64_t walk = static_cast<int64_t>(gridDim.x) * kUnits;  // rows from one of the unit's to the next
     const float inv = 1.0f / static_cast<float>(p.width);
     float w[N][V], dw[N][V], db[N][V];
     H x, dy, next_x, next_dy;
@@ -254,18 +271,17 @@ __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
         next_dy.load(p.dy, r * p.dy_stride, p.width);
         next_mean = p.mean[r], next_rstd = p.rstd[r];
     };
-    if constexpr (AHEAD) fetch(unit);
+    if (AHEAD && unit < p.rows) fetch(unit);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
+        load_w<V>(p.weight, p.w_f32, min(H::column(i), p.width - V), 1.0f, w[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            w[i][j] = load_w(p.weight, p.w_f32, min(H::column(i) + j, p.width - 1), 1.0f);
-            dw[i][j] = db[i][j] = 0.0f;
-        }
-    for (int64_t r = unit; r < p.rows; r += p.units) {
+        for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = 0.0f;
+    }
+    for (int64_t r = unit; r < p.rows; r += walk) {
         if constexpr (!AHEAD) fetch(r);
         x = next_x, dy = next_dy, mean = next_mean, rstd = next_rstd;
-        if (AHEAD && r + p.units < p.rows) fetch(r + p.units);
+        if (AHEAD && r + walk < p.rows) fetch(r + walk);
         // columns past the width have dy = 0: they add nothing (x = 0 there, so xh is finite as mean and rstd are)
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -294,7 +310,29 @@ __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
             store_v<F32, V>(p.y, r * p.y_stride + c, dx);
         }
     }
-    float *mine = p.partial + unit * 2 * p.width;
+    if constexpr (kUnits > 1) {  // the waves' shares, in wave order, are the workgroup's
+        __shared__ float share[kUnits][2][N * V][T];
+        const int w_in = wave_in_block(), lane = threadIdx.x % T;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                share[w_in][0][i * V + j][lane] = dw[i][j];
+                share[w_in][1][i * V + j][lane] = db[i][j];
+            }
+        __syncthreads();
+        if (w_in != 0) return;
+#pragma unroll
+        for (int u = 1; u < kUnits; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    dw[i][j] += share[u][0][i * V + j][lane];
+                    db[i][j] += share[u][1][i * V + j][lane];
+                }
+    }
+    float *mine = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.width;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int64_t c = H::column(i);
@@ -342,73 +380,101 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs p) {
             p.rstd[r] = rstd;
         }
         for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
+            float w[V], b[V];
             load_v<F32, V>(p.x, x0 + c, v);
+            load_w<V>(p.weight, p.w_f32, c, 1.0f, w);
+            load_w<V>(p.bias, p.w_f32, c, 0.0f, b);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[j] = __builtin_fmaf((v[j] - mean) * rstd, load_w(p.weight, p.w_f32, c + j, 1.0f),
-                                      load_w(p.bias, p.w_f32, c + j, 0.0f));
+            for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[j], b[j]);
             store_v<F32, V>(p.y, y0 + c, v);
         }
     }
 }
 
+// The backward pass of long rows, in two kernels: first each row's two sums,
+// then, by columns, what needs them.
 template <bool F32, int V>
-__global__ __launch_bounds__(kLong) void norm_grad_long_kernel(NormArgs p) {
+__global__ __launch_bounds__(kLong) void norm_grad_sums_kernel(NormArgs p) {
     __shared__ float lds[2 * 2 * (kLong / kWave)];
     int turn = 0;
     const float inv = 1.0f / static_cast<float>(p.width);
-    float *mine = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.width;
-    for (int64_t r = blockIdx.x; r < p.rows; r += p.units) {
-        const int64_t x0 = r * p.x_stride, d0 = r * p.dy_stride, y0 = r * p.y_stride;
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const float mean = p.mean[r], rstd = p.rstd[r];
-        const bool first = r == static_cast<int64_t>(blockIdx.x);
-        float s[2] = {0.0f, 0.0f}, x[V], dy[V];
+        float s[2] = {0.0f, 0.0f}, x[V], dy[V], w[V];
         for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
-            load_v<F32, V>(p.x, x0 + c, x);
-            load_v<F32, V>(p.dy, d0 + c, dy);
+            load_v<F32, V>(p.x, r * p.x_stride + c, x);
+            load_v<F32, V>(p.dy, r * p.dy_stride + c, dy);
+            load_w<V>(p.weight, p.w_f32, c, 1.0f, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                x[j] = (x[j] - mean) * rstd;
-                // a thread's columns of the unit's shares are its own
-                mine[c + j] = __builtin_fmaf(dy[j], x[j], first ? 0.0f : mine[c + j]);
-                mine[p.width + c + j] = dy[j] + (first ? 0.0f : mine[p.width + c + j]);
-                dy[j] *= load_w(p.weight, p.w_f32, c + j, 1.0f);
-                s[0] += dy[j];
-                s[1] = __builtin_fmaf(dy[j], x[j], s[1]);
+                const float g = dy[j] * w[j];
+                s[0] += g;
+                s[1] = __builtin_fmaf(g, (x[j] - mean) * rstd, s[1]);
             }
         }
         unit_sum<kLong>(s, lds, turn);
-        const float m0 = s[0] * inv, m1 = s[1] * inv;
-        for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
-            load_v<F32, V>(p.x, x0 + c, x);
-            load_v<F32, V>(p.dy, d0 + c, dy);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                dy[j] *= load_w(p.weight, p.w_f32, c + j, 1.0f);
-                x[j] = (dy[j] - m0 - (x[j] - mean) * rstd * m1) * rstd;
-            }
-            store_v<F32, V>(p.y, y0 + c, x);
+        if (threadIdx.x == 0) {
+            p.sums[2 * r] = s[0] * inv;
+            p.sums[2 * r + 1] = s[1] * inv;
         }
     }
 }
 
-// dw and db from the units' shares: a workgroup has 32 columns and 8 runs of
+// A workgroup has 256 V columns of every p.units-th row; its share of dw and db
+// is those rows'.
+template <bool F32, int V>
+__global__ __launch_bounds__(256) void norm_grad_columns_kernel(NormArgs p) {
+    const int64_t strips = (p.width + 256 * V - 1) / (256 * V);
+    const int64_t unit = blockIdx.x / strips, c = ((blockIdx.x % strips) * 256 + threadIdx.x) * V;
+    if (c >= p.width) return;
+    float w[V], dw[V], db[V];
+    load_w<V>(p.weight, p.w_f32, c, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.0f;
+#pragma unroll 4
+    for (int64_t r = unit; r < p.rows; r += p.units) {
+        const float mean = p.mean[r], rstd = p.rstd[r], m0 = p.sums[2 * r], m1 = p.sums[2 * r + 1];
+        float x[V], dy[V];
+        load_v<F32, V>(p.x, r * p.x_stride + c, x);
+        load_v<F32, V>(p.dy, r * p.dy_stride + c, dy);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = (x[j] - mean) * rstd;
+            dw[j] = __builtin_fmaf(dy[j], xh, dw[j]);
+            db[j] += dy[j];
+            x[j] = (dy[j] * w[j] - m0 - xh * m1) * rstd;
+        }
+        store_v<F32, V>(p.y, r * p.y_stride + c, x);
+    }
+    float *mine = p.partial + unit * 2 * p.width + c;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        mine[j] = dw[j];
+        mine[p.width + j] = db[j];
+    }
+}
+
+// dw and db from the units' shares: a workgroup has 32 columns and 32 runs of
 // units, each summed in order, then the runs in order.
-__global__ __launch_bounds__(kBlockThreads) void norm_join_kernel(const float *__restrict__ partial, int64_t units,
-                                                                  int64_t width, void *dw, void *db, bool w_f32) {
-    __shared__ float lds[8][32];
+constexpr int kRuns = 32;
+
+__global__ __launch_bounds__(32 * kRuns) void norm_join_kernel(const float *__restrict__ partial, int64_t units,
+                                                               int64_t width, void *dw, void *db, bool w_f32) {
+    __shared__ float lds[kRuns][33];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // over dw's columns, then db's
-    const int64_t per = (units + 7) / 8;
+    const int64_t per = (units + kRuns - 1) / kRuns, u1 = min(units, (run + 1) * per);
     float s = 0.0f;
-    if (i < 2 * width)
-        for (int64_t u = run * per; u < min(units, (run + 1) * per); ++u) s += partial[u * 2 * width + i];
+    if (i < 2 * width) {
+#pragma unroll 8
+        for (int64_t u = run * per; u < u1; ++u) s += partial[u * 2 * width + i];
+    }
     lds[run][lane] = s;
     __syncthreads();
     if (run != 0 || i >= 2 * width) return;
     s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += lds[k][lane];
+    for (int k = 0; k < kRuns; ++k) s += lds[k][lane];
     void *o = i < width ? dw : db;
     const int64_t c = i < width ? i : i - width;
     if (!o) return;
@@ -420,13 +486,15 @@ __global__ __launch_bounds__(kBlockThreads) void norm_join_kernel(const float *_
 
 constexpr int64_t kMaxHeld = 32768, kMaxGradHeld = 16384;  // widest rows in registers
 
-// Units of the backward pass: two workgroups a CU, so that one's loads run
-// under the other's sums; every unit more is two rows of binary32 sums to write
-// and read again.
+// Shares of the backward pass (workgroups): as many as a CU holds, so that one's
+// loads run under another's sums, but 16 rows a share as long as that leaves
+// every CU one, because a share is two rows of binary32 sums to write and to
+// read again.
 int64_t grad_units(int64_t rows, int64_t width) {
-    if (width > kMaxGradHeld) return std::min<int64_t>(rows, 256);
-    if (width <= 512) return std::min<int64_t>(rows, 2048);
-    return std::min<int64_t>(rows, 512);
+    if (width > kMaxGradHeld) return std::min<int64_t>((rows + 15) / 16, 128);
+    const int64_t most = width <= 2048 ? 2048 : width <= 4096 ? 768 : width <= 8192 ? 512 : 256;
+    const int64_t of = width <= 512 ? 4 : 1;  // rows a workgroup has at a time
+    return std::min({(rows + of - 1) / of, most, std::max<int64_t>(rows / 16, 256)});
 }
 
 // Threads of a unit and elements a thread holds: as few as hold the row.
@@ -457,7 +525,7 @@ hipError_t launch_norm_grad(const NormArgs &p, hipStream_t stream) {
     const int64_t h = p.width;
     const unsigned n = static_cast<unsigned>(p.units);
     if (h <= 512)
-        norm_grad_kernel<F32, V, 64, 8 / V, true><<<(n + 3) / 4, 256, 0, stream>>>(p);
+        norm_grad_kernel<F32, V, 64, 8 / V, true><<<n, 256, 0, stream>>>(p);
     else if (h <= 2048)
         norm_grad_kernel<F32, V, 256, 8 / V, true><<<n, 256, 0, stream>>>(p);
     else if (h <= 4096)
@@ -474,12 +542,16 @@ template <bool F32, int V>
 hipError_t launch_norm_any(NormArgs p, bool grad, hipStream_t stream) {
     if (p.width <= (grad ? kMaxGradHeld : kMaxHeld))
         return grad ? launch_norm_grad<F32, V>(p, stream) : launch_norm<F32, V>(p, stream);
-    if (!grad) p.units = std::min<int64_t>(p.rows, 512);
-    const unsigned n = static_cast<unsigned>(p.units);
-    if (grad)
-        norm_grad_long_kernel<F32, V><<<n, kLong, 0, stream>>>(p);
-    else
+    const unsigned n = static_cast<unsigned>(std::min<int64_t>(p.rows, 512));
+    if (!grad) {
+        p.units = n;
         norm_long_kernel<F32, V><<<n, kLong, 0, stream>>>(p);
+        return hipGetLastError();
+    }
+    norm_grad_sums_kernel<F32, V><<<n, kLong, 0, stream>>>(p);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const int64_t strips = (p.width + 256 * V - 1) / (256 * V);
+    norm_grad_columns_kernel<F32, V><<<static_cast<unsigned>(strips * p.units), 256, 0, stream>>>(p);
     return hipGetLastError();
 }
 
@@ -502,7 +574,10 @@ hipError_t launch_layer_norm(const void *x, bool f32, int64_t x_stride, int64_t 
     return launch_norm_typed(p, false, f32, stream);
 }
 
-int64_t layer_norm_grad_workspace(int64_t rows, int64_t width) { return grad_units(rows, width) * 2 * width * 4; }
+// The shares and, for long rows, the rows' sums after them.
+int64_t layer_norm_grad_workspace(int64_t rows, int64_t width) {
+    return (grad_units(rows, width) * 2 * width + (width > kMaxGradHeld ? 2 * rows : 0)) * 4;
+}
 
 hipError_t launch_layer_norm_grad(const void *dy, int64_t dy_stride, const void *x, bool f32, int64_t x_stride,
                                   int64_t rows, int64_t width, const void *weight, bool w_f32, const float *mean,
@@ -515,12 +590,13 @@ hipError_t launch_layer_norm_grad(const void *dy, int64_t dy_stride, const void 
     p.mean = const_cast<float *>(mean), p.rstd = const_cast<float *>(rstd);
     p.partial = static_cast<float *>(workspace);
     p.units = grad_units(rows, width);
+    p.sums = p.partial + p.units * 2 * width;
     if (rows > 0) {
         if (const hipError_t e = launch_norm_typed(p, true, f32, stream); e != hipSuccess) return e;
     }
     if (!dweight && !dbias) return hipSuccess;
     // no rows, no units: the sums are zero
-    norm_join_kernel<<<static_cast<unsigned>((2 * width + 31) / 32), kBlockThreads, 0, stream>>>(
+    norm_join_kernel<<<static_cast<unsigned>((2 * width + 31) / 32), 32 * kRuns, 0, stream>>>(
         p.partial, p.units, width, dweight, dbias, w_f32);
     return hipGetLastError();
 }
