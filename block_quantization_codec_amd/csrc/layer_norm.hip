@@ -13,13 +13,11 @@
 // nothing is read twice; the next row is on its way meanwhile. Units walk over the rows, keeping the weights,
 // and in the backward pass their share of dw and db, in registers; the units'
 // shares go to the workspace and a second kernel sums them in unit order, so
-// the result does not change from run to run. Rows wider than 32,768 elements
-// (16,384 backward) are read again for each sum instead, and the backward pass
+// the result does not change from run to run. Rows wider than 16,384 elements
+// (32,768 of whole bf16 pieces, forward) are read again for each sum instead, and the backward pass
 // takes two kernels, one along the rows and one down the columns.
 //
-// All sums are binary32. Rows whose elements lie on 16-byte pieces move as
-// such (V elements each); any others element by element, still contiguous
-// across the wave.
+// All sums are binary32.
 #include <algorithm>
 
 #include "zpp_device.h"
@@ -71,64 +69,115 @@ __device__ __forceinline__ void unit_sum(float (&v)[N], float *lds, int &turn) {
     }
 }
 
-// V elements at p, widened.
-template <bool F32, int V>
-__device__ __forceinline__ void load_v(const void *base, int64_t e, float *f) {
-    if constexpr (F32) {
-        if constexpr (V == 4) {
-            const f32x4 v = ld<f32x4>(static_cast<const float *>(base) + e);
+// Rows whose elements lie on 16-byte pieces are WHOLE: every V elements of a row
+// are one aligned access. Other rows are read and written in the same pieces,
+// at the addresses they have, but for a last one that would pass the row's end,
+// which goes element by element.
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));  // 16 bytes at any element of either type
+
+// V elements from element e on, packed; `left` (> 0) are in the row.
+template <bool F32, int V, bool WHOLE>
+__device__ __forceinline__ void load_packed(const void *base, int64_t e, int64_t left, uint32_t *w) {
+    static_assert(V == (F32 ? 4 : 8), "16 bytes");
+    if (WHOLE || left >= V) {
+        const uint8_t *p = static_cast<const uint8_t *>(base) + e * (F32 ? 4 : 2);
+        const u32x4 v = WHOLE ? *reinterpret_cast<const u32x4 *>(p) : *reinterpret_cast<const u32x4_at2 *>(p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = v[i];
-        } else {
-            f[0] = static_cast<const float *>(base)[e];
-        }
+        for (int j = 0; j < 4; ++j) w[j] = v[j];
     } else {
-        if constexpr (V == 8) {
-            const u32x4 v = ld<u32x4>(static_cast<const uint16_t *>(base) + e);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(v[i]), f[2 * i + 1] = bf16_hi(v[i]);
-        } else {
-            f[0] = bf16_lo(static_cast<const uint16_t *>(base)[e]);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (F32) {
+                w[j] = j < left ? static_cast<const uint32_t *>(base)[e + j] : 0u;
+            } else {
+                const uint16_t *p = static_cast<const uint16_t *>(base) + e;
+                w[j] = (2 * j < left ? p[2 * j] : 0u) | (2 * j + 1 < left ? static_cast<uint32_t>(p[2 * j + 1]) << 16 : 0u);
+            }
         }
     }
 }
 
-template <bool F32, int V>
-__device__ __forceinline__ void store_v(void *base, int64_t e, const float *f) {
-    if constexpr (F32) {
-        if constexpr (V == 4)
-            st_out<f32x4>(static_cast<float *>(base) + e, f32x4{f[0], f[1], f[2], f[3]});
+template <bool F32>
+__device__ __forceinline__ float unpack(const uint32_t *w, int j) {
+    if constexpr (F32)
+        return as_f(w[j]);
+    else
+        return j % 2 == 0 ? bf16_lo(w[j / 2]) : bf16_hi(w[j / 2]);
+}
+
+template <bool F32, int V, bool WHOLE>
+__device__ __forceinline__ void load_v(const void *base, int64_t e, int64_t left, float (&f)[V]) {
+    uint32_t w[4];
+    load_packed<F32, V, WHOLE>(base, e, left, w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = unpack<F32>(w, j);
+}
+
+template <bool F32, int V, bool WHOLE>
+__device__ __forceinline__ void store_v(void *base, int64_t e, int64_t left, const float (&f)[V]) {
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = F32 ? as_u(f[F32 ? j : 0]) : pack_bf16x2(f[F32 ? 0 : 2 * j], f[F32 ? 0 : 2 * j + 1]);
+    if (WHOLE || left >= V) {
+        uint8_t *p = static_cast<uint8_t *>(base) + e * (F32 ? 4 : 2);
+        if constexpr (WHOLE)
+            st_out<u32x4>(p, v);
         else
-            st_out<float>(static_cast<float *>(base) + e, f[0]);
+            *reinterpret_cast<u32x4_at2 *>(p) = v;
     } else {
-        if constexpr (V == 8)
-            st_out<u32x4>(static_cast<uint16_t *>(base) + e,
-                          u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                pack_bf16x2(f[6], f[7])});
-        else
-            st_out<uint16_t>(static_cast<uint16_t *>(base) + e, static_cast<uint16_t>(pack_bf16x2(f[0], 0.0f)));
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (j >= left) break;
+            if constexpr (F32)
+                static_cast<uint32_t *>(base)[e + j] = v[j];
+            else
+                static_cast<uint16_t *>(base)[e + j] = static_cast<uint16_t>(v[j / 2] >> (16 * (j % 2)));
+        }
     }
 }
 
 // V elements of a weight vector of either type from column c on (a multiple of
-// V within the width); a missing vector's are `none`.
-template <int V>
-__device__ __forceinline__ void load_w(const void *w, bool f32, int64_t c, float none, float (&o)[V]) {
+// V below the width); a missing vector's are `none`.
+template <int V, bool WHOLE>
+__device__ __forceinline__ void load_w(const void *w, bool f32, int64_t c, int64_t width, float none, float (&o)[V]) {
     if (!w) {
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = none;
-    } else if (f32) {
-        if constexpr (V == 1) {
-            o[0] = static_cast<const float *>(w)[c];
-        } else {
+    } else if (!WHOLE && c + V > width) {
 #pragma unroll
-            for (int j = 0; j < V; j += 4) load_v<true, 4>(w, c + j, o + j);
+        for (int j = 0; j < V; ++j) {
+            o[j] = 0.0f;
+            if (c + j < width)
+                o[j] = f32 ? static_cast<const float *>(w)[c + j] : bf16_lo(static_cast<const uint16_t *>(w)[c + j]);
         }
-    } else if constexpr (V == 4) {
-        const u32x2 v = ld<u32x2>(static_cast<const uint16_t *>(w) + c);
-        o[0] = bf16_lo(v[0]), o[1] = bf16_hi(v[0]), o[2] = bf16_lo(v[1]), o[3] = bf16_hi(v[1]);
+    } else if (f32) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const f32x4 v = ld<f32x4>(static_cast<const float *>(w) + c + j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[j + k] = v[k];
+        }
     } else {
-        load_v<false, V>(w, c, o);
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const u32x2 v = ld<u32x2>(static_cast<const uint16_t *>(w) + c + j);
+            o[j] = bf16_lo(v[0]), o[j + 1] = bf16_hi(v[0]), o[j + 2] = bf16_lo(v[1]), o[j + 3] = bf16_hi(v[1]);
+        }
+    }
+}
+
+// V of a share's sums, of which `left` are in the row.
+template <int V, bool WHOLE>
+__device__ __forceinline__ void store_share(float *o, int64_t left, const float (&v)[V]) {
+    if (WHOLE || left >= V) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4)
+            *reinterpret_cast<f32x4_at4 *>(o + j) = f32x4{v[j], v[j + 1], v[j + 2], v[j + 3]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < left) o[j] = v[j];
     }
 }
 
@@ -151,13 +200,18 @@ struct NormArgs {
 
 // What a thread holds of a row, as loaded: N chunks of V elements, chunk i at
 // column (i T + thread) V. Rows are loaded one ahead, so they stay packed.
-template <bool F32, int V, int T, int N>
+template <bool F32, bool WHOLE, int T, int N>
 struct Held {
-    static constexpr int kW = F32 ? V : (V + 1) / 2;  // dwords of a chunk
-    uint32_t w[N][kW];
+    static constexpr int V = F32 ? 4 : 8;
+    uint32_t w[N][4];
 
     static __device__ __forceinline__ int64_t column(int i) {
         return (static_cast<int64_t>(i) * T + threadIdx.x % T) * V;
+    }
+
+    // Whether element j of chunk i is in the row.
+    static __device__ __forceinline__ bool in(int i, int j, int64_t width) {
+        return column(i) + (WHOLE ? 0 : j) < width;
     }
 
     // Columns past the width are zeros.
@@ -166,32 +220,21 @@ struct Held {
         for (int i = 0; i < N; ++i) {
             const int64_t c = column(i);
 #pragma unroll
-            for (int j = 0; j < kW; ++j) w[i][j] = 0;
-            if (c >= width) continue;
-            if constexpr (V == 1) {
-                w[i][0] = F32 ? static_cast<const uint32_t *>(base)[e + c] : static_cast<const uint16_t *>(base)[e + c];
-            } else {
-                const u32x4 v = ld<u32x4>(static_cast<const uint8_t *>(base) + (e + c) * (F32 ? 4 : 2));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[i][j] = v[j];
-            }
+            for (int j = 0; j < 4; ++j) w[i][j] = 0;
+            if (c < width) load_packed<F32, V, WHOLE>(base, e + c, width - c, w[i]);
         }
     }
 
-    __device__ __forceinline__ float at(int i, int j) const {
-        if constexpr (F32)
-            return as_f(w[i][j]);
-        else
-            return V == 1 || j % 2 == 0 ? bf16_lo(w[i][j / 2]) : bf16_hi(w[i][j / 2]);
-    }
+    __device__ __forceinline__ float at(int i, int j) const { return unpack<F32>(w[i], j); }
 };
 
 constexpr int group(int T) { return T < 256 ? 256 : T; }  // threads of a workgroup
 
 // HOLD: the weights stay in registers over the rows (else they are read again for each).
-template <bool F32, int V, int T, int N, bool HOLD>
+template <bool F32, bool WHOLE, int T, int N, bool HOLD>
 __global__ __launch_bounds__(group(T)) void norm_kernel(NormArgs p) {
-    using H = Held<F32, V, T, N>;
+    using H = Held<F32, WHOLE, T, N>;
+    constexpr int V = H::V;
     constexpr int kUnits = group(T) / T;
     __shared__ float lds[T > kWave ? 2 * (T / kWave) : 1];
     int turn = 0;
@@ -204,9 +247,9 @@ __global__ __launch_bounds__(group(T)) void norm_kernel(NormArgs p) {
     if constexpr (HOLD) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int64_t c = min(H::column(i), p.width - V);
-            load_w<V>(p.weight, p.w_f32, c, 1.0f, w[i]);
-            load_w<V>(p.bias, p.w_f32, c, 0.0f, b[i]);
+            const int64_t c = H::column(i) < p.width ? H::column(i) : 0;
+            load_w<V, WHOLE>(p.weight, p.w_f32, c, p.width, 1.0f, w[i]);
+            load_w<V, WHOLE>(p.bias, p.w_f32, c, p.width, 0.0f, b[i]);
         }
     }
     for (int64_t r = unit; r < p.rows; r += p.units) {
@@ -225,7 +268,7 @@ __global__ __launch_bounds__(group(T)) void norm_kernel(NormArgs p) {
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float d = H::column(i) < p.width ? x.at(i, j) - mean : 0.0f;
+                const float d = H::in(i, j, p.width) ? x.at(i, j) - mean : 0.0f;
                 s[0] = __builtin_fmaf(d, d, s[0]);
             }
         unit_sum<T>(s, lds, turn);
@@ -241,22 +284,23 @@ __global__ __launch_bounds__(group(T)) void norm_kernel(NormArgs p) {
             float y[V];
             constexpr int one = HOLD ? 1 : 0;
             if constexpr (!HOLD) {
-                load_w<V>(p.weight, p.w_f32, c, 1.0f, w[0]);
-                load_w<V>(p.bias, p.w_f32, c, 0.0f, b[0]);
+                load_w<V, WHOLE>(p.weight, p.w_f32, c, p.width, 1.0f, w[0]);
+                load_w<V, WHOLE>(p.bias, p.w_f32, c, p.width, 0.0f, b[0]);
             }
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 y[j] = __builtin_fmaf((x.at(i, j) - mean) * rstd, w[one * i][j], b[one * i][j]);
-            store_v<F32, V>(p.y, r * p.y_stride + c, y);
+            store_v<F32, V, WHOLE>(p.y, r * p.y_stride + c, p.width - c, y);
         }
     }
 }
 
 // AHEAD: the next row's loads are made before this row's sums; a workgroup of
 // 16 waves has too few registers a lane for that.
-template <bool F32, int V, int T, int N, bool AHEAD>
+template <bool F32, bool WHOLE, int T, int N, bool AHEAD>
 __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
-    using H = Held<F32, V, T, N>;
+    using H = Held<F32, WHOLE, T, N>;
+    constexpr int V = H::V;
     constexpr int kUnits = group(T) / T;
     __shared__ float lds[T > kWave ? 2 * 2 * (T / kWave) : 1];
     int turn = 0;
@@ -274,7 +318,7 @@ __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
     if (AHEAD && unit < p.rows) fetch(unit);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        load_w<V>(p.weight, p.w_f32, min(H::column(i), p.width - V), 1.0f, w[i]);
+        load_w<V, WHOLE>(p.weight, p.w_f32, H::column(i) < p.width ? H::column(i) : 0, p.width, 1.0f, w[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = 0.0f;
     }
@@ -292,7 +336,7 @@ __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
                 dw[i][j] = __builtin_fmaf(d, xh, dw[i][j]);
                 db[i][j] += d;
                 s[0] += g;
-                s[1] = __builtin_fmaf(g, H::column(i) < p.width ? xh : 0.0f, s[1]);
+                s[1] = __builtin_fmaf(g, H::in(i, j, p.width) ? xh : 0.0f, s[1]);
             }
         }
         unit_sum<T>(s, lds, turn);
@@ -307,7 +351,7 @@ __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
                 const float xh = (x.at(i, j) - mean) * rstd;
                 dx[j] = (dy.at(i, j) * w[i][j] - m0 - xh * m1) * rstd;
             }
-            store_v<F32, V>(p.y, r * p.y_stride + c, dx);
+            store_v<F32, V, WHOLE>(p.y, r * p.y_stride + c, p.width - c, dx);
         }
     }
     if constexpr (kUnits > 1) {  // the waves' shares, in wave order, are the workgroup's
@@ -337,23 +381,16 @@ __global__ __launch_bounds__(group(T)) void norm_grad_kernel(NormArgs p) {
     for (int i = 0; i < N; ++i) {
         const int64_t c = H::column(i);
         if (c >= p.width) continue;
-        if constexpr (V > 1) {  // the width is a multiple of V, so both shares are 16-byte aligned
-#pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                st<f32x4>(mine + c + j, f32x4{dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]});
-                st<f32x4>(mine + p.width + c + j, f32x4{db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]});
-            }
-        } else {
-            mine[c] = dw[i][0];
-            mine[p.width + c] = db[i][0];
-        }
+        store_share<V, WHOLE>(mine + c, p.width - c, dw[i]);
+        store_share<V, WHOLE>(mine + p.width + c, p.width - c, db[i]);
     }
 }
 
 constexpr int kLong = 1024;  // threads of a unit for rows beyond the registers
 
-template <bool F32, int V>
+template <bool F32, bool WHOLE>
 __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs p) {
+    constexpr int V = F32 ? 4 : 8;
     __shared__ float lds[2 * (kLong / kWave)];
     int turn = 0;
     const float inv = 1.0f / static_cast<float>(p.width);
@@ -361,7 +398,7 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs p) {
         const int64_t x0 = r * p.x_stride, y0 = r * p.y_stride;
         float s[1] = {0.0f}, v[V];
         for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
-            load_v<F32, V>(p.x, x0 + c, v);
+            load_v<F32, V, WHOLE>(p.x, x0 + c, p.width - c, v);
 #pragma unroll
             for (int j = 0; j < V; ++j) s[0] += v[j];
         }
@@ -369,9 +406,12 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs p) {
         const float mean = s[0] * inv;
         s[0] = 0.0f;
         for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
-            load_v<F32, V>(p.x, x0 + c, v);
+            load_v<F32, V, WHOLE>(p.x, x0 + c, p.width - c, v);
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[0] = __builtin_fmaf(v[j] - mean, v[j] - mean, s[0]);
+            for (int j = 0; j < V; ++j) {
+                const float d = WHOLE || c + j < p.width ? v[j] - mean : 0.0f;
+                s[0] = __builtin_fmaf(d, d, s[0]);
+            }
         }
         unit_sum<kLong>(s, lds, turn);
         const float rstd = 1.0f / __builtin_sqrtf(s[0] * inv + p.eps);
@@ -381,20 +421,21 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs p) {
         }
         for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
             float w[V], b[V];
-            load_v<F32, V>(p.x, x0 + c, v);
-            load_w<V>(p.weight, p.w_f32, c, 1.0f, w);
-            load_w<V>(p.bias, p.w_f32, c, 0.0f, b);
+            load_v<F32, V, WHOLE>(p.x, x0 + c, p.width - c, v);
+            load_w<V, WHOLE>(p.weight, p.w_f32, c, p.width, 1.0f, w);
+            load_w<V, WHOLE>(p.bias, p.w_f32, c, p.width, 0.0f, b);
 #pragma unroll
             for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[j], b[j]);
-            store_v<F32, V>(p.y, y0 + c, v);
+            store_v<F32, V, WHOLE>(p.y, y0 + c, p.width - c, v);
         }
     }
 }
 
 // The backward pass of long rows, in two kernels: first each row's two sums,
 // then, by columns, what needs them.
-template <bool F32, int V>
+template <bool F32, bool WHOLE>
 __global__ __launch_bounds__(kLong) void norm_grad_sums_kernel(NormArgs p) {
+    constexpr int V = F32 ? 4 : 8;
     __shared__ float lds[2 * 2 * (kLong / kWave)];
     int turn = 0;
     const float inv = 1.0f / static_cast<float>(p.width);
@@ -402,14 +443,14 @@ __global__ __launch_bounds__(kLong) void norm_grad_sums_kernel(NormArgs p) {
         const float mean = p.mean[r], rstd = p.rstd[r];
         float s[2] = {0.0f, 0.0f}, x[V], dy[V], w[V];
         for (int64_t c = threadIdx.x * V; c < p.width; c += kLong * V) {
-            load_v<F32, V>(p.x, r * p.x_stride + c, x);
-            load_v<F32, V>(p.dy, r * p.dy_stride + c, dy);
-            load_w<V>(p.weight, p.w_f32, c, 1.0f, w);
+            load_v<F32, V, WHOLE>(p.x, r * p.x_stride + c, p.width - c, x);
+            load_v<F32, V, WHOLE>(p.dy, r * p.dy_stride + c, p.width - c, dy);
+            load_w<V, WHOLE>(p.weight, p.w_f32, c, p.width, 1.0f, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float g = dy[j] * w[j];
                 s[0] += g;
-                s[1] = __builtin_fmaf(g, (x[j] - mean) * rstd, s[1]);
+                s[1] = __builtin_fmaf(g, WHOLE || c + j < p.width ? (x[j] - mean) * rstd : 0.0f, s[1]);
             }
         }
         unit_sum<kLong>(s, lds, turn);
@@ -422,21 +463,22 @@ __global__ __launch_bounds__(kLong) void norm_grad_sums_kernel(NormArgs p) {
 
 // A workgroup has 256 V columns of every p.units-th row; its share of dw and db
 // is those rows'.
-template <bool F32, int V>
+template <bool F32, bool WHOLE>
 __global__ __launch_bounds__(256) void norm_grad_columns_kernel(NormArgs p) {
+    constexpr int V = F32 ? 4 : 8;
     const int64_t strips = (p.width + 256 * V - 1) / (256 * V);
     const int64_t unit = blockIdx.x / strips, c = ((blockIdx.x % strips) * 256 + threadIdx.x) * V;
     if (c >= p.width) return;
     float w[V], dw[V], db[V];
-    load_w<V>(p.weight, p.w_f32, c, 1.0f, w);
+    load_w<V, WHOLE>(p.weight, p.w_f32, c, p.width, 1.0f, w);
 #pragma unroll
     for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.0f;
 #pragma unroll 4
     for (int64_t r = unit; r < p.rows; r += p.units) {
         const float mean = p.mean[r], rstd = p.rstd[r], m0 = p.sums[2 * r], m1 = p.sums[2 * r + 1];
         float x[V], dy[V];
-        load_v<F32, V>(p.x, r * p.x_stride + c, x);
-        load_v<F32, V>(p.dy, r * p.dy_stride + c, dy);
+        load_v<F32, V, WHOLE>(p.x, r * p.x_stride + c, p.width - c, x);
+        load_v<F32, V, WHOLE>(p.dy, r * p.dy_stride + c, p.width - c, dy);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float xh = (x[j] - mean) * rstd;
@@ -444,14 +486,11 @@ __global__ __launch_bounds__(256) void norm_grad_columns_kernel(NormArgs p) {
             db[j] += dy[j];
             x[j] = (dy[j] * w[j] - m0 - xh * m1) * rstd;
         }
-        store_v<F32, V>(p.y, r * p.y_stride + c, x);
+        store_v<F32, V, WHOLE>(p.y, r * p.y_stride + c, p.width - c, x);
     }
     float *mine = p.partial + unit * 2 * p.width + c;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        mine[j] = dw[j];
-        mine[p.width + j] = db[j];
-    }
+    store_share<V, WHOLE>(mine, p.width - c, dw);
+    store_share<V, WHOLE>(mine + p.width, p.width - c, db);
 }
 
 // dw and db from the units' shares: a workgroup has 32 columns and 32 runs of
@@ -484,7 +523,10 @@ __global__ __launch_bounds__(32 * kRuns) void norm_join_kernel(const float *__re
         static_cast<uint16_t *>(o)[c] = static_cast<uint16_t>(pack_bf16x2(s, 0.0f));
 }
 
-constexpr int64_t kMaxHeld = 32768, kMaxGradHeld = 16384;  // widest rows in registers
+constexpr int64_t kMaxGradHeld = 16384;  // widest rows in registers
+// Forward, twice that where the registers suffice.
+template <bool F32, bool WHOLE>
+constexpr int64_t kMaxHeld = !F32 && WHOLE ? 32768 : 16384;
 
 // Shares of the backward pass (workgroups): as many as a CU holds, so that one's
 // loads run under another's sums, but 16 rows a share as long as that leaves
@@ -498,68 +540,70 @@ int64_t grad_units(int64_t rows, int64_t width) {
 }
 
 // Threads of a unit and elements a thread holds: as few as hold the row.
-template <bool F32, int V>
+template <bool F32, bool WHOLE>
 hipError_t launch_norm(NormArgs p, hipStream_t stream) {
+    constexpr int V = F32 ? 4 : 8;
     const int64_t h = p.width;
     auto go = [&](auto kernel, int units_of_group, int threads, int64_t most) {
         p.units = std::min<int64_t>((p.rows + units_of_group - 1) / units_of_group, most / units_of_group) * units_of_group;
         kernel<<<static_cast<unsigned>(p.units / units_of_group), threads, 0, stream>>>(p);
     };
     if (h <= 512)
-        go(norm_kernel<F32, V, 64, 8 / V, true>, 4, 256, 8192);
+        go(norm_kernel<F32, WHOLE, 64, 8 / V, true>, 4, 256, 8192);
     else if (h <= 2048)
-        go(norm_kernel<F32, V, 256, 8 / V, true>, 1, 256, 2048);
+        go(norm_kernel<F32, WHOLE, 256, 8 / V, true>, 1, 256, 2048);
     else if (h <= 4096)
-        go(norm_kernel<F32, V, 256, 16 / V, true>, 1, 256, 2048);
+        go(norm_kernel<F32, WHOLE, 256, 16 / V, true>, 1, 256, 2048);
     else if (h <= 8192)
-        go(norm_kernel<F32, V, 256, 32 / V, true>, 1, 256, 1024);
+        go(norm_kernel<F32, WHOLE, 256, 32 / V, true>, 1, 256, 1024);
     else if (h <= 16384)
-        go(norm_kernel<F32, V, 1024, 16 / V, true>, 1, 1024, 512);
-    else
-        go(norm_kernel<F32, V, 1024, 32 / V, false>, 1, 1024, 512);
+        go(norm_kernel<F32, WHOLE, 1024, 16 / V, true>, 1, 1024, 512);
+    else if constexpr (kMaxHeld<F32, WHOLE> > 16384)
+        go(norm_kernel<F32, WHOLE, 1024, 32 / V, false>, 1, 1024, 512);
     return hipGetLastError();
 }
 
-template <bool F32, int V>
+template <bool F32, bool WHOLE>
 hipError_t launch_norm_grad(const NormArgs &p, hipStream_t stream) {
+    constexpr int V = F32 ? 4 : 8;
     const int64_t h = p.width;
     const unsigned n = static_cast<unsigned>(p.units);
     if (h <= 512)
-        norm_grad_kernel<F32, V, 64, 8 / V, true><<<n, 256, 0, stream>>>(p);
+        norm_grad_kernel<F32, WHOLE, 64, 8 / V, true><<<n, 256, 0, stream>>>(p);
     else if (h <= 2048)
-        norm_grad_kernel<F32, V, 256, 8 / V, true><<<n, 256, 0, stream>>>(p);
+        norm_grad_kernel<F32, WHOLE, 256, 8 / V, true><<<n, 256, 0, stream>>>(p);
     else if (h <= 4096)
-        norm_grad_kernel<F32, V, 256, 16 / V, true><<<n, 256, 0, stream>>>(p);
+        norm_grad_kernel<F32, WHOLE, 256, 16 / V, true><<<n, 256, 0, stream>>>(p);
     else if (h <= 8192)
-        norm_grad_kernel<F32, V, 512, 16 / V, true><<<n, 512, 0, stream>>>(p);
+        norm_grad_kernel<F32, WHOLE, 512, 16 / V, true><<<n, 512, 0, stream>>>(p);
     else
-        norm_grad_kernel<F32, V, 1024, 16 / V, false><<<n, 1024, 0, stream>>>(p);
+        norm_grad_kernel<F32, WHOLE, 1024, 16 / V, false><<<n, 1024, 0, stream>>>(p);
     return hipGetLastError();
 }
 
-// V elements of a row at a time where they lie on 16-byte pieces, one otherwise.
-template <bool F32, int V>
+template <bool F32, bool WHOLE>
 hipError_t launch_norm_any(NormArgs p, bool grad, hipStream_t stream) {
-    if (p.width <= (grad ? kMaxGradHeld : kMaxHeld))
-        return grad ? launch_norm_grad<F32, V>(p, stream) : launch_norm<F32, V>(p, stream);
+    if (p.width <= (grad ? kMaxGradHeld : kMaxHeld<F32, WHOLE>))
+        return grad ? launch_norm_grad<F32, WHOLE>(p, stream) : launch_norm<F32, WHOLE>(p, stream);
     const unsigned n = static_cast<unsigned>(std::min<int64_t>(p.rows, 512));
     if (!grad) {
         p.units = n;
-        norm_long_kernel<F32, V><<<n, kLong, 0, stream>>>(p);
+        norm_long_kernel<F32, WHOLE><<<n, kLong, 0, stream>>>(p);
         return hipGetLastError();
     }
-    norm_grad_sums_kernel<F32, V><<<n, kLong, 0, stream>>>(p);
+    norm_grad_sums_kernel<F32, WHOLE><<<n, kLong, 0, stream>>>(p);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    constexpr int V = F32 ? 4 : 8;
     const int64_t strips = (p.width + 256 * V - 1) / (256 * V);
-    norm_grad_columns_kernel<F32, V><<<static_cast<unsigned>(strips * p.units), 256, 0, stream>>>(p);
+    norm_grad_columns_kernel<F32, WHOLE><<<static_cast<unsigned>(strips * p.units), 256, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 hipError_t launch_norm_typed(const NormArgs &p, bool grad, bool f32, hipStream_t stream) {
     const int v = f32 ? 4 : 8;
-    const bool vec = p.width % v == 0 && p.x_stride % v == 0 && p.y_stride % v == 0 && p.dy_stride % v == 0;
-    if (f32) return vec ? launch_norm_any<true, 4>(p, grad, stream) : launch_norm_any<true, 1>(p, grad, stream);
-    return vec ? launch_norm_any<false, 8>(p, grad, stream) : launch_norm_any<false, 1>(p, grad, stream);
+    const bool whole = p.width % v == 0 && p.x_stride % v == 0 && p.y_stride % v == 0 && p.dy_stride % v == 0;
+    if (f32) return whole ? launch_norm_any<true, true>(p, grad, stream) : launch_norm_any<true, false>(p, grad, stream);
+    return whole ? launch_norm_any<false, true>(p, grad, stream) : launch_norm_any<false, false>(p, grad, stream);
 }
 
 }  // namespace
