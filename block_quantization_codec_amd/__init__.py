@@ -116,7 +116,8 @@ def _stream(stream):
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle, without the Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -357,20 +358,36 @@ def dequant_reduce_average(codes_in, scales_in, n_inputs: int, bits_in: int, num
     return avg
 
 
+_CODES: dict = {}  # torch dtype -> zpp_dtype, filled at the first use
+
+
+def _code(dtype) -> int:
+    c = _CODES.get(dtype)
+    if c is None:
+        import torch
+
+        _CODES.update({torch.bfloat16: ZPP_BF16, torch.float32: ZPP_FP32})
+        c = _CODES.get(dtype)
+        if c is None:
+            raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 expected")
+    return c
+
+
 def _rows(t, name: str):
     """(rows, width, row stride in elements) of a tensor whose leading dimensions
     follow one stride and whose last one is contiguous."""
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    width = t.shape[-1]
+    width = shape[-1]
     rows = t.numel() // width if width else 0
+    if t.is_contiguous():
+        return rows, width, width
     if rows <= 1:
         if width > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name}'s last dimension must be contiguous")
         return rows, width, width
-    if t.dim() > 2 and t.is_contiguous():
-        return rows, width, width
-    lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    lead = [(n, s) for n, s in zip(shape[:-1], t.stride()[:-1]) if n > 1]
     if (width > 1 and t.stride(-1) != 1) or any(a[1] != b[0] * b[1] for a, b in zip(lead, lead[1:])):
         raise ValueError(f"{name} must be rows of contiguous elements with one stride between them")
     return rows, width, lead[-1][1]
@@ -379,31 +396,42 @@ def _rows(t, name: str):
 def _check_weight(codes, scales, bits: int, block: int, numel: int) -> None:
     import torch
 
-    _need_contiguous(codes=codes, scales=scales)
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
     if codes.element_size() != 1 or scales.dtype != torch.float32:
         raise TypeError("codes must be bytes and scales float32")
     if codes.numel() * 8 != numel * bits or scales.numel() * block != numel:
         raise ValueError(f"codes and scales do not hold {numel} weights in {bits}-bit blocks of {block}")
 
 
-def _linear(grad: bool, a, codes, scales, bits, block, out_len, dtype, out, workspace, stream):
-    import torch
+def _workspace(workspace, need: int, like):
+    """(address, bytes, the tensor to keep) of a call's workspace, on ``like``'s device."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        import torch
 
+        workspace = like.new_empty(need, dtype=torch.uint8)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _linear(name: str, grad: int, a, codes, scales, bits, block, out_len, dtype, out, workspace, stream):
     rows, width, stride = _rows(a, "dy" if grad else "x")
-    out_features, in_features = (width, out_len) if grad else (out_len, width)
-    _check_weight(codes, scales, bits, block, out_features * in_features)
+    n_out, n_in = (width, out_len) if grad else (out_len, width)
+    _check_weight(codes, scales, bits, block, n_out * n_in)
+    adt, ostride = _code(a.dtype), out_len
     if out is None:
-        out = torch.empty(*a.shape[:-1], out_len, dtype=dtype or a.dtype, device=a.device)
-    elif tuple(out.shape) != (*a.shape[:-1], out_len):
-        raise ValueError(f"out must be of shape {(*a.shape[:-1], out_len)}")
-    ostride = _rows(out, "out")[2]
-    adt, odt = _dtype_code(a), _dtype_code(out)
-    need = zpp_linear_blocks_workspace(int(grad), adt, odt, rows, out_features, in_features)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
-    call = zpp_linear_blocks_grad if grad else zpp_linear_blocks
-    call(a, adt, stride, rows, codes, scales, bits, out_features, in_features, block, out, odt, ostride, workspace,
-         0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+        dtype = dtype or a.dtype
+        odt = _code(dtype)
+        out = a.new_empty((*a.shape[:-1], out_len), dtype=dtype)
+    else:
+        if tuple(out.shape) != (*a.shape[:-1], out_len) or (dtype or out.dtype) != out.dtype:
+            raise ValueError(f"out must be of shape {(*a.shape[:-1], out_len)} and of the dtype asked for")
+        odt, ostride = _code(out.dtype), _rows(out, "out")[2]
+    need = _lib.zpp_linear_blocks_workspace(grad, adt, odt, rows, n_out, n_in)
+    ws, ws_bytes, keep = _workspace(workspace, need, a)
+    _call(name, a.data_ptr(), adt, stride, rows, codes.data_ptr(), scales.data_ptr(), bits, n_out, n_in, block,
+          out.data_ptr(), odt, ostride, ws, ws_bytes, _stream(stream))
     return out
 
 
@@ -415,29 +443,35 @@ def linear(x, codes, scales, bits: int, block: int, out_features: int, dtype=Non
     device tensor of at least ``zpp_linear_blocks_workspace`` bytes; with a
     ``stream`` that is not torch's current one, pass ``out`` and ``workspace``
     (memory torch allocates here belongs to its current stream)."""
-    return _linear(False, x, codes, scales, bits, block, out_features, dtype, out, workspace, stream)
+    return _linear("zpp_linear_blocks", 0, x, codes, scales, bits, block, out_features, dtype, out, workspace, stream)
 
 
 def linear_grad(dy, codes, scales, bits: int, block: int, in_features: int, dtype=None, out=None, workspace=None,
                 stream=None):
     """dy @ W: the gradient of :func:`linear` with respect to x, for dy
     [..., out_features]. Arguments as there."""
-    return _linear(True, dy, codes, scales, bits, block, in_features, dtype, out, workspace, stream)
+    return _linear("zpp_linear_blocks_grad", 1, dy, codes, scales, bits, block, in_features, dtype, out, workspace,
+                   stream)
 
 
-def _check_norm(width: int, **vectors):
-    """The shared dtype code of the given weight-like vectors (None: left out)."""
-    code = None
-    for name, v in vectors.items():
-        if v is None:
-            continue
-        _need_contiguous(**{name: v})
-        if v.numel() != width:
-            raise ValueError(f"{name} must have {width} elements")
-        if code is not None and _dtype_code(v) != code:
-            raise TypeError("weight and bias must be of one dtype")
-        code = _dtype_code(v)
-    return code
+def _vector(v, width: int, name: str):
+    """(address, dtype code) of a weight-like vector, (None, None) of None."""
+    if v is None:
+        return None, None
+    if not v.is_contiguous() or v.numel() != width:
+        raise ValueError(f"{name} must be contiguous, of {width} elements")
+    return v.data_ptr(), _code(v.dtype)
+
+
+def _like(out, x):
+    """``out`` (or a new tensor) of x's shape and dtype, and its row stride."""
+    if out is None:
+        import torch
+
+        return torch.empty_like(x, memory_format=torch.contiguous_format), x.shape[-1]
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must be of x's shape and dtype")
+    return out, _rows(out, "out")[2]
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
@@ -447,15 +481,16 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     import torch
 
     rows, width, stride = _rows(x, "x")
-    wdt = _check_norm(width, weight=weight, bias=bias) or _dtype_code(x)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must be of x's shape and dtype")
-    stats = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    zpp_layer_norm(x, _dtype_code(x), stride, rows, width, weight, bias, wdt, eps, out, _rows(out, "out")[2], mean,
-                   rstd, stream)
+    xdt = _code(x.dtype)
+    w, wdt = _vector(weight, width, "weight")
+    b, bdt = _vector(bias, width, "bias")
+    if wdt and bdt and wdt != bdt:
+        raise TypeError("weight and bias must be of one dtype")
+    out, ostride = _like(out, x)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
+    _call("zpp_layer_norm", x.data_ptr(), xdt, stride, rows, width, w, b, wdt or bdt or xdt, eps, out.data_ptr(),
+          ostride, mean.data_ptr(), rstd.data_ptr(), _stream(stream))
     return out, mean, rstd
 
 
@@ -469,20 +504,19 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype
     rows, width, stride = _rows(x, "x")
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must be of x's shape and dtype")
-    _need_contiguous(mean=mean, rstd=rstd)
-    if mean.numel() != rows or rstd.numel() != rows or mean.dtype != torch.float32 or rstd.dtype != torch.float32:
-        raise ValueError("mean and rstd must be float32, one element per row")
+    f32 = torch.float32
+    if not (mean.is_contiguous() and rstd.is_contiguous() and mean.numel() == rstd.numel() == rows
+            and mean.dtype == rstd.dtype == f32):
+        raise ValueError("mean and rstd must be contiguous float32, one element per row")
+    w, _ = _vector(weight, width, "weight")
     wt = weight.dtype if weight is not None else (w_dtype or x.dtype)
-    _check_norm(width, weight=weight)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must be of x's shape and dtype")
-    dw = torch.empty(width, dtype=wt, device=x.device)
-    db = torch.empty(width, dtype=wt, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(zpp_layer_norm_grad_workspace(rows, width), dtype=torch.uint8, device=x.device)
-    zpp_layer_norm_grad(dy, _rows(dy, "dy")[2], x, _dtype_code(x), stride, rows, width, weight, _dtype_code(dw), mean,
-                        rstd, out, _rows(out, "out")[2], dw, db, workspace,
-                        workspace.numel() * workspace.element_size(), stream)
+    xdt, wdt, dy_stride = _code(x.dtype), _code(wt), _rows(dy, "dy")[2]
+    out, ostride = _like(out, x)
+    dw = x.new_empty(width, dtype=wt)
+    db = torch.empty_like(dw)
+    need = _lib.zpp_layer_norm_grad_workspace(rows, width) if workspace is None else 0
+    ws, ws_bytes, keep = _workspace(workspace, need, x)
+    _call("zpp_layer_norm_grad", dy.data_ptr(), dy_stride, x.data_ptr(), xdt, stride, rows, width, w, wdt,
+          mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), ostride, dw.data_ptr(), db.data_ptr(), ws, ws_bytes,
+          _stream(stream))
     return out, dw, db
