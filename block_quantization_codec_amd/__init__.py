@@ -43,7 +43,7 @@ ZPP_MAX_BLOCK = 4096
 ZPP_MAX_INPUTS = 4096
 ZPP_MAX_DIVISOR = 1 << 24
 ZPP_MAX_NUMEL = 1 << 40
-ZPP_MAX_FEATURES = 1 << 26
+ZPP_MAX_FEATURES = 1 << 22
 ZPP_MAX_ROWS = 1 << 30
 
 EXPORTED = ("zpp_quantize_blocks", "zpp_quantize_reordered", "zpp_dequantize_blocks", "zpp_reorder_slices",
@@ -83,7 +83,7 @@ def _load() -> ctypes.CDLL:
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = ctypes.c_int
-    lib.zpp_linear_blocks_workspace.argtypes = [I32, I32, I32, I64, I64, I64]
+    lib.zpp_linear_blocks_workspace.argtypes = [I32, I32, I64, I32, I64, I64, I64]
     lib.zpp_linear_blocks_workspace.restype = I64
     lib.zpp_layer_norm_grad_workspace.argtypes = [I64, I64]
     lib.zpp_layer_norm_grad_workspace.restype = I64
@@ -185,8 +185,9 @@ def zpp_linear_blocks_grad(dy, dy_dtype, dy_stride, rows, codes, scales, bits, o
           _stream(stream))
 
 
-def zpp_linear_blocks_workspace(grad, in_dtype, out_dtype, rows, out_features, in_features) -> int:
-    return int(_lib.zpp_linear_blocks_workspace(grad, in_dtype, out_dtype, rows, out_features, in_features))
+def zpp_linear_blocks_workspace(grad, in_dtype, in_stride, out_dtype, rows, out_features, in_features) -> int:
+    return int(_lib.zpp_linear_blocks_workspace(grad, in_dtype, in_stride, out_dtype, rows, out_features,
+                                                in_features))
 
 
 def zpp_layer_norm(x, x_dtype, x_stride, rows, width, weight, bias, w_dtype, eps, y, y_stride, mean, rstd,
@@ -428,7 +429,7 @@ def _linear(name: str, grad: int, a, codes, scales, bits, block, out_len, dtype,
         if tuple(out.shape) != (*a.shape[:-1], out_len) or (dtype or out.dtype) != out.dtype:
             raise ValueError(f"out must be of shape {(*a.shape[:-1], out_len)} and of the dtype asked for")
         odt, ostride = _code(out.dtype), _rows(out, "out")[2]
-    need = _lib.zpp_linear_blocks_workspace(grad, adt, odt, rows, n_out, n_in)
+    need = _lib.zpp_linear_blocks_workspace(grad, adt, stride, odt, rows, n_out, n_in)
     ws, ws_bytes, keep = _workspace(workspace, need, a)
     _call(name, a.data_ptr(), adt, stride, rows, codes.data_ptr(), scales.data_ptr(), bits, n_out, n_in, block,
           out.data_ptr(), odt, ostride, ws, ws_bytes, _stream(stream))

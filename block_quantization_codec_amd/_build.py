@@ -21,7 +21,7 @@ ARCH = os.environ.get("ZPP_OFFLOAD_ARCH", "gfx950")
 
 DRR_UNITS = [f"drr_in{i}_out{o}.hip" for i in (4, 8) for o in (0, 4, 8)]
 LINEAR_UNITS = ["linear_few.hip", "linear_mid.hip",
-                *(f"linear_{k}_{d}{b}.hip" for k in ("tile", "big") for d in ("fwd", "grad") for b in (4, 8))]
+                *(f"linear_big_{d}{b}.hip" for d in ("fwd", "grad") for b in (4, 8))]
 SOURCES = ["quantize.hip", "dequantize.hip", "reorder.hip", "drr.hip", *DRR_UNITS, "linear.hip", *LINEAR_UNITS,
            "layer_norm.hip", "zpp_api.hip"]
 HEADERS = ["zpp_device.h", "zpp_launch.h", "drr_kernel.h", "linear_device.h", "linear_codes.h",

@@ -1,5 +1,6 @@
-// linear.hip - which kernels a linear product on block codes takes, and the
-// sum of the parts of a split contraction.
+// linear.hip - which kernels a linear product on block codes takes, the packing
+// of activations that the tiled ones cannot read, and the sum of the parts of a
+// split contraction.
 #include <algorithm>
 #include <cmath>
 
@@ -10,14 +11,10 @@ namespace zpp {
 
 hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream);
 hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream);
-hipError_t launch_linear_tile_fwd4(const LinArgs &p, int mode, int mt, hipStream_t stream);
-hipError_t launch_linear_big_fwd4(const LinArgs &p, int mt, hipStream_t stream);
-hipError_t launch_linear_tile_fwd8(const LinArgs &p, int mode, int mt, hipStream_t stream);
-hipError_t launch_linear_big_fwd8(const LinArgs &p, int mt, hipStream_t stream);
-hipError_t launch_linear_tile_grad4(const LinArgs &p, int mode, int mt, hipStream_t stream);
-hipError_t launch_linear_big_grad4(const LinArgs &p, int mt, hipStream_t stream);
-hipError_t launch_linear_tile_grad8(const LinArgs &p, int mode, int mt, hipStream_t stream);
-hipError_t launch_linear_big_grad8(const LinArgs &p, int mt, hipStream_t stream);
+hipError_t launch_linear_big_fwd4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
 
 namespace {
 
@@ -25,7 +22,6 @@ constexpr int64_t kCus = 256;       // MI355X
 constexpr int64_t kFewRows = 4;     // forward: at most this many rows stream the codes, x in registers,
 constexpr int64_t kMidRows = 64;    // and this many with x in LDS
 constexpr int64_t kMidGroups = 512;  // workgroups the middle kernel's contraction is split for
-constexpr int64_t kMaxBigStride = INT64_C(1) << 22;  // elements: a tile's offsets of linear_big.h are 32-bit
 constexpr int64_t kMaxTiles = 1 << 23;  // workgroups of one launch
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -141,14 +137,71 @@ __global__ __launch_bounds__(kBlockThreads) void linear_join_kernel(const float 
     }
 }
 
+// Activations as the tiled kernels read them: PA planes of bf16 parts, rows of
+// whole steps, zeros past the end. 8 elements a thread. `vec`: rows lie on
+// 16-byte pieces.
+template <int PA>
+__global__ __launch_bounds__(kBlockThreads) void linear_pack_kernel(const void *__restrict__ a, int64_t lda,
+                                                                    int64_t rows, int64_t len, int64_t ldp, bool vec,
+                                                                    uint16_t *__restrict__ out) {
+    const int64_t per = ldp / 8, n = static_cast<int64_t>(gridDim.x) * kBlockThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlockThreads + threadIdx.x; i < rows * per; i += n) {
+        const int64_t r = i / per, c = (i - r * per) * 8;
+        u32x4 v[PA];
+        if constexpr (PA == 3) {
+            const uint32_t *from = static_cast<const uint32_t *>(a) + r * lda + c;
+            uint32_t f[8];
+            if (vec && c + 8 <= len) {
+                const u32x4 lo = ld<u32x4>(from), hi = ld<u32x4>(from + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = lo[j], f[4 + j] = hi[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = c + j < len ? from[j] : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[3];
+                to_parts<3>(as_f(f[2 * j]), as_f(f[2 * j + 1]), w);
+#pragma unroll
+                for (int x = 0; x < 3; ++x) v[x][j] = w[x];
+            }
+        } else {
+            const uint16_t *from = static_cast<const uint16_t *>(a) + r * lda + c;
+            if (vec && c + 8 <= len) {
+                v[0] = ld<u32x4>(from);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[0][j] = (c + 2 * j < len ? from[2 * j] : 0u) |
+                              (c + 2 * j + 1 < len ? static_cast<uint32_t>(from[2 * j + 1]) << 16 : 0u);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < PA; ++x) st<u32x4>(out + (x * rows + r) * ldp + c, v[x]);
+    }
+}
+
+// The tiled kernels read bf16 rows on 16-byte pieces, of strides that 32-bit
+// offsets of 256 rows can take; anything else is packed first.
+bool needs_pack(const Plan &p, bool in_f32, int64_t lda, int64_t c_len) {
+    return p.way == Way::tile && (in_f32 || lda % 8 != 0 || c_len % 8 != 0 || lda > (INT64_C(1) << 22));
+}
+
+int64_t packed_bytes(const Plan &p, bool in_f32, int64_t rows, int64_t c_len) {
+    return ceil_div(c_len, 64) * 64 * std::min(rows, p.rows) * 2 * (in_f32 ? 3 : 1);
+}
+
 }  // namespace
 
-int64_t linear_workspace(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
+int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int64_t rows, int64_t n_out,
+                         int64_t n_in) {
     if (rows == 0) return 0;
     const Plan p = make_plan(grad, in_f32, out_f32, rows, n_out, n_in);
-    if (p.splits == 1) return 0;
-    const int64_t len = grad ? n_in : n_out;
-    return p.splits * std::min(rows, p.rows) * ((len + 3) & ~INT64_C(3)) * 4;
+    const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
+    int64_t bytes = needs_pack(p, in_f32, lda, c_len) ? packed_bytes(p, in_f32, rows, c_len) : 0;
+    if (p.splits > 1) bytes += p.splits * std::min(rows, p.rows) * ((len + 3) & ~INT64_C(3)) * 4;
+    return bytes;
 }
 
 hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int64_t rows, const void *codes,
@@ -156,7 +209,7 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
                          bool out_f32, int64_t ldo, void *workspace, hipStream_t stream) {
     const Plan plan = make_plan(grad, in_f32, out_f32, rows, n_out, n_in);
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
-    const int mode = in_f32 ? 3 : out_f32 ? 2 : (lda % 8 == 0 && c_len % 8 == 0 && lda <= kMaxBigStride) ? 0 : 1;
+    const bool pack = needs_pack(plan, in_f32, lda, c_len);
     for (int64_t r0 = 0; r0 < rows; r0 += plan.rows) {
         LinArgs p{};
         p.a = static_cast<const uint8_t *>(a) + r0 * lda * (in_f32 ? 4 : 2);
@@ -170,10 +223,25 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
         p.out = static_cast<uint8_t *>(out) + r0 * ldo * (out_f32 ? 4 : 2);
         p.ldo = ldo;
         p.out_f32 = out_f32;
-        p.partial = static_cast<float *>(workspace);
+        p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                              (pack ? packed_bytes(plan, in_f32, rows, c_len) : 0));
         p.splits = plan.splits;
         p.split_steps = plan.split_steps;
-        hipError_t e;
+        hipError_t e = hipSuccess;
+        if (pack) {
+            const int64_t ldp = ceil_div(c_len, 64) * 64;
+            const unsigned grid = static_cast<unsigned>(
+                std::min<int64_t>(ceil_div(p.rows * ldp / 8, kBlockThreads), 1 << 16));
+            uint16_t *to = static_cast<uint16_t *>(workspace);
+            if (in_f32)
+                linear_pack_kernel<3><<<grid, kBlockThreads, 0, stream>>>(p.a, lda, p.rows, c_len, ldp, lda % 4 == 0, to);
+            else
+                linear_pack_kernel<1><<<grid, kBlockThreads, 0, stream>>>(p.a, lda, p.rows, c_len, ldp, lda % 8 == 0, to);
+            if (e = hipGetLastError(); e != hipSuccess) return e;
+            p.a = to;
+            p.lda = ldp;
+            p.plane = p.rows * ldp;
+        }
         if (plan.way == Way::few) {
             e = launch_linear_few(p, bits, in_f32, stream);
         } else if (plan.way == Way::mid) {
@@ -181,20 +249,15 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
             p.col_tiles = ceil_div(n_out, 64 * kMidTiles);
             e = launch_linear_mid(p, bits, in_f32, plan.mt, stream);
         } else {
+            const int parts = in_f32 ? 2 : out_f32 ? 1 : 0;
             p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
             p.col_tiles = ceil_div(len, 256);
-            if (mode == 0 && grad)
-                e = bits == 4 ? launch_linear_big_grad4(p, plan.mt, stream)
-                              : launch_linear_big_grad8(p, plan.mt, stream);
-            else if (mode == 0)
-                e = bits == 4 ? launch_linear_big_fwd4(p, plan.mt, stream)
-                              : launch_linear_big_fwd8(p, plan.mt, stream);
-            else if (grad)
-                e = bits == 4 ? launch_linear_tile_grad4(p, mode, plan.mt, stream)
-                              : launch_linear_tile_grad8(p, mode, plan.mt, stream);
+            if (grad)
+                e = bits == 4 ? launch_linear_big_grad4(p, parts, plan.mt, stream)
+                              : launch_linear_big_grad8(p, parts, plan.mt, stream);
             else
-                e = bits == 4 ? launch_linear_tile_fwd4(p, mode, plan.mt, stream)
-                              : launch_linear_tile_fwd8(p, mode, plan.mt, stream);
+                e = bits == 4 ? launch_linear_big_fwd4(p, parts, plan.mt, stream)
+                              : launch_linear_big_fwd8(p, parts, plan.mt, stream);
         }
         if (e != hipSuccess) return e;
         if (plan.splits > 1) {

@@ -111,6 +111,7 @@ struct LinArgs {
     int splits;
     int64_t split_steps;  // contraction steps of each split
     int64_t row_tiles, col_tiles;
+    int64_t plane;        // elements from one part of packed activations to the next
 };
 
 }  // namespace zpp

@@ -18,7 +18,7 @@ template <int BITS, int PA, int NT, int MT, int U, bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
     constexpr bool ASYNC = PA == 1;
     using C = CodeStream<BITS, NT, U, WIDE>;
-    using T = LinTile<false, BITS, PA, 1, MT, ASYNC>;  // its tiles of 64 indices
+    using T = LinTile<PA, MT>;
     constexpr int kTile = PA * T::kPlane;
     __shared__ __attribute__((aligned(128))) uint8_t tiles[2][2 * U][kTile];
 

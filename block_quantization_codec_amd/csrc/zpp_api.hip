@@ -216,14 +216,17 @@ zpp_status linear(bool grad, const void *a, int32_t a_dtype, int64_t a_stride, i
     if (!is_stride(a_stride, rows, a_len) || !is_stride(out_stride, rows, out_len)) return ZPP_ERR_ARG;
     if (workspace_bytes < 0) return ZPP_ERR_ARG;
     if (rows == 0) return ZPP_OK;
-    const int64_t need = zpp::linear_workspace(grad, a_dtype == ZPP_FP32, out_dtype == ZPP_FP32, rows, n_out, n_in);
+    // one row has no stride to speak of: it is its own length
+    if (rows == 1) (grad ? out_stride : a_stride) = n_in;
+    const int64_t need =
+        zpp::linear_workspace(grad, a_dtype == ZPP_FP32, a_stride, out_dtype == ZPP_FP32, rows, n_out, n_in);
     if (workspace_bytes < need) return ZPP_ERR_ARG;
     if (!a || !codes || !scales || !out || (need > 0 && !workspace)) return ZPP_ERR_NULL;
     if (!aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return ZPP_ERR_ALIGN;
     if (need > 0 && !aligned(workspace, 16)) return ZPP_ERR_ALIGN;
     // the side of in_features moves in 16-byte pieces
     const int64_t wide = grad ? out_stride * dtype_bytes(out_dtype) : a_stride * dtype_bytes(a_dtype);
-    if (rows > 1 && wide % 16 != 0) return ZPP_ERR_ALIGN;
+    if (wide % 16 != 0) return ZPP_ERR_ALIGN;
     const Range ra = matrix(a, rows, a_stride, a_len, a_dtype), rc{codes, code_bytes(n_out * n_in, bits)},
         rs{scales, 4 * (n_out * n_in / block)}, ro = matrix(out, rows, out_stride, out_len, out_dtype),
         rw{workspace, need};
@@ -233,13 +236,6 @@ zpp_status linear(bool grad, const void *a, int32_t a_dtype, int64_t a_stride, i
     if (overlap(ro, rw)) return ZPP_ERR_OVERLAP;
     const Range all[] = {ra, rc, rs, ro, rw};
     if (zpp_status s = check_all(all); s != ZPP_OK) return s;
-    // one row has no stride to speak of: a well-formed one, so that the kernels' rules see whole pieces
-    if (rows == 1) {
-        if (grad)
-            out_stride = n_in;
-        else
-            a_stride = n_in;
-    }
     return launch_checked([&] {
         return zpp::launch_linear(grad, a, a_dtype == ZPP_FP32, a_stride, rows, codes, scales, bits, n_out, n_in,
                    log2_of(block), out, out_dtype == ZPP_FP32, out_stride, workspace,
@@ -453,11 +449,12 @@ zpp_status zpp_linear_blocks_grad(const void *dy, int32_t dy_dtype, int64_t dy_s
                   dx_dtype, dx_stride, workspace, workspace_bytes, stream);
 }
 
-int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int32_t out_dtype, int64_t rows,
-                                    int64_t out_features, int64_t in_features) {
+int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
+                                    int64_t rows, int64_t out_features, int64_t in_features) {
     if (!is_dtype(in_dtype) || !is_dtype(out_dtype) || !is_linear_size(rows, out_features, in_features)) return 0;
-    return zpp::linear_workspace(grad != 0, in_dtype == ZPP_FP32, out_dtype == ZPP_FP32, rows, out_features,
-                                 in_features);
+    if (!is_stride(in_stride, rows, grad != 0 ? out_features : in_features)) return 0;
+    return zpp::linear_workspace(grad != 0, in_dtype == ZPP_FP32, in_stride, out_dtype == ZPP_FP32, rows,
+                                 out_features, in_features);
 }
 
 zpp_status zpp_layer_norm(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t width,

@@ -82,7 +82,7 @@ extern "C" {
 #define ZPP_MAX_BLOCK 4096
 #define ZPP_MAX_INPUTS 4096
 #define ZPP_MAX_DIVISOR 16777216 /* 2^24: every divisor up to it is exact in binary32 */
-#define ZPP_MAX_FEATURES 67108864 /* 2^26: the longest row of a weight matrix or of a norm */
+#define ZPP_MAX_FEATURES 4194304 /* 2^22: the longest row of a weight matrix or of a norm */
 #define ZPP_MAX_ROWS 1073741824  /* 2^30: the most rows of one linear or norm call */
 /* 2^40: the largest element count, input stride (bytes for codes, floats
  * for scales), and reordered buffer (elements, or bytes / 4) accepted; far
@@ -329,11 +329,14 @@ zpp_status zpp_linear_blocks_grad(const void *dy, int32_t dy_dtype, int64_t dy_s
                                   void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace that zpp_linear_blocks (grad == 0) or zpp_linear_blocks_grad
- * (grad != 0) needs for these types and sizes: 0 in most cases, and more where
- * few tiles of results are shared out over the GPU by splitting the sums.
- * It depends on the arguments alone; 0 for sizes the calls refuse. */
-int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int32_t out_dtype, int64_t rows,
-                                    int64_t out_features, int64_t in_features);
+ * (grad != 0) needs for these types, sizes and row stride of its input (any
+ * stride that is the row's length or more; it matters only whether rows lie on
+ * 16-byte pieces): for the sums of a contraction that is split to share out few
+ * tiles of results over the GPU, and for a packed copy of activations of
+ * binary32 or of odd lengths or strides. 0 where neither is needed. It depends
+ * on the arguments alone; 0 for sizes the calls refuse. */
+int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
+                                    int64_t rows, int64_t out_features, int64_t in_features);
 
 /*
  * Layer norm over each row of `width` elements, as it stands before the

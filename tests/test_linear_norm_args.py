@@ -33,10 +33,10 @@ def test_linear_argument_errors(z, grad):
         kw.setdefault("wsb", 1 << 30)
         return _linear(z, grad, **kw)
 
-    big = (1 << 26) + 32
+    big = (1 << 22) + 32
     for bad in (dict(adt=0), dict(adt=3), dict(odt=0), dict(odt=-1), dict(bits=2), dict(bits=16), dict(rows=-1),
                 dict(rows=(1 << 30) + 1), dict(n=0), dict(n=-1), dict(n=big), dict(k=0), dict(k=16), dict(k=48),
-                dict(k=-32), dict(k=big), dict(n=1 << 26, k=1 << 26), dict(block=16), dict(block=8192),
+                dict(k=-32), dict(k=big), dict(n=1 << 22, k=1 << 22), dict(block=16), dict(block=8192),
                 dict(block=96), dict(n=3, k=32, block=64), dict(astr=8), dict(ostr=8), dict(astr=-128),
                 dict(astr=(1 << 40) + 8), dict(astr=1 << 40, rows=3), dict(ostr=1 << 40, rows=3), dict(wsb=-1)):
         assert call(**bad) == z.ZPP_ERR_ARG, bad
@@ -53,7 +53,7 @@ def test_linear_argument_errors(z, grad):
 
 def test_linear_workspace_is_asked_for_and_checked(z):
     w = z.zpp_linear_blocks_workspace
-    need = w(1, 1, 1, 16, 8192, 1024)  # one row of tiles, a long contraction: split
+    need = w(1, 1, 8192, 1, 16, 8192, 1024)  # one row of tiles, a long contraction: split
     assert need > 0 and need % 16 == 0
     kw = dict(grad=True, rows=16, n=8192, k=1024)
     assert _linear(z, ws=A + 4 * G, wsb=need - 1, **kw) == z.ZPP_ERR_ARG
@@ -61,10 +61,15 @@ def test_linear_workspace_is_asked_for_and_checked(z):
     assert _linear(z, ws=A + 4 * G + 8, wsb=need, **kw) == z.ZPP_ERR_ALIGN
     for at in (A, A + G, A + 2 * G, A + 3 * G):  # on the input, the codes, the scales, the output
         assert _linear(z, ws=at, wsb=need, **kw) == z.ZPP_ERR_OVERLAP
-    assert w(0, 1, 1, 1, 8192, 8192) == 0      # one token
-    assert w(0, 1, 1, 0, 8192, 8192) == 0      # no rows
-    for bad in ((0, 7, 1, 4, 64, 64), (0, 1, 7, 4, 64, 64), (0, 1, 1, -1, 64, 64), (0, 1, 1, 4, 0, 64),
-                (0, 1, 1, 4, 64, 33)):
+    assert w(0, 1, 8192, 1, 1, 8192, 8192) == 0      # one token
+    assert w(0, 1, 8192, 1, 0, 8192, 8192) == 0      # no rows
+    assert w(1, 1, 8192, 1, 4096, 8192, 8192) == 0   # enough tiles, rows on 16-byte pieces
+    # odd strides, odd lengths and binary32 are packed: rows of whole 64s, two bytes an element and part
+    assert w(1, 1, 8193, 1, 4096, 8192, 8192) == 4096 * 8192 * 2
+    assert w(1, 1, 8131, 1, 4096, 8131, 8192) == 4096 * 8192 * 2
+    assert w(1, 2, 8192, 1, 4096, 8192, 8192) == 4096 * 8192 * 2 * 3
+    for bad in ((0, 7, 64, 1, 4, 64, 64), (0, 1, 64, 7, 4, 64, 64), (0, 1, 64, 1, -1, 64, 64), (0, 1, 64, 1, 4, 0, 64),
+                (0, 1, 64, 1, 4, 64, 33), (0, 1, 63, 1, 4, 64, 64)):
         assert w(*bad) == 0
 
 
@@ -76,7 +81,7 @@ def _norm(z, x=A, xdt=1, xs=128, rows=4, width=128, w=A + G, b=A + 2 * G, wdt=2,
 def test_layer_norm_argument_errors(z):
     nan, inf = float("nan"), float("inf")
     for bad in (dict(xdt=0), dict(wdt=9), dict(rows=-1), dict(rows=(1 << 30) + 1), dict(width=0), dict(width=-4),
-                dict(width=(1 << 26) + 1), dict(xs=127), dict(ys=127), dict(xs=(1 << 40) + 1),
+                dict(width=(1 << 22) + 1), dict(xs=127), dict(ys=127), dict(xs=(1 << 40) + 1),
                 dict(xs=1 << 40, rows=3), dict(eps=-1e-9), dict(eps=nan), dict(eps=inf)):
         assert _norm(z, **bad) == z.ZPP_ERR_ARG, bad
     for bad in (dict(x=None), dict(y=None), dict(mean=None), dict(rstd=None)):
