@@ -43,11 +43,12 @@ struct Plan {
 // the operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured
 // at 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
 double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, int64_t split_steps) {
-    static constexpr double step_us[3][4] = {{0.92, 1.05, 1.08, 1.60}, {1.90, 2.30, 3.20, 0}, {2.10, 3.30, 5.00, 0}};
+    static constexpr double step_us[3][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0}};
     const int i = mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3;
     const double tiles = static_cast<double>(ceil_div(rows, 16 * mt) * ceil_div(len, 256) * splits);
     double rounds = std::max(tiles / kCus, 1.0);
-    if (parts > 0 || mt == 16) rounds = std::ceil(rounds);  // one workgroup a CU; otherwise they overlap
+    // where a CU holds one workgroup; otherwise they overlap
+    if (mt == 16 || (parts == 1 && mt == 8) || (parts == 2 && mt >= 4)) rounds = std::ceil(rounds);
     double t = rounds * static_cast<double>(split_steps) * step_us[parts][i];
     if (splits > 1) t += 7.0 + static_cast<double>(splits * rows * len) * 8 / 5.5e6;
     return t;

@@ -298,8 +298,10 @@ struct LinBig {
     // The scale of index I of the lane's 16, in the lane's own half of the columns.
     template <int I>
     static __device__ __forceinline__ float row_scale(const Scales &s) {
-        const float lo = as_f(dpp_u32<0x150 + I>(as_u(s[0]))), hi = as_f(dpp_u32<0x150 + I>(as_u(s[1])));
-        return (threadIdx.x & 8) ? hi : lo;
+        // every lane of a row takes lane I's
+        const int lo = __builtin_amdgcn_mov_dpp(static_cast<int>(as_u(s[0])), 0x150 + I, 0xF, 0xF, true);
+        const int hi = __builtin_amdgcn_mov_dpp(static_cast<int>(as_u(s[1])), 0x150 + I, 0xF, 0xF, true);
+        return as_f(static_cast<uint32_t>((threadIdx.x & 8) ? hi : lo));
     }
 
     // B operands of a half: parts of four tiles.
