@@ -19,14 +19,15 @@ namespace zpp {
 
 constexpr int kChunk = 128;
 
-// 4-bit codes become bf16 in pairs by bit operations alone: bf16 holds 16 + u
-// exactly for u = 0..15, with u in its upper mantissa bits, so code + 24 is
-// the code's nibble with its top bit flipped, shifted into place under the
-// exponent of 16. The sum starts from -24 times the sum of x, which the matrix
-// instruction makes itself from a constant operand: about one instruction a
-// code in place of two, and all of it exact but the binary32 sums (whose terms
-// are up to 4 times larger for it). A dword's nibbles come out as pairs
-// (p, p + 4), so x is dealt in that order too.
+// BIAS: 4-bit codes become bf16 in pairs by bit operations alone: bf16 holds
+// 16 + u exactly for u = 0..15, with u in its upper mantissa bits, so code + 24
+// is the code's nibble with its top bit flipped, shifted into place under the
+// exponent of 16. -24 times the sum of x, which the matrix instruction makes
+// itself from a constant operand, is added to each chunk's sum: about one
+// instruction a code in place of two, all of it exact but the binary32 sums,
+// whose terms are 4 to 5 times larger for it. That is far below what a bf16
+// result can show; for binary32 results codes are converted one by one. A
+// dword's nibbles come out as pairs (p, p + 4), so x is dealt in that order too.
 constexpr uint32_t kBiasPair = 0xC1C0C1C0u;  // -24, -24 in bf16
 
 __device__ __forceinline__ uint32_t code4_pair(uint32_t w, int p) {
@@ -45,18 +46,18 @@ __device__ __forceinline__ void spread(float v, float (&s)[4]) {
 
 // 8 activations (as loaded: 16 bytes of bf16, 32 of binary32) as bf16 parts, in
 // the order of the codes' pairs.
-template <int BITS, int PA>
+template <bool BIAS, int PA>
 __device__ __forceinline__ void deal(const u32x4 (&v)[PA == 3 ? 2 : 1], u32x4 (&x)[PA]) {
     if constexpr (PA == 3) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = BITS == 4 ? j : 2 * j, f = BITS == 4 ? j + 4 : 2 * j + 1;
+            const int e = BIAS ? j : 2 * j, f = BIAS ? j + 4 : 2 * j + 1;
             uint32_t w[3];
             to_parts<3>(as_f(v[e / 4][e % 4]), as_f(v[f / 4][f % 4]), w);
 #pragma unroll
             for (int a = 0; a < 3; ++a) x[a][j] = w[a];
         }
-    } else if constexpr (BITS == 4) {
+    } else if constexpr (BIAS) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             x[0][j] = __builtin_amdgcn_perm(v[0][2 + j / 2], v[0][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
@@ -65,8 +66,10 @@ __device__ __forceinline__ void deal(const u32x4 (&v)[PA == 3 ? 2 : 1], u32x4 (&
     }
 }
 
-template <int BITS, int NT, int U, bool WIDE>
+template <int BITS, int NT, int U, bool WIDE, bool BIAS>
 struct CodeStream {
+    static_assert(!BIAS || BITS == 4, "8-bit codes have no room for one");
+    static constexpr float kScale = BIAS ? 1.0f : kCodeScale<BITS>;  // what the sums are multiplied by at the end
     static constexpr int kUnit = WIDE ? 7 : 5;    // log2 of the indices of one scale
     static constexpr int kS = WIDE ? (U + 3) / 4 : U;  // loads of scales, four a load
     static constexpr int kW = BITS == 4 ? 4 : 8;  // dwords of a chunk's codes
@@ -170,44 +173,46 @@ struct CodeStream {
             }
     }
 
-    // acc += chunk u's products with the activations a[m][s] of its four instructions.
-    template <int PA, int MT>
-    static __device__ __forceinline__ void chunk(const Chunks &c, int u, const u32x4 (&a)[MT][4][PA],
-                                                 const float (&scale)[kS][NT][4], f32x4 (&acc)[NT][MT]) {
+    // acc += chunk u's products. read(m, s, a) gives the operand of rows m and
+    // instruction s.
+    template <int PA, int MT, class F>
+    static __device__ __forceinline__ void chunk(const Chunks &c, int u, const float (&scale)[kS][NT][4],
+                                                 f32x4 (&acc)[NT][MT], F &&read) {
         const f32x4 zero = {0, 0, 0, 0};
         const u32x4 pair[1] = {u32x4{kBiasPair, kBiasPair, kBiasPair, kBiasPair}};
-        f32x4 bias[MT][WIDE ? 1 : 4];
+        f32x4 sum[NT][MT], bias[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int s = 0; s < 4; ++s) {
+            constexpr bool each = !WIDE;  // a scale for each instruction, or one for the chunk
+            u32x4 b[NT][1];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                f32x4 &o = bias[m][WIDE ? 0 : s];
-                if (!WIDE || s == 0) o = zero;
-                if constexpr (BITS == 4) o = mfma_parts<PA, 1>(a[m][s], pair, o);
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            f32x4 sum[MT];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                u32x4 b[1];
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if constexpr (BITS == 4) {
-                        b[0][j] = code4_pair(c.w[u][t][s], j);
+                    if constexpr (BIAS) {
+                        b[t][0][j] = code4_pair(c.w[u][t][s], j);
                     } else {
-                        const uint32_t w = c.w[u][t][2 * s + j / 2];
-                        b[0][j] = pack_hi(code_f32<8>(w, 2 * (j % 2)), code_f32<8>(w, 2 * (j % 2) + 1));
+                        constexpr int per = 32 / BITS;
+                        const int i = 8 * s + 2 * j;
+                        b[t][0][j] = pack_hi(code_f32<BITS>(c.w[u][t][i / per], i % per),
+                                             code_f32<BITS>(c.w[u][t][i / per], i % per + 1));
                     }
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    sum[m] = mfma_parts<PA, 1>(a[m][s], b, WIDE && s > 0 ? sum[m] : bias[m][WIDE ? 0 : s]);
-                    if (!WIDE || s == 3) {
-                        const float f = WIDE ? scale[u / 4][t][u % 4] : scale[u][t][s];
+            for (int m = 0; m < MT; ++m) {
+                u32x4 a[PA];
+                read(m, s, a);
+                const bool first = each || s == 0, last = each || s == 3;
+                if constexpr (BIAS) bias[m] = mfma_parts<PA, 1>(a, pair, first ? zero : bias[m]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[t][m][i] = __builtin_fmaf(sum[m][i], f, acc[t][m][i]);
-                    }
+                for (int t = 0; t < NT; ++t) {
+                    sum[t][m] = mfma_parts<PA, 1>(a, b[t], first ? zero : sum[t][m]);
+                    if (!last) continue;
+                    const float f = WIDE ? scale[u / 4][t][u % 4] : scale[u][t][s];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][m][i] =
+                            __builtin_fmaf(BIAS ? sum[t][m][i] + bias[m][i] : sum[t][m][i], f, acc[t][m][i]);
                 }
             }
         }

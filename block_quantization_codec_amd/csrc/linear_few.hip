@@ -30,9 +30,9 @@ __device__ __forceinline__ void rotate_parts(const u32x4 (&v)[PA], u32x4 (&o)[PA
 // RM is the number of rows of x that lie in one operand (a power of two below
 // 16): the lanes of a quarter load 16 / RM operands' pieces at once, and each
 // operand is a rotation of them.
-template <int BITS, int PA, int NT, int RM, int U, bool WIDE>
+template <int BITS, int PA, int NT, int RM, int U, bool WIDE, bool BIAS>
 struct Few {
-    using C = CodeStream<BITS, NT, U, WIDE>;
+    using C = CodeStream<BITS, NT, U, WIDE, BIAS>;
     static constexpr int kPer = 16 / RM;                  // operands of one load of x
     static constexpr int kX = (4 * U + kPer - 1) / kPer;  // loads of x
     using Raw = u32x4[kX][PA == 3 ? 2 : 1];
@@ -55,19 +55,19 @@ struct Few {
     template <int I>
     static __device__ __forceinline__ void use_from(const u32x4 (&x)[kX][PA], const typename C::Chunks &c,
                                                     const float (&scale)[C::kS][NT][4], f32x4 (&acc)[NT][1]) {
-        u32x4 a[1][4][PA];
-        rotate_parts<I % kPer * RM, PA>(x[I / kPer], a[0][0]);
-        rotate_parts<(I + 1) % kPer * RM, PA>(x[(I + 1) / kPer], a[0][1]);
-        rotate_parts<(I + 2) % kPer * RM, PA>(x[(I + 2) / kPer], a[0][2]);
-        rotate_parts<(I + 3) % kPer * RM, PA>(x[(I + 3) / kPer], a[0][3]);
-        C::template chunk<PA, 1>(c, I / 4, a, scale, acc);
+        C::template chunk<PA, 1>(c, I / 4, scale, acc, [&](int, int i, u32x4 (&a)[PA]) {
+            if (i == 0) rotate_parts<I % kPer * RM, PA>(x[I / kPer], a);
+            if (i == 1) rotate_parts<(I + 1) % kPer * RM, PA>(x[(I + 1) / kPer], a);
+            if (i == 2) rotate_parts<(I + 2) % kPer * RM, PA>(x[(I + 2) / kPer], a);
+            if (i == 3) rotate_parts<(I + 3) % kPer * RM, PA>(x[(I + 3) / kPer], a);
+        });
         if constexpr (I + 4 < 4 * U) use_from<I + 4>(x, c, scale, acc);
     }
 };
 
-template <int BITS, int PA, int NT, int RM, int U, bool WIDE, int WK>
+template <int BITS, int PA, int NT, int RM, int U, bool WIDE, bool BIAS, int WK>
 __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
-    using F = Few<BITS, PA, NT, RM, U, WIDE>;
+    using F = Few<BITS, PA, NT, RM, U, WIDE, BIAS>;
     using C = typename F::C;
     __shared__ float sums[WK][NT * 256];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
         C::scales(p, k, c, scale);
         u32x4 x[F::kX][PA];
 #pragma unroll
-        for (int l = 0; l < F::kX; ++l) deal<BITS, PA>(raw[l], x[l]);
+        for (int l = 0; l < F::kX; ++l) deal<BIAS, PA>(raw[l], x[l]);
         F::template use_from<0>(x, c, scale, acc);
     }
 
@@ -108,6 +108,7 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < WK; ++k) v += sums[k][o];
+        v *= C::kScale;
         if (p.out_f32)
             static_cast<float *>(p.out)[row_out * p.ldo + col] = v;
         else
@@ -115,29 +116,38 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
     }
 }
 
-template <int BITS, int PA, int NT, int RM, int U, int WK>
+template <int BITS, int PA, bool BIAS, int RM>
 hipError_t launch_as(const LinArgs &p, bool wide, hipStream_t stream) {
+    constexpr int NT = 1, U = 4, WK = 8;
     const unsigned grid = static_cast<unsigned>((p.n_out + 16 * NT - 1) / (16 * NT));
     if (wide)
-        linear_few_kernel<BITS, PA, NT, RM, U, true, WK><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, true, BIAS, WK><<<grid, WK * kWave, 0, stream>>>(p);
     else
-        linear_few_kernel<BITS, PA, NT, RM, U, false, WK><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, false, BIAS, WK><<<grid, WK * kWave, 0, stream>>>(p);
     return hipGetLastError();
 }
 
-template <int BITS, int PA>
+template <int BITS, int PA, bool BIAS>
 hipError_t launch_rows(const LinArgs &p, bool wide, hipStream_t stream) {
-    if (p.rows == 1) return launch_as<BITS, PA, 1, 1, 4, 8>(p, wide, stream);
-    if (p.rows == 2) return launch_as<BITS, PA, 1, 2, 4, 8>(p, wide, stream);
-    return launch_as<BITS, PA, 1, 4, 4, 8>(p, wide, stream);
+    if (p.rows == 1) return launch_as<BITS, PA, BIAS, 1>(p, wide, stream);
+    if (p.rows == 2) return launch_as<BITS, PA, BIAS, 2>(p, wide, stream);
+    return launch_as<BITS, PA, BIAS, 4>(p, wide, stream);
+}
+
+template <int BITS, int PA>
+hipError_t launch_out(const LinArgs &p, bool wide, hipStream_t stream) {
+    if constexpr (BITS == 4) {
+        if (!p.out_f32) return launch_rows<BITS, PA, true>(p, wide, stream);
+    }
+    return launch_rows<BITS, PA, false>(p, wide, stream);
 }
 
 }  // namespace
 
 hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream) {
     const bool wide = p.log2b >= 7 && p.n_in % kChunk == 0;
-    if (bits == 4) return a_f32 ? launch_rows<4, 3>(p, wide, stream) : launch_rows<4, 1>(p, wide, stream);
-    return a_f32 ? launch_rows<8, 3>(p, wide, stream) : launch_rows<8, 1>(p, wide, stream);
+    if (bits == 4) return a_f32 ? launch_out<4, 3>(p, wide, stream) : launch_out<4, 1>(p, wide, stream);
+    return a_f32 ? launch_out<8, 3>(p, wide, stream) : launch_out<8, 1>(p, wide, stream);
 }
 
 }  // namespace zpp
