@@ -36,10 +36,15 @@ struct Plan {
     int64_t rows; // rows of one launch
 };
 
+// What the parts of a split contraction cost, in microseconds: their writing,
+// reading and joining (5.5 bytes a nanosecond and 7 us).
+double join_time(int64_t splits, int64_t rows, int64_t len) {
+    return splits > 1 ? 7.0 + static_cast<double>(splits * rows * len) * 8 / 5.5e6 : 0;
+}
+
 // What a tiled call takes, in microseconds, with workgroups of mt rows of 16
 // and the contraction in `splits` parts: rounds of workgroups over the CUs
-// times steps times a step's time, and, if split, the writing, reading and
-// joining of the parts (5.5 bytes a nanosecond and 7 us). A step takes, with
+// times steps times a step's time, and the join. A step takes, with
 // the operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured
 // at 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
 double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, int64_t split_steps) {
@@ -50,8 +55,7 @@ double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, i
     // where a CU holds one workgroup; otherwise they overlap
     if (mt == 16 || (parts == 1 && mt == 8) || (parts == 2 && mt >= 4)) rounds = std::ceil(rounds);
     double t = rounds * static_cast<double>(split_steps) * step_us[parts][i];
-    if (splits > 1) t += 7.0 + static_cast<double>(splits * rows * len) * 8 / 5.5e6;
-    return t;
+    return t + join_time(splits, rows, len);
 }
 
 // The way of the least time. Measured on the way: 128 rows of 8192 x 8192 int4,
@@ -59,10 +63,15 @@ double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, i
 // in 8, 50 as 64-row tiles in 4 and 135 or more unsplit; 1024 rows, 132 us as
 // 256-row tiles in 2 (133) against 146 as 128-row tiles unsplit (142).
 //
-// A product to binary32 (or from it) multiplies by the exact codes at any
+// A forward product from bf16 to binary32 multiplies by the exact codes at any
 // number of rows: one part of the weights in place of three. 333 rows of 11008
-// x 4096 int8: 86 us so, 155 with three parts in tiles. From 128 rows of binary32 on, the tiles are faster (1024 rows of
-// 8192 x 8192 int4: 643 us against 829).
+// x 4096 int8: 86 us so, 155 with three parts in tiles. One from binary32 does
+// so up to 128 rows, and beyond them where its estimate, 3.25 us for each 128
+// indices of a workgroup, one of which fills a CU, is below the tiles' and
+// their packing's (10 bytes read and written an element, and a launch of 3 us):
+// 4019 rows of 512 x 928 int8, 30 us against 45 in tiles; 512 of 1024 x 8192
+// int4, 54 against 62; 200 of 8192 x 8192 int4, 173 against 155; 1024, 677
+// against 584.
 Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
     Plan p{};
     if (!grad && rows <= kFewRows) {
@@ -71,16 +80,20 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
         p.splits = 1;
         return p;
     }
-    if (!grad && rows <= (in_f32 ? 2 * kMidRows : out_f32 ? ZPP_MAX_ROWS : kMidRows)) {
-        p.way = Way::mid;
-        p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    Plan mid{};
+    double mid_us = 0;
+    if (!grad && (rows <= kMidRows || in_f32 || out_f32)) {
+        mid.way = Way::mid;
+        mid.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
         const int64_t steps = ceil_div(n_in, 128 * kMidChunks), col_tiles = ceil_div(n_out, 64 * kMidTiles);
-        const int64_t tiles = col_tiles * ceil_div(rows, 16 * p.mt);
+        const int64_t tiles = col_tiles * ceil_div(rows, 16 * mid.mt);
         const int64_t splits = std::max<int64_t>(std::min(kMidGroups / tiles, steps / 4), 1);
-        p.split_steps = ceil_div(steps, splits);
-        p.splits = static_cast<int>(ceil_div(steps, p.split_steps));
-        p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
-        return p;
+        mid.split_steps = ceil_div(steps, splits);
+        mid.splits = static_cast<int>(ceil_div(steps, mid.split_steps));
+        mid.rows = std::max<int64_t>(kMaxTiles / col_tiles / mid.splits, 1) * 16 * mid.mt;
+        if (!in_f32 || rows <= 2 * kMidRows) return mid;
+        mid_us = static_cast<double>(ceil_div(tiles * mid.splits, kCus) * mid.split_steps * kMidChunks) * 3.25 +
+                 join_time(mid.splits, rows, n_out);
     }
     p.way = Way::tile;
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
@@ -102,6 +115,7 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
             }
         }
     }
+    if (mid.mt != 0 && mid_us < least + 3.0 + static_cast<double>(rows * c_len) * 10 / 5.5e6) return mid;
     p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
     return p;
 }
