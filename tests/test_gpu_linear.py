@@ -106,6 +106,18 @@ def test_many_tiles_and_split_sums(z, grad, types, bits):
         assert torch.equal(got, want), (rows, n, k, block)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("ot", [BF, F32], ids=["fb", "ff"])
+@pytest.mark.parametrize("rows,n,k,block", [
+    # on either side of the choice between exact codes and tiles of 16, 64 and 128 rows, split and not
+    (129, 1056, 96, 32), (260, 8200, 352, 32), (200, 4100, 1056, 32), (333, 1001, 2080, 32), (520, 4100, 1056, 32),
+    (700, 1000, 4128, 32), (300, 4096, 992, 64), (600, 1001, 1024, 128), (300, 96, 160, 64), (129, 8192, 1184, 512),
+])
+def test_many_rows_of_binary32(z, rows, n, k, block, ot, bits):
+    got, want, _ = whole_case(z, 11, False, rows, n, k, bits, block, F32, ot)
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("grad", [False, True], ids=["y", "dx"])
 @pytest.mark.parametrize("rows", [1, 3, 20, 70, 300])
 def test_row_strides_leave_gaps_alone(z, grad, rows):
