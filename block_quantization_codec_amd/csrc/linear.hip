@@ -20,8 +20,7 @@ namespace {
 
 constexpr int64_t kCus = 256;       // MI355X
 constexpr int64_t kFewRows = 4;     // forward: at most this many rows stream the codes, x in registers,
-constexpr int64_t kMidRows = 64;    // and this many with x in LDS
-constexpr int64_t kMidGroups = 512;  // workgroups the middle kernel's contraction is split for
+constexpr int64_t kMidRows = 64;    // at most this many always with x in LDS
 constexpr int64_t kMaxTiles = 1 << 23;  // workgroups of one launch
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -37,16 +36,28 @@ struct Plan {
 };
 
 // What the parts of a split contraction cost, in microseconds: their writing,
-// reading and joining (5.5 bytes a nanosecond and 7 us).
+// reading and joining (5.5 bytes a nanosecond and 4 us).
 double join_time(int64_t splits, int64_t rows, int64_t len) {
-    return splits > 1 ? 7.0 + static_cast<double>(splits * rows * len) * 8 / 5.5e6 : 0;
+    return splits > 1 ? 4.0 + static_cast<double>(splits * rows * len) * 8 / 5.5e6 : 0;
+}
+
+// What a call by the middle kernel takes, in microseconds: steps of 256 indices
+// times the time of one in the CU that holds most workgroups, and the join. One
+// workgroup alone leaves the CU idle in its waits; more share its issue. Three
+// parts of 64 rows fill LDS, one workgroup a CU. 333 rows of 4096 x 11008 int4:
+// 61 us in 4 parts (66 estimated), 71 in 2 (77), 65 in 5 (71); 16 of 8192 x 28672
+// int8: 57 in 8 (51), 61 in 12 (54).
+double mid_time(bool in_f32, int mt, int64_t tiles, int64_t splits, int64_t split_steps, int64_t rows, int64_t len) {
+    const double n = static_cast<double>(ceil_div(tiles * splits, kCus));
+    const double cu = in_f32 && mt == 4 ? 6.5 * n : std::max(2.2, 1.5 * n) * (in_f32 ? 2 : 1);
+    return static_cast<double>(split_steps) * cu + join_time(splits, rows, len);
 }
 
 // What a tiled call takes, in microseconds, with workgroups of mt rows of 16
 // and the contraction in `splits` parts: rounds of workgroups over the CUs
-// times steps times a step's time, and the join. A step takes, with
-// the operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured
-// at 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
+// times steps times a step's time, and the join. A step takes, with the
+// operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured at
+// 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
 double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, int64_t split_steps) {
     static constexpr double step_us[3][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0}};
     const int i = mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3;
@@ -54,24 +65,24 @@ double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, i
     double rounds = std::max(tiles / kCus, 1.0);
     // where a CU holds one workgroup; otherwise they overlap
     if (mt == 16 || (parts == 1 && mt == 8) || (parts == 2 && mt >= 4)) rounds = std::ceil(rounds);
-    double t = rounds * static_cast<double>(split_steps) * step_us[parts][i];
-    return t + join_time(splits, rows, len);
+    return rounds * static_cast<double>(split_steps) * step_us[parts][i] + join_time(splits, rows, len);
 }
 
 // The way of the least time. Measured on the way: 128 rows of 8192 x 8192 int4,
-// 39 us as 128-row tiles in 8 parts (41 estimated) against 48 as 256-row tiles
+// 39 us as 128-row tiles in 8 parts (34 estimated) against 48 as 256-row tiles
 // in 8, 50 as 64-row tiles in 4 and 135 or more unsplit; 1024 rows, 132 us as
 // 256-row tiles in 2 (133) against 146 as 128-row tiles unsplit (142).
 //
-// A forward product from bf16 to binary32 multiplies by the exact codes at any
-// number of rows: one part of the weights in place of three. 333 rows of 11008
-// x 4096 int8: 86 us so, 155 with three parts in tiles. One from binary32 does
-// so up to 128 rows, and beyond them where its estimate, 3.25 us for each 128
-// indices of a workgroup, one of which fills a CU, is below the tiles' and
-// their packing's (10 bytes read and written an element, and a launch of 3 us):
-// 4019 rows of 512 x 928 int8, 30 us against 45 in tiles; 512 of 1024 x 8192
-// int4, 54 against 62; 200 of 8192 x 8192 int4, 173 against 155; 1024, 677
-// against 584.
+// A forward product of up to 64 rows, and from bf16 to binary32 of any number,
+// multiplies by the exact codes: with binary32 results that is one part of the
+// weights in place of three (333 rows of 4096 x 11008 int8: 74 us so, 155 with
+// three parts in tiles). Other products do so where the estimate is below the
+// tiles' (with a binary32 x, the tiles' and their packing's: 10 bytes read and
+// written an element, and a launch of 3 us; with bf16, by a quarter, which is
+// what its estimate misses at 128 to 1024 rows). 70 rows of 1024 x 8192 int4 bf16,
+// 14 us against 21 in tiles; 256 of 8192 x 8192, 69 against 56; 1024 of
+// 4096 x 4096, 64 against 56. binary32: 4019 rows of 512 x 928 int8, 30 us against
+// 45; 200 of 4096 x 11008 int8, 131 against 115.
 Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
     Plan p{};
     if (!grad && rows <= kFewRows) {
@@ -82,18 +93,23 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
     }
     Plan mid{};
     double mid_us = 0;
-    if (!grad && (rows <= kMidRows || in_f32 || out_f32)) {
+    if (!grad) {
         mid.way = Way::mid;
         mid.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
         const int64_t steps = ceil_div(n_in, 128 * kMidChunks), col_tiles = ceil_div(n_out, 64 * kMidTiles);
         const int64_t tiles = col_tiles * ceil_div(rows, 16 * mid.mt);
-        const int64_t splits = std::max<int64_t>(std::min(kMidGroups / tiles, steps / 4), 1);
-        mid.split_steps = ceil_div(steps, splits);
-        mid.splits = static_cast<int>(ceil_div(steps, mid.split_steps));
+        for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            if (want > steps) break;
+            const int64_t each = ceil_div(steps, want), n = ceil_div(steps, each);
+            const double t = mid_time(in_f32, mid.mt, tiles, n, each, rows, n_out);
+            if (mid.splits == 0 || t < mid_us) {
+                mid_us = t;
+                mid.splits = static_cast<int>(n);
+                mid.split_steps = each;
+            }
+        }
         mid.rows = std::max<int64_t>(kMaxTiles / col_tiles / mid.splits, 1) * 16 * mid.mt;
-        if (!in_f32 || rows <= 2 * kMidRows) return mid;
-        mid_us = static_cast<double>(ceil_div(tiles * mid.splits, kCus) * mid.split_steps * kMidChunks) * 3.25 +
-                 join_time(mid.splits, rows, n_out);
+        if (rows <= kMidRows || (out_f32 && !in_f32)) return mid;
     }
     p.way = Way::tile;
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
@@ -115,7 +131,8 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
             }
         }
     }
-    if (mid.mt != 0 && mid_us < least + 3.0 + static_cast<double>(rows * c_len) * 10 / 5.5e6) return mid;
+    if (in_f32) least += 3.0 + static_cast<double>(rows * c_len) * 10 / 5.5e6;
+    if (mid.mt != 0 && mid_us * (in_f32 ? 1.0 : 1.25) < least) return mid;
     p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
     return p;
 }
@@ -129,7 +146,17 @@ __global__ __launch_bounds__(kBlockThreads) void linear_join_kernel(const float 
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlockThreads + threadIdx.x; i < rows * per; i += n) {
         const int64_t r = i / per, c = (i - r * per) * 4;
         f32x4 v = {0, 0, 0, 0};
-        for (int s = 0; s < splits; ++s) v += ld<f32x4>(partial + (s * rows + r) * ldp + c);
+        const float *from = partial + r * ldp + c;
+        int s = 0;
+        for (; s + 8 <= splits; s += 8) {  // eight loads in flight
+            f32x4 part[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) part[j] = ld<f32x4>(from + (s + j) * rows * ldp);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v += part[j];
+        }
+#pragma unroll 4
+        for (; s < splits; ++s) v += ld<f32x4>(from + s * rows * ldp);
         const bool whole = (ldo & 3) == 0 && c + 4 <= len;
         if (out_f32) {
             float *o = static_cast<float *>(out) + r * ldo + c;

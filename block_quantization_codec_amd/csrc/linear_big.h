@@ -258,7 +258,7 @@ struct LinBig {
         for (int x = 0; x < PA; ++x) {
             LinArgs part = p;
             part.a = static_cast<const uint16_t *>(p.a) + x * p.plane;
-            Tile::stage_async(part, m0, c0, c_len, tile + x * kPlane);
+            Tile::stage_async(Tile::rows(part, m0), c0, c_len, tile + x * kPlane);
         }
     }
 

@@ -173,47 +173,46 @@ struct CodeStream {
             }
     }
 
-    // acc += chunk u's products. read(m, s, a) gives the operand of rows m and
-    // instruction s.
-    template <int PA, int MT, class F>
-    static __device__ __forceinline__ void chunk(const Chunks &c, int u, const float (&scale)[kS][NT][4],
-                                                 f32x4 (&acc)[NT][MT], F &&read) {
+    // A chunk's sums before they are scaled.
+    template <int MT>
+    struct Sums {
+        f32x4 v[NT][MT], bias[MT];
+    };
+
+    // Instruction s of chunk u for all the rows, whose operands are a; acc takes
+    // each sum at the end of its scale's indices.
+    template <int PA, int MT>
+    static __device__ __forceinline__ void step(const Chunks &c, int u, int s, const float (&scale)[kS][NT][4],
+                                                const u32x4 (&a)[MT][PA], Sums<MT> &sum, f32x4 (&acc)[NT][MT]) {
         const f32x4 zero = {0, 0, 0, 0};
         const u32x4 pair[1] = {u32x4{kBiasPair, kBiasPair, kBiasPair, kBiasPair}};
-        f32x4 sum[NT][MT], bias[MT];
+        const bool first = !WIDE || s == 0, last = !WIDE || s == 3;
+        u32x4 b[NT][1];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            constexpr bool each = !WIDE;  // a scale for each instruction, or one for the chunk
-            u32x4 b[NT][1];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (BIAS) {
-                        b[t][0][j] = code4_pair(c.w[u][t][s], j);
-                    } else {
-                        constexpr int per = 32 / BITS;
-                        const int i = 8 * s + 2 * j;
-                        b[t][0][j] = pack_hi(code_f32<BITS>(c.w[u][t][i / per], i % per),
-                                             code_f32<BITS>(c.w[u][t][i / per], i % per + 1));
-                    }
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (BIAS) {
+                    b[t][0][j] = code4_pair(c.w[u][t][s], j);
+                } else {
+                    constexpr int per = 32 / BITS;
+                    const int i = 8 * s + 2 * j;
+                    b[t][0][j] = pack_hi(code_f32<BITS>(c.w[u][t][i / per], i % per),
+                                         code_f32<BITS>(c.w[u][t][i / per], i % per + 1));
                 }
+            }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                u32x4 a[PA];
-                read(m, s, a);
-                const bool first = each || s == 0, last = each || s == 3;
-                if constexpr (BIAS) bias[m] = mfma_parts<PA, 1>(a, pair, first ? zero : bias[m]);
+        for (int m = 0; m < MT; ++m) {
+            if constexpr (BIAS) sum.bias[m] = mfma_parts<PA, 1>(a[m], pair, first ? zero : sum.bias[m]);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    sum[t][m] = mfma_parts<PA, 1>(a, b[t], first ? zero : sum[t][m]);
-                    if (!last) continue;
-                    const float f = WIDE ? scale[u / 4][t][u % 4] : scale[u][t][s];
+            for (int t = 0; t < NT; ++t) {
+                sum.v[t][m] = mfma_parts<PA, 1>(a[m], b[t], first ? zero : sum.v[t][m]);
+                if (!last) continue;
+                const float f = WIDE ? scale[u / 4][t][u % 4] : scale[u][t][s];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[t][m][i] =
-                            __builtin_fmaf(BIAS ? sum[t][m][i] + bias[m][i] : sum[t][m][i], f, acc[t][m][i]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    acc[t][m][i] =
+                        __builtin_fmaf(BIAS ? sum.v[t][m][i] + sum.bias[m][i] : sum.v[t][m][i], f, acc[t][m][i]);
             }
         }
     }

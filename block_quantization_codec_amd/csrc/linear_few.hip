@@ -55,12 +55,14 @@ struct Few {
     template <int I>
     static __device__ __forceinline__ void use_from(const u32x4 (&x)[kX][PA], const typename C::Chunks &c,
                                                     const float (&scale)[C::kS][NT][4], f32x4 (&acc)[NT][1]) {
-        C::template chunk<PA, 1>(c, I / 4, scale, acc, [&](int, int i, u32x4 (&a)[PA]) {
-            if (i == 0) rotate_parts<I % kPer * RM, PA>(x[I / kPer], a);
-            if (i == 1) rotate_parts<(I + 1) % kPer * RM, PA>(x[(I + 1) / kPer], a);
-            if (i == 2) rotate_parts<(I + 2) % kPer * RM, PA>(x[(I + 2) / kPer], a);
-            if (i == 3) rotate_parts<(I + 3) % kPer * RM, PA>(x[(I + 3) / kPer], a);
-        });
+        u32x4 a[4][1][PA];
+        rotate_parts<I % kPer * RM, PA>(x[I / kPer], a[0][0]);
+        rotate_parts<(I + 1) % kPer * RM, PA>(x[(I + 1) / kPer], a[1][0]);
+        rotate_parts<(I + 2) % kPer * RM, PA>(x[(I + 2) / kPer], a[2][0]);
+        rotate_parts<(I + 3) % kPer * RM, PA>(x[(I + 3) / kPer], a[3][0]);
+        typename C::template Sums<1> sum;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) C::template step<PA, 1>(c, I / 4, s, scale, a[s], sum, acc);
         if constexpr (I + 4 < 4 * U) use_from<I + 4>(x, c, scale, acc);
     }
 };

@@ -1,5 +1,5 @@
-// linear_mid.hip - y = x W^T on block codes for up to 64 rows of x, and for any
-// number where x or y is binary32: the stream over the codes of
+// linear_mid.hip - y = x W^T on block codes for 5 to 64 rows of x, and for more
+// where linear.hip finds it faster than tiles: the stream over the codes of
 // linear_few.hip, with the activations in LDS.
 //
 // With more than a few rows, every wave reading x for itself takes as much of
@@ -8,6 +8,13 @@
 // of x that they multiply by, double-buffered in LDS like the activations of
 // linear_tile.h; few workgroups then cover the features, so the contraction is
 // split over workgroups to fill the GPU and a second kernel joins the parts.
+//
+// 16 rows of 8192 x 28672 int8: 56 us, 4.2 TB/s of codes, near what the memory
+// gives; 64 rows of 28672 x 8192 int4: 68 us, and 333 of 4096 x 11008 int8 to
+// binary32: 67 to 74 us, where conversion and matrix instructions of the two
+// waves that a SIMD holds take the time (conversion is shared by 64 rows only).
+// Where the pieces of x lie is found once: found in every step it took 8% more.
+// Reading the operands from LDS an instruction ahead gained nothing.
 #include "linear_codes.h"
 #include "linear_tile.h"
 
@@ -42,11 +49,12 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
     typename C::Chunks c;
     typename T::Held held[2 * U];
 
+    [[maybe_unused]] const typename T::Rows rows = T::rows(p, m0);
     auto fetch = [&](int64_t k, int buf) {
 #pragma unroll
         for (int h = 0; h < 2 * U; ++h) {
             if constexpr (ASYNC)
-                T::stage_async(p, m0, k + h * 64, p.n_in, tiles[buf][h]);
+                T::stage_async(rows, k + h * 64, p.n_in, tiles[buf][h]);
             else
                 T::stage_load(p, m0, k + h * 64, p.n_in, vec, held[h]);
         }
@@ -73,20 +81,24 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
         }
         float scale[C::kS][NT][4];
         C::scales(p, k, c, scale);
+        typename C::template Sums<MT> sum;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            C::template chunk<PA, MT>(c, u, scale, acc, [&](int m, int s, u32x4 (&a)[PA]) {
-                const uint32_t i = C::index(q, s);
-                const uint8_t *tile = tiles[cur][2 * u] + (i >> 6) * kTile;
-                const int piece = lds_piece(m * 16 + (lane & 15), (i & 63) >> 3);
+        for (int i = 0; i < 4 * U; ++i) {
+            const uint32_t at_k = C::index(q, i % 4);
+            const uint8_t *tile = tiles[cur][2 * (i / 4)] + (at_k >> 6) * kTile;
+            u32x4 a[MT][PA];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int piece = lds_piece(m * 16 + (lane & 15), (at_k & 63) >> 3);
 #pragma unroll
                 for (int x = 0; x < PA; ++x) {  // the parts are bf16 already: each is dealt like one
                     const u32x4 v[1] = {*reinterpret_cast<const u32x4 *>(tile + x * T::kPlane + piece)};
                     u32x4 o[1];
                     deal<BIAS, 1>(v, o);
-                    a[x] = o[0];
+                    a[m][x] = o[0];
                 }
-            });
+            }
+            C::template step<PA, MT>(c, i / 4, i % 4, scale, a, sum, acc);
         }
         if (more) {
             land(cur ^ 1);

@@ -45,19 +45,30 @@ struct LinTile {
     static constexpr int kPieces = (kRows * 8 + kBlockThreads - 1) / kBlockThreads;  // 16-byte pieces per thread
 
     // Straight from global memory to LDS; every wave's instruction fills 8 rows.
-    static __device__ __forceinline__ void stage_async(const LinArgs &p, int64_t m0, int64_t c0, int64_t c_len,
-                                                       uint8_t *tile) {
+    // Where this lane's pieces lie in their rows, found once:
+    struct Rows {
+        const uint16_t *at[(2 * MT + 3) / 4];
+    };
+
+    static __device__ __forceinline__ Rows rows(const LinArgs &p, int64_t m0) {
+        const int lane = threadIdx.x & (kWave - 1), r = wave_in_block() * 8 + (lane >> 3);
+        Rows o;
+#pragma unroll
+        for (int i = 0; i < (2 * MT + 3) / 4; ++i)
+            o.at[i] = static_cast<const uint16_t *>(p.a) + min(m0 + i * 32 + r, p.rows - 1) * p.lda +
+                      ((lane & 7) ^ (r & 7)) * 8;
+        return o;
+    }
+
+    static __device__ __forceinline__ void stage_async(const Rows &rows, int64_t c0, int64_t c_len, uint8_t *tile) {
         const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
-        const uint16_t *a = static_cast<const uint16_t *>(p.a);
+        const int c = (lane & 7) ^ (lane >> 3);
+        const bool in = c * 8 < c_len - c0;
 #pragma unroll
         for (int i = 0; i < (2 * MT + 3) / 4; ++i) {
             const int g = i * 4 + w;  // group of 8 rows
             if (2 * MT % 4 != 0 && g >= 2 * MT) break;
-            const int r = g * 8 + (lane >> 3);
-            const int c = (lane & 7) ^ (r & 7);
-            const int64_t row = min(m0 + r, p.rows - 1);
-            const int64_t k = c0 + c * 8;
-            const void *src = k < c_len ? static_cast<const void *>(a + row * p.lda + k) : g_lin_zeros;
+            const uint16_t *src = in ? rows.at[i] + c0 : reinterpret_cast<const uint16_t *>(g_lin_zeros);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
                                              (__attribute__((address_space(3))) void *)(tile + g * 1024), 16, 0, 0);
         }

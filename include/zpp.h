@@ -293,10 +293,12 @@ zpp_status zpp_dequant_reduce_average(const void *codes_in, int64_t codes_stride
  *
  * the second being the gradient of the first with respect to x. Any number
  * of rows, from one token to a long sequence. Sums are binary32. Where input
- * and output are both ZPP_BF16 and there are more than 64 rows, and in every
- * bf16 gradient, the weights enter the products as bf16, exactly the values
- * zpp_dequantize_blocks writes as ZPP_BF16; otherwise nothing is rounded below
- * binary32 but the result.
+ * and output are both ZPP_BF16, the weights may enter the products of more
+ * than 64 rows, and enter those of every gradient, as bf16: exactly the values
+ * zpp_dequantize_blocks writes as ZPP_BF16. Otherwise nothing is rounded below
+ * binary32 but the result. The number of rows chooses kernels, so a row's
+ * result can differ by roundings between calls of different numbers of rows;
+ * calls of the same sizes give the same bits.
  *
  *   x / dy          in   rows of in_features (dy: out_features) elements of x_dtype, 16-B aligned
  *   x_stride        in   elements from one row to the next, >= the row's length; for x a
