@@ -7,6 +7,13 @@
 // pairs, for any number of rows. A wave has NT tiles of 16 output features;
 // the WK waves of a workgroup take U chunks of 128 indices in turn and join
 // their sums in LDS at the end, in wave order.
+//
+// One row of 28672 x 8192 int4: 27 to 28 us, 4.4 TB/s of codes and scales, the
+// vector instructions of the conversion 0.58 of the time (4 rows: 34 us); 1024 x
+// 8192: 5.3 us, of which the launch, a load's round trip and the join are most.
+// x in registers and rotated into place takes one load for 16 instructions'
+// operands: loaded for each, x took as much of the path from L2 as the codes
+// and the first case 54 us. Non-temporal loads gained nothing.
 #include "linear_codes.h"
 
 namespace zpp {
