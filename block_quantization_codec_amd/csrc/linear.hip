@@ -62,16 +62,17 @@ double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, i
     static constexpr double step_us[3][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0}};
     const int i = mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3;
     const double tiles = static_cast<double>(ceil_div(rows, 16 * mt) * ceil_div(len, 256) * splits);
-    double rounds = std::max(tiles / kCus, 1.0);
-    // where a CU holds one workgroup; otherwise they overlap
-    if (mt == 16 || (parts == 1 && mt == 8) || (parts == 2 && mt >= 4)) rounds = std::ceil(rounds);
+    // Workgroups that share a CU take about as long as one after the other.
+    const double rounds = std::ceil(tiles / kCus);
     return rounds * static_cast<double>(split_steps) * step_us[parts][i] + join_time(splits, rows, len);
 }
 
 // The way of the least time. Measured on the way: 128 rows of 8192 x 8192 int4,
 // 39 us as 128-row tiles in 8 parts (34 estimated) against 48 as 256-row tiles
-// in 8, 50 as 64-row tiles in 4 and 135 or more unsplit; 1024 rows, 132 us as
-// 256-row tiles in 2 (133) against 146 as 128-row tiles unsplit (142).
+// in 8, 50 as 64-row tiles in 4 and 135 or more unsplit; 100 rows of 28672 x
+// 8192 int4, 92 us as 128-row tiles in 2 parts (83), 122 in 3 (119) and 139 as
+// 64-row tiles unsplit (134); 1024 rows of 8192 x 8192, 132 us as 256-row tiles in
+// 2 (130) against 146 as 128-row tiles unsplit (141).
 //
 // A forward product of up to 64 rows, and from bf16 to binary32 of any number,
 // multiplies by the exact codes: with binary32 results that is one part of the
