@@ -36,7 +36,6 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
     const int64_t n0 = (place.col * 4 + w) * (16 * NT);
     // a wave past the last feature works on it, and stores nothing
     const typename C::At at = C::place(p, min(n0, p.n_out - 1));
-    const bool vec = (p.lda & 3) == 0;
 
     f32x4 acc[NT][MT];
 #pragma unroll
@@ -56,7 +55,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
             if constexpr (ASYNC)
                 T::stage_async(rows, k + h * 64, p.n_in, tiles[buf][h]);
             else
-                T::stage_load(p, m0, k + h * 64, p.n_in, vec, held[h]);
+                T::stage_load(p, m0, k + h * 64, p.n_in, held[h]);
         }
     };
     auto land = [&](int buf) {

@@ -74,60 +74,41 @@ struct LinTile {
         }
     }
 
-    using Held = uint32_t[kPieces][PA == 3 ? 8 : 4];
+    using Held = uint32_t[kPieces][8];
 
-    // Through registers: any row stride, any contraction length, both types.
+    // binary32 activations, through registers. Rows and their length are whole
+    // 16-byte pieces, and the length whole 8 elements.
     static __device__ __forceinline__ void stage_load(const LinArgs &p, int64_t m0, int64_t c0, int64_t c_len,
-                                                      bool vec, Held &h) {
+                                                      Held &h) {
+        static_assert(PA == 3);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int id = i * kBlockThreads + threadIdx.x;
             if (id >= kRows * 8) break;
             const int64_t row = min(m0 + id / 8, p.rows - 1);
             const int64_t k = c0 + (id & 7) * 8;
-            if constexpr (PA == 3) {
-                const float *a = static_cast<const float *>(p.a) + row * p.lda + k;
-                if (vec && k + 8 <= c_len) {
-                    const u32x4 u = ld<u32x4>(a), v = ld<u32x4>(a + 4);
+            const float *a = static_cast<const float *>(p.a) + row * p.lda + k;
+            u32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+            if (k < c_len) u = ld<u32x4>(a), v = ld<u32x4>(a + 4);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) h[i][j] = u[j], h[i][4 + j] = v[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) h[i][j] = k + j < c_len ? as_u(a[j]) : 0;
-                }
-            } else {
-                const uint16_t *a = static_cast<const uint16_t *>(p.a) + row * p.lda + k;
-                if (vec && k + 8 <= c_len) {
-                    const u32x4 u = ld<u32x4>(a);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[i][j] = u[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        h[i][j] = (k + 2 * j < c_len ? a[2 * j] : 0u) |
-                                  (k + 2 * j + 1 < c_len ? static_cast<uint32_t>(a[2 * j + 1]) << 16 : 0u);
-                }
-            }
+            for (int j = 0; j < 4; ++j) h[i][j] = u[j], h[i][4 + j] = v[j];
         }
     }
 
     static __device__ __forceinline__ void stage_store(const Held &h, uint8_t *tile) {
+        static_assert(PA == 3);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int id = i * kBlockThreads + threadIdx.x;
             if (id >= kRows * 8) break;
             const int at = lds_piece(id / 8, id & 7);
             u32x4 v[PA];
-            if constexpr (PA == 3) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t w[3];
-                    to_parts<3>(as_f(h[i][2 * j]), as_f(h[i][2 * j + 1]), w);
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[3];
+                to_parts<3>(as_f(h[i][2 * j]), as_f(h[i][2 * j + 1]), w);
 #pragma unroll
-                    for (int a = 0; a < 3; ++a) v[a][j] = w[a];
-                }
-            } else {
-                v[0] = u32x4{h[i][0], h[i][1], h[i][2], h[i][3]};
+                for (int a = 0; a < 3; ++a) v[a][j] = w[a];
             }
 #pragma unroll
             for (int a = 0; a < PA; ++a) *reinterpret_cast<u32x4 *>(tile + a * kPlane + at) = v[a];
