@@ -62,12 +62,15 @@
 namespace zpp {
 
 // acc += A B. PIN keeps the sums in accumulation registers: 256 of them leave
-// the compiler's allocator none to move one through, and it then moves them
-// through the others and memory. The instruction is written out for that, so
-// the compiler does not know that operands written by ordinary instructions
-// have to be two wait states old: operands_ready() stands before every run of
-// these, and within a run nothing but LDS reads (which are waited for) writes
-// an operand.
+// the compiler's allocator none to move one through, and in the loop it then
+// moves them through the others and memory. (Outside the loop, the bf16 kernels of
+// 64 to 256 rows copy sums where their paths meet, and those of 128 rows put one
+// or two addresses into scratch memory before the loop and fetch them after it.)
+// The instruction is written out for that, so the compiler does not know that
+// operands written by ordinary instructions have to be two wait states old:
+// operands_ready() stands before every run of these, and within a run nothing
+// but LDS reads (which are waited for) writes an operand. Nor does it know how
+// long the sums have to be left alone: sums_ready().
 template <bool PIN>
 __device__ __forceinline__ void mfma(u32x4 a, u32x4 b, f32x4 &acc) {
     if constexpr (PIN)
@@ -85,11 +88,16 @@ __device__ __forceinline__ void operands_ready() {
     }
 }
 
-// After the last mfma<true>: the wait states before ordinary instructions may
-// read the sums.
+// After a run of mfma<true>, in the same basic block: the eight wait states
+// before anything but another product may read or write the sums, a copy that
+// the compiler makes where control flow meets among them.
 template <bool PIN>
-__device__ __forceinline__ void settle(f32x4 &acc) {
-    if constexpr (PIN) asm volatile("s_nop 15\n\ts_nop 3" : "+a"(acc));
+__device__ __forceinline__ void sums_ready() {
+    if constexpr (PIN) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 7");
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // A barrier that waits for no memory operation of the wave's own: neither the
@@ -531,6 +539,7 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
                 step(i + 2, raw[2], raw[3]);
                 step(i + 3, raw[3], raw[0]);
             }
+            sums_ready<L::kPin>();
         }
         wait_loads();
     }
@@ -553,12 +562,11 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
             L::template products<0, 4>(x, b0, acc[m]);
             L::template products<0, 4>(y, b1, acc[m]);
         }
+        sums_ready<L::kPin>();
     }
 
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) settle<L::kPin>(acc[m][t]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t row = m0 + m * 16 + 4 * q + i;
