@@ -12,7 +12,10 @@ The short helpers (:func:`quantize`, :func:`dequantize`, :func:`reorder`,
 :func:`dequant_reduce_requant`, :func:`dequant_reduce_average`,
 :func:`quantize_reordered`, :func:`linear`, :func:`linear_grad`,
 :func:`layer_norm`, :func:`layer_norm_grad`) allocate their outputs with torch on the
-input's device and call the same entry points.
+input's device and call the same entry points. With ``stream`` they do so as
+under ``torch.cuda.stream(stream)``: what they allocate is that stream's, so it
+is not handed out again while the stream still uses it. When the inputs are
+ready for that stream, and its results for others, is the caller's to order.
 
 Importing the package fails with ``ImportError`` when ``libzpp.so`` has not
 been built (``python block_quantization_codec_amd/_build.py``); there is no
@@ -121,6 +124,28 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _under(stream, helper, *args):
+    """``helper(*args)`` with ``stream`` as torch's current one, so that what it
+    allocates, temporaries too, belongs to the stream that uses it. Its arguments
+    stay valid for the work on that stream, and its results for the caller's
+    current one, whichever of them is freed first."""
+    import torch
+
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = helper(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and t.is_cuda:
+            t.record_stream(caller)
+    return out
 
 
 def _call(name: str, *args) -> None:
@@ -242,6 +267,8 @@ def _need_contiguous(**tensors) -> None:
 
 def quantize(x, block: int, bits: int, stream=None):
     """Block-quantize a contiguous bf16/fp32 device tensor. Returns (codes uint8, scales fp32)."""
+    if stream is not None:
+        return _under(stream, quantize, x, block, bits)
     import torch
 
     _need_contiguous(x=x)
@@ -257,6 +284,8 @@ def quantize_reordered(x, n_nodes: int, gpus_per_node: int, block: int, bits: in
     """Quantize the tensor-slice reordered view of contiguous x (N equal slices)
     without writing the reordered tensor. Returns (codes, scales) of output slices
     [first_slice, first_slice + n_slices)."""
+    if stream is not None:
+        return _under(stream, quantize_reordered, x, n_nodes, gpus_per_node, block, bits, first_slice, n_slices)
     import torch
 
     _need_contiguous(x=x)
@@ -275,6 +304,8 @@ def quantize_reordered(x, n_nodes: int, gpus_per_node: int, block: int, bits: in
 
 def dequantize(codes, scales, bits: int, numel: int, block: int, dtype=None, stream=None):
     """Rebuild ``numel`` values (bf16 by default, or fp32) from codes and scales."""
+    if stream is not None:
+        return _under(stream, dequantize, codes, scales, bits, numel, block, dtype)
     import torch
 
     _need_contiguous(codes=codes, scales=scales)
@@ -286,6 +317,8 @@ def dequantize(codes, scales, bits: int, numel: int, block: int, dtype=None, str
 
 def reorder(t, n_nodes: int, gpus_per_node: int, stream=None):
     """Reorder the n_nodes*gpus_per_node equal slices of a contiguous device tensor."""
+    if stream is not None:
+        return _under(stream, reorder, t, n_nodes, gpus_per_node)
     import torch
 
     _need_contiguous(t=t)
@@ -304,6 +337,9 @@ def dequant_reduce_requant(codes_in, scales_in, n_inputs: int, bits_in: int, num
     """Sum ``n_inputs`` quantized pieces laid side by side (strides default to one
     piece) and optionally requantize. Returns (codes_out, scales_out, sum_out),
     with None for outputs not requested."""
+    if stream is not None:
+        return _under(stream, dequant_reduce_requant, codes_in, scales_in, n_inputs, bits_in, numel, block,
+                      bits_out, want_sum, codes_stride_bytes, scales_stride)
     import torch
 
     _need_contiguous(codes_in=codes_in, scales_in=scales_in)
@@ -329,6 +365,9 @@ def dequant_reduce_requant_split(codes_in, scales_in, n_inputs: int, bits_in: in
     [keep_begin, keep_begin + keep_elems) (whole blocks) to the kept pair, all
     others, in order, to the send pair. Returns (send_codes, send_scales,
     keep_codes, keep_scales), with None for an empty pair."""
+    if stream is not None:
+        return _under(stream, dequant_reduce_requant_split, codes_in, scales_in, n_inputs, bits_in, numel, block,
+                      keep_begin, keep_elems, bits_out, codes_stride_bytes, scales_stride)
     import torch
 
     _need_contiguous(codes_in=codes_in, scales_in=scales_in)
@@ -349,6 +388,9 @@ def dequant_reduce_average(codes_in, scales_in, n_inputs: int, bits_in: int, num
                            codes_stride_bytes: int | None = None, scales_stride: int | None = None, stream=None):
     """Sum ``n_inputs`` quantized pieces laid side by side and divide by ``divisor``
     (the number of contributing GPUs). Returns the fp32 average."""
+    if stream is not None:
+        return _under(stream, dequant_reduce_average, codes_in, scales_in, n_inputs, bits_in, numel, block, divisor,
+                      codes_stride_bytes, scales_stride)
     import torch
 
     _need_contiguous(codes_in=codes_in, scales_in=scales_in)
@@ -441,9 +483,9 @@ def linear(x, codes, scales, bits: int, block: int, out_features: int, dtype=Non
     """x @ W.T for x [..., in_features] and the [out_features, in_features] weight
     that ``quantize`` turned into codes and scales. The result is of ``dtype``
     (x's by default), or written into ``out``. ``workspace``, if given, is a
-    device tensor of at least ``zpp_linear_blocks_workspace`` bytes; with a
-    ``stream`` that is not torch's current one, pass ``out`` and ``workspace``
-    (memory torch allocates here belongs to its current stream)."""
+    device tensor of at least ``zpp_linear_blocks_workspace`` bytes."""
+    if stream is not None:
+        return _under(stream, linear, x, codes, scales, bits, block, out_features, dtype, out, workspace)
     return _linear("zpp_linear_blocks", 0, x, codes, scales, bits, block, out_features, dtype, out, workspace, stream)
 
 
@@ -451,6 +493,8 @@ def linear_grad(dy, codes, scales, bits: int, block: int, in_features: int, dtyp
                 stream=None):
     """dy @ W: the gradient of :func:`linear` with respect to x, for dy
     [..., out_features]. Arguments as there."""
+    if stream is not None:
+        return _under(stream, linear_grad, dy, codes, scales, bits, block, in_features, dtype, out, workspace)
     return _linear("zpp_linear_blocks_grad", 1, dy, codes, scales, bits, block, in_features, dtype, out, workspace,
                    stream)
 
@@ -479,6 +523,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     """Layer norm over x's last dimension. Returns (y, mean, rstd): y of x's
     shape and dtype (or ``out``), mean and rstd float32, one each per row, as
     :func:`layer_norm_grad` takes them."""
+    if stream is not None:
+        return _under(stream, layer_norm, x, weight, bias, eps, out)
     import torch
 
     rows, width, stride = _rows(x, "x")
@@ -500,6 +546,8 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype
     last two in weight's dtype (``w_dtype``, or x's, when weight is None).
     ``workspace``, if given, is a device tensor of at least
     ``zpp_layer_norm_grad_workspace(rows, width)`` bytes."""
+    if stream is not None:
+        return _under(stream, layer_norm_grad, dy, x, weight, mean, rstd, out, workspace, w_dtype)
     import torch
 
     rows, width, stride = _rows(x, "x")
