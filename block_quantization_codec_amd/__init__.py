@@ -455,6 +455,8 @@ def _workspace(workspace, need: int, like):
         import torch
 
         workspace = like.new_empty(need, dtype=torch.uint8)
+    elif not workspace.is_contiguous():  # it would be taken for as many bytes from its first one on
+        raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
