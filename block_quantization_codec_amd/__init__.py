@@ -510,6 +510,15 @@ def _vector(v, width: int, name: str):
     return v.data_ptr(), _code(v.dtype)
 
 
+def _buffer(t, shape, dtype, name: str, x):
+    """``t``, for a result of that shape and dtype, or a new tensor on x's device."""
+    if t is None:
+        return x.new_empty(shape, dtype=dtype)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)} and {dtype}")
+    return t
+
+
 def _like(out, x):
     """``out`` (or a new tensor) of x's shape and dtype, and its row stride."""
     if out is None:
@@ -521,12 +530,12 @@ def _like(out, x):
     return out, _rows(out, "out")[2]
 
 
-def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None, mean=None, rstd=None):
     """Layer norm over x's last dimension. Returns (y, mean, rstd): y of x's
     shape and dtype (or ``out``), mean and rstd float32, one each per row, as
-    :func:`layer_norm_grad` takes them."""
+    :func:`layer_norm_grad` takes them (new tensors, or those passed in)."""
     if stream is not None:
-        return _under(stream, layer_norm, x, weight, bias, eps, out)
+        return _under(stream, layer_norm, x, weight, bias, eps, out, None, mean, rstd)
     import torch
 
     rows, width, stride = _rows(x, "x")
@@ -536,20 +545,22 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     if wdt and bdt and wdt != bdt:
         raise TypeError("weight and bias must be of one dtype")
     out, ostride = _like(out, x)
-    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    rstd = torch.empty_like(mean)
+    mean = _buffer(mean, x.shape[:-1], torch.float32, "mean", x)
+    rstd = _buffer(rstd, x.shape[:-1], torch.float32, "rstd", x)
     _call("zpp_layer_norm", x.data_ptr(), xdt, stride, rows, width, w, b, wdt or bdt or xdt, eps, out.data_ptr(),
           ostride, mean.data_ptr(), rstd.data_ptr(), _stream(stream))
     return out, mean, rstd
 
 
-def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype=None, stream=None):
+def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype=None, stream=None, dweight=None,
+                    dbias=None):
     """Backward pass of :func:`layer_norm`. Returns (dx, dweight, dbias); the
-    last two in weight's dtype (``w_dtype``, or x's, when weight is None).
+    last two in weight's dtype (``w_dtype``, or x's, when weight is None), in
+    new tensors or in those passed in.
     ``workspace``, if given, is a device tensor of at least
     ``zpp_layer_norm_grad_workspace(rows, width)`` bytes."""
     if stream is not None:
-        return _under(stream, layer_norm_grad, dy, x, weight, mean, rstd, out, workspace, w_dtype)
+        return _under(stream, layer_norm_grad, dy, x, weight, mean, rstd, out, workspace, w_dtype, None, dweight, dbias)
     import torch
 
     rows, width, stride = _rows(x, "x")
@@ -563,8 +574,8 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype
     wt = weight.dtype if weight is not None else (w_dtype or x.dtype)
     xdt, wdt, dy_stride = _code(x.dtype), _code(wt), _rows(dy, "dy")[2]
     out, ostride = _like(out, x)
-    dw = x.new_empty(width, dtype=wt)
-    db = torch.empty_like(dw)
+    dw = _buffer(dweight, (width,), wt, "dweight", x)
+    db = _buffer(dbias, (width,), wt, "dbias", x)
     need = _lib.zpp_layer_norm_grad_workspace(rows, width) if workspace is None else 0
     ws, ws_bytes, keep = _workspace(workspace, need, x)
     _call("zpp_layer_norm_grad", dy.data_ptr(), dy_stride, x.data_ptr(), xdt, stride, rows, width, w, wdt,

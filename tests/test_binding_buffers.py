@@ -27,3 +27,27 @@ def test_a_workspace_with_gaps_or_repeats_is_refused(z, view, monkeypatch):
         z.linear_grad(dy, codes, scales, 4, 32, 32, workspace=ws)
     with pytest.raises(ValueError):
         z.layer_norm_grad(x, x, None, stats, stats, workspace=ws)
+
+
+def test_norm_results_go_where_they_are_asked_for(z, monkeypatch):
+    calls = []
+    monkeypatch.setattr(z, "_call", lambda name, *args: calls.append(args))
+    monkeypatch.setattr(z, "_stream", lambda stream: 0)
+    x, w, mean, rstd = torch.zeros(5, 8, 32), torch.ones(32, dtype=torch.bfloat16), torch.empty(5, 8), torch.empty(5, 8)
+    _, m, r = z.layer_norm(x, w, w, mean=mean, rstd=rstd)
+    assert m is mean and r is rstd and calls[-1][-3:-1] == (mean.data_ptr(), rstd.data_ptr())
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    _, a, b = z.layer_norm_grad(x, x, w, mean, rstd, dweight=dw, dbias=db)
+    assert a is dw and b is db and calls[-1][-5:-3] == (dw.data_ptr(), db.data_ptr())
+    n = len(calls)
+    for bad in (torch.empty(5, 7), torch.empty(40), torch.empty(5, 8, dtype=torch.float64), torch.empty(8, 5).t()):
+        with pytest.raises(ValueError):
+            z.layer_norm(x, w, w, mean=bad)
+        with pytest.raises(ValueError):
+            z.layer_norm(x, w, w, rstd=bad)
+    for bad in (torch.empty(32), dw[:31], torch.empty(64, dtype=dw.dtype)[::2]):
+        with pytest.raises(ValueError):
+            z.layer_norm_grad(x, x, w, mean, rstd, dweight=bad)
+        with pytest.raises(ValueError):
+            z.layer_norm_grad(x, x, w, mean, rstd, dbias=bad)
+    assert len(calls) == n
