@@ -5,6 +5,9 @@
 //
 // Codes are exact in bf16, so the inner sums have no rounding but the binary32
 // accumulation, and the scale multiplies each chunk's sum in binary32.
+// 4-bit codes are converted one by one: pairs made by bit operations alone carry
+// an offset, whose sum with a large activation leaves little of the others' even
+// where the code there is zero, and they saved 3% of the time of one row.
 //
 // A wave reads NT tiles of 16 output features, U chunks of 128 indices at a
 // time. WIDE: every chunk lies in one block (block >= 128 and in_features a
@@ -19,22 +22,6 @@ namespace zpp {
 
 constexpr int kChunk = 128;
 
-// BIAS: 4-bit codes become bf16 in pairs by bit operations alone: bf16 holds
-// 16 + u exactly for u = 0..15, with u in its upper mantissa bits, so code + 24
-// is the code's nibble with its top bit flipped, shifted into place under the
-// exponent of 16. -24 times the sum of x, which the matrix instruction makes
-// itself from a constant operand, is added to each chunk's sum: about one
-// instruction a code in place of two, all of it exact but the binary32 sums,
-// whose terms are 4 to 5 times larger for it. That is far below what a bf16
-// result can show; for binary32 results codes are converted one by one. A
-// dword's nibbles come out as pairs (p, p + 4), so x is dealt in that order too.
-constexpr uint32_t kBiasPair = 0xC1C0C1C0u;  // -24, -24 in bf16
-
-__device__ __forceinline__ uint32_t code4_pair(uint32_t w, int p) {
-    const uint32_t at = p == 0 ? w << 3 : w >> (4 * p - 3);
-    return ((at & 0x00780078u) ^ 0x00400040u) | 0x41804180u;
-}
-
 // One scale a lane, of row (lane & 15) and of the quarter's chunk, to four
 // scales of the row, the same in all quarters.
 __device__ __forceinline__ void spread(float v, float (&s)[4]) {
@@ -44,32 +31,24 @@ __device__ __forceinline__ void spread(float v, float (&s)[4]) {
     s[0] = as_f(a[0]), s[1] = as_f(b[0]), s[2] = as_f(a[1]), s[3] = as_f(b[1]);
 }
 
-// 8 activations (as loaded: 16 bytes of bf16, 32 of binary32) as bf16 parts, in
-// the order of the codes' pairs.
-template <bool BIAS, int PA>
-__device__ __forceinline__ void deal(const u32x4 (&v)[PA == 3 ? 2 : 1], u32x4 (&x)[PA]) {
+// 8 activations (as loaded: 16 bytes of bf16, 32 of binary32) as bf16 parts.
+template <int PA>
+__device__ __forceinline__ void parts_of(const u32x4 (&v)[PA == 3 ? 2 : 1], u32x4 (&x)[PA]) {
     if constexpr (PA == 3) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = BIAS ? j : 2 * j, f = BIAS ? j + 4 : 2 * j + 1;
             uint32_t w[3];
-            to_parts<3>(as_f(v[e / 4][e % 4]), as_f(v[f / 4][f % 4]), w);
+            to_parts<3>(as_f(v[j / 2][2 * (j % 2)]), as_f(v[j / 2][2 * (j % 2) + 1]), w);
 #pragma unroll
             for (int a = 0; a < 3; ++a) x[a][j] = w[a];
         }
-    } else if constexpr (BIAS) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            x[0][j] = __builtin_amdgcn_perm(v[0][2 + j / 2], v[0][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
     } else {
         x[0] = v[0];
     }
 }
 
-template <int BITS, int NT, int U, bool WIDE, bool BIAS>
+template <int BITS, int NT, int U, bool WIDE>
 struct CodeStream {
-    static_assert(!BIAS || BITS == 4, "8-bit codes have no room for one");
-    static constexpr float kScale = BIAS ? 1.0f : kCodeScale<BITS>;  // what the sums are multiplied by at the end
     static constexpr int kUnit = WIDE ? 7 : 5;    // log2 of the indices of one scale
     static constexpr int kS = WIDE ? (U + 3) / 4 : U;  // loads of scales, four a load
     static constexpr int kW = BITS == 4 ? 4 : 8;  // dwords of a chunk's codes
@@ -96,7 +75,7 @@ struct CodeStream {
         for (int t = 0; t < NT; ++t) {
             const uint32_t n =
                 static_cast<uint32_t>(min(static_cast<int64_t>(t * 16 + (lane & 15)), p.n_out - 1 - n0));
-            // 16 bytes a quarter in each 64-byte run; 8 codes a quarter of each 32. Up to 32 rows of 2^26 codes.
+            // 16 bytes a quarter in each 64-byte run; 8 codes a quarter of each 32. Up to 32 rows of 2^22 codes.
             static_assert(NT <= 2, "offsets are 32-bit");
             a.code[t] = n * static_cast<uint32_t>(p.n_in * BITS / 8) + q * (WIDE ? 16 : BITS);
             a.unit[t] = rem + n * static_cast<uint32_t>(units);
@@ -176,7 +155,7 @@ struct CodeStream {
     // A chunk's sums before they are scaled.
     template <int MT>
     struct Sums {
-        f32x4 v[NT][MT], bias[MT];
+        f32x4 v[NT][MT];
     };
 
     // Instruction s of chunk u for all the rows, whose operands are a; acc takes
@@ -185,25 +164,19 @@ struct CodeStream {
     static __device__ __forceinline__ void step(const Chunks &c, int u, int s, const float (&scale)[kS][NT][4],
                                                 const u32x4 (&a)[MT][PA], Sums<MT> &sum, f32x4 (&acc)[NT][MT]) {
         const f32x4 zero = {0, 0, 0, 0};
-        const u32x4 pair[1] = {u32x4{kBiasPair, kBiasPair, kBiasPair, kBiasPair}};
         const bool first = !WIDE || s == 0, last = !WIDE || s == 3;
         u32x4 b[NT][1];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if constexpr (BIAS) {
-                    b[t][0][j] = code4_pair(c.w[u][t][s], j);
-                } else {
-                    constexpr int per = 32 / BITS;
-                    const int i = 8 * s + 2 * j;
-                    b[t][0][j] = pack_hi(code_f32<BITS>(c.w[u][t][i / per], i % per),
-                                         code_f32<BITS>(c.w[u][t][i / per], i % per + 1));
-                }
+                constexpr int per = 32 / BITS;
+                const int i = 8 * s + 2 * j;
+                b[t][0][j] = pack_hi(code_f32<BITS>(c.w[u][t][i / per], i % per),
+                                     code_f32<BITS>(c.w[u][t][i / per], i % per + 1));
             }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            if constexpr (BIAS) sum.bias[m] = mfma_parts<PA, 1>(a[m], pair, first ? zero : sum.bias[m]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 sum.v[t][m] = mfma_parts<PA, 1>(a[m], b[t], first ? zero : sum.v[t][m]);
@@ -211,8 +184,7 @@ struct CodeStream {
                 const float f = WIDE ? scale[u / 4][t][u % 4] : scale[u][t][s];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[t][m][i] =
-                        __builtin_fmaf(BIAS ? sum.v[t][m][i] + sum.bias[m][i] : sum.v[t][m][i], f, acc[t][m][i]);
+                    acc[t][m][i] = __builtin_fmaf(sum.v[t][m][i], f, acc[t][m][i]);
             }
         }
     }

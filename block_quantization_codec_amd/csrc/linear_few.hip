@@ -3,14 +3,14 @@
 //
 // Every code is read once from HBM by one wave, 16 bytes a lane, and used for
 // all rows; even with one row the matrix instruction costs less than
-// multiply-adds would: about one instruction a code makes 4-bit codes bf16
+// multiply-adds would: some 1.6 instructions a code make 4-bit codes bf16
 // pairs, for any number of rows. A wave has NT tiles of 16 output features;
 // the WK waves of a workgroup take U chunks of 128 indices in turn and join
 // their sums in LDS at the end, in wave order.
 //
-// One row of 28672 x 8192 int4: 27 to 28 us, 4.4 TB/s of codes and scales, the
-// vector instructions of the conversion 0.58 of the time (4 rows: 34 us); 1024 x
-// 8192: 5.3 us, of which the launch, a load's round trip and the join are most.
+// One row of 28672 x 8192 int4: 28.5 us, 4.4 TB/s of codes and scales (4 rows: 38
+// us); 1024 x 8192: 6.0 us, of which the launch, a load's round trip and the join
+// are most.
 // x in registers and rotated into place takes one load for 16 instructions'
 // operands: loaded for each, x took as much of the path from L2 as the codes
 // and the first case 54 us. Non-temporal loads gained nothing.
@@ -37,9 +37,9 @@ __device__ __forceinline__ void rotate_parts(const u32x4 (&v)[PA], u32x4 (&o)[PA
 // RM is the number of rows of x that lie in one operand (a power of two below
 // 16): the lanes of a quarter load 16 / RM operands' pieces at once, and each
 // operand is a rotation of them.
-template <int BITS, int PA, int NT, int RM, int U, bool WIDE, bool BIAS>
+template <int BITS, int PA, int NT, int RM, int U, bool WIDE>
 struct Few {
-    using C = CodeStream<BITS, NT, U, WIDE, BIAS>;
+    using C = CodeStream<BITS, NT, U, WIDE>;
     static constexpr int kPer = 16 / RM;                  // operands of one load of x
     static constexpr int kX = (4 * U + kPer - 1) / kPer;  // loads of x
     using Raw = u32x4[kX][PA == 3 ? 2 : 1];
@@ -74,9 +74,9 @@ struct Few {
     }
 };
 
-template <int BITS, int PA, int NT, int RM, int U, bool WIDE, bool BIAS, int WK>
+template <int BITS, int PA, int NT, int RM, int U, bool WIDE, int WK>
 __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
-    using F = Few<BITS, PA, NT, RM, U, WIDE, BIAS>;
+    using F = Few<BITS, PA, NT, RM, U, WIDE>;
     using C = typename F::C;
     __shared__ float sums[WK][NT * 256];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
         C::scales(p, k, c, scale);
         u32x4 x[F::kX][PA];
 #pragma unroll
-        for (int l = 0; l < F::kX; ++l) deal<BIAS, PA>(raw[l], x[l]);
+        for (int l = 0; l < F::kX; ++l) parts_of<PA>(raw[l], x[l]);
         F::template use_from<0>(x, c, scale, acc);
     }
 
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < WK; ++k) v += sums[k][o];
-        v *= C::kScale;
+        v *= kCodeScale<BITS>;
         if (p.out_f32)
             static_cast<float *>(p.out)[row_out * p.ldo + col] = v;
         else
@@ -125,38 +125,30 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
     }
 }
 
-template <int BITS, int PA, bool BIAS, int RM>
+template <int BITS, int PA, int RM>
 hipError_t launch_as(const LinArgs &p, bool wide, hipStream_t stream) {
     constexpr int NT = 1, U = 4, WK = 8;
     const unsigned grid = static_cast<unsigned>((p.n_out + 16 * NT - 1) / (16 * NT));
     if (wide)
-        linear_few_kernel<BITS, PA, NT, RM, U, true, BIAS, WK><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, true, WK><<<grid, WK * kWave, 0, stream>>>(p);
     else
-        linear_few_kernel<BITS, PA, NT, RM, U, false, BIAS, WK><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, false, WK><<<grid, WK * kWave, 0, stream>>>(p);
     return hipGetLastError();
 }
 
-template <int BITS, int PA, bool BIAS>
-hipError_t launch_rows(const LinArgs &p, bool wide, hipStream_t stream) {
-    if (p.rows == 1) return launch_as<BITS, PA, BIAS, 1>(p, wide, stream);
-    if (p.rows == 2) return launch_as<BITS, PA, BIAS, 2>(p, wide, stream);
-    return launch_as<BITS, PA, BIAS, 4>(p, wide, stream);
-}
-
 template <int BITS, int PA>
-hipError_t launch_out(const LinArgs &p, bool wide, hipStream_t stream) {
-    if constexpr (BITS == 4) {
-        if (!p.out_f32) return launch_rows<BITS, PA, true>(p, wide, stream);
-    }
-    return launch_rows<BITS, PA, false>(p, wide, stream);
+hipError_t launch_rows(const LinArgs &p, bool wide, hipStream_t stream) {
+    if (p.rows == 1) return launch_as<BITS, PA, 1>(p, wide, stream);
+    if (p.rows == 2) return launch_as<BITS, PA, 2>(p, wide, stream);
+    return launch_as<BITS, PA, 4>(p, wide, stream);
 }
 
 }  // namespace
 
 hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream) {
     const bool wide = p.log2b >= 7 && p.n_in % kChunk == 0;
-    if (bits == 4) return a_f32 ? launch_out<4, 3>(p, wide, stream) : launch_out<4, 1>(p, wide, stream);
-    return a_f32 ? launch_out<8, 3>(p, wide, stream) : launch_out<8, 1>(p, wide, stream);
+    if (bits == 4) return a_f32 ? launch_rows<4, 3>(p, wide, stream) : launch_rows<4, 1>(p, wide, stream);
+    return a_f32 ? launch_rows<8, 3>(p, wide, stream) : launch_rows<8, 1>(p, wide, stream);
 }
 
 }  // namespace zpp

@@ -10,7 +10,7 @@
 // split over workgroups to fill the GPU and a second kernel joins the parts.
 //
 // 16 rows of 8192 x 28672 int8: 56 us, 4.2 TB/s of codes, near what the memory
-// gives; 64 rows of 28672 x 8192 int4: 68 us, and 333 of 4096 x 11008 int8 to
+// gives; 64 rows of 28672 x 8192 int4: 61 us, and 333 of 4096 x 11008 int8 to
 // binary32: 67 to 74 us, where conversion and matrix instructions of the two
 // waves that a SIMD holds take the time (conversion is shared by 64 rows only).
 // Where the pieces of x lie is found once: found in every step it took 8% more.
@@ -21,10 +21,10 @@
 namespace zpp {
 namespace {
 
-template <int BITS, int PA, int NT, int MT, int U, bool WIDE, bool BIAS>
+template <int BITS, int PA, int NT, int MT, int U, bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
     constexpr bool ASYNC = PA == 1;
-    using C = CodeStream<BITS, NT, U, WIDE, BIAS>;
+    using C = CodeStream<BITS, NT, U, WIDE>;
     using T = LinTile<PA, MT>;
     constexpr int kTile = PA * T::kPlane;
     __shared__ __attribute__((aligned(128))) uint8_t tiles[2][2 * U][kTile];
@@ -90,12 +90,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
             for (int m = 0; m < MT; ++m) {
                 const int piece = lds_piece(m * 16 + (lane & 15), (at_k & 63) >> 3);
 #pragma unroll
-                for (int x = 0; x < PA; ++x) {  // the parts are bf16 already: each is dealt like one
-                    const u32x4 v[1] = {*reinterpret_cast<const u32x4 *>(tile + x * T::kPlane + piece)};
-                    u32x4 o[1];
-                    deal<BIAS, 1>(v, o);
-                    a[m][x] = o[0];
-                }
+                for (int x = 0; x < PA; ++x) a[m][x] = *reinterpret_cast<const u32x4 *>(tile + x * T::kPlane + piece);
             }
             C::template step<PA, MT>(c, i / 4, i % 4, scale, a, sum, acc);
         }
@@ -114,7 +109,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
             for (int i = 0; i < 4; ++i) {
                 const int64_t row = m0 + m * 16 + 4 * q + i;
                 if (row >= p.rows || col >= p.n_out) continue;
-                const float v = acc[t][m][i] * C::kScale;
+                const float v = acc[t][m][i] * kCodeScale<BITS>;
                 if (p.splits > 1)
                     p.partial[(split * p.rows + row) * ((p.n_out + 3) & ~INT64_C(3)) + col] = v;
                 else if (p.out_f32)
@@ -125,38 +120,30 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
     }
 }
 
-template <int BITS, int PA, bool BIAS, int MT>
+template <int BITS, int PA, int MT>
 hipError_t launch_as(const LinArgs &p, bool wide, hipStream_t stream) {
     constexpr int U = PA == 1 ? kMidChunks : 1;  // three parts of 64 rows fill LDS as they are
     const unsigned grid = static_cast<unsigned>(p.row_tiles * p.col_tiles * p.splits);
     if (wide)
-        linear_mid_kernel<BITS, PA, kMidTiles, MT, U, true, BIAS><<<grid, kBlockThreads, 0, stream>>>(p);
+        linear_mid_kernel<BITS, PA, kMidTiles, MT, U, true><<<grid, kBlockThreads, 0, stream>>>(p);
     else
-        linear_mid_kernel<BITS, PA, kMidTiles, MT, U, false, BIAS><<<grid, kBlockThreads, 0, stream>>>(p);
+        linear_mid_kernel<BITS, PA, kMidTiles, MT, U, false><<<grid, kBlockThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
-template <int BITS, int PA, bool BIAS>
-hipError_t launch_rows(const LinArgs &p, bool wide, int mt, hipStream_t stream) {
-    if (mt == 1) return launch_as<BITS, PA, BIAS, 1>(p, wide, stream);
-    if (mt == 2) return launch_as<BITS, PA, BIAS, 2>(p, wide, stream);
-    return launch_as<BITS, PA, BIAS, 4>(p, wide, stream);
-}
-
 template <int BITS, int PA>
-hipError_t launch_out(const LinArgs &p, bool wide, int mt, hipStream_t stream) {
-    if constexpr (BITS == 4) {
-        if (!p.out_f32) return launch_rows<BITS, PA, true>(p, wide, mt, stream);
-    }
-    return launch_rows<BITS, PA, false>(p, wide, mt, stream);
+hipError_t launch_rows(const LinArgs &p, bool wide, int mt, hipStream_t stream) {
+    if (mt == 1) return launch_as<BITS, PA, 1>(p, wide, stream);
+    if (mt == 2) return launch_as<BITS, PA, 2>(p, wide, stream);
+    return launch_as<BITS, PA, 4>(p, wide, stream);
 }
 
 }  // namespace
 
 hipError_t launch_linear_mid(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream) {
     const bool wide = p.log2b >= 7 && p.n_in % kChunk == 0;
-    if (bits == 4) return a_f32 ? launch_out<4, 3>(p, wide, mt, stream) : launch_out<4, 1>(p, wide, mt, stream);
-    return a_f32 ? launch_out<8, 3>(p, wide, mt, stream) : launch_out<8, 1>(p, wide, mt, stream);
+    if (bits == 4) return a_f32 ? launch_rows<4, 3>(p, wide, mt, stream) : launch_rows<4, 1>(p, wide, mt, stream);
+    return a_f32 ? launch_rows<8, 3>(p, wide, mt, stream) : launch_rows<8, 1>(p, wide, mt, stream);
 }
 
 }  // namespace zpp
