@@ -118,6 +118,7 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
 #pragma unroll
         for (int k = 0; k < WK; ++k) v += sums[k][o];
         v *= kCodeScale<BITS>;
+        if (out_of_range(v)) v = scaled_sum<BITS, PA>(p, row_out, col, 0, p.n_in);
         if (p.out_f32)
             static_cast<float *>(p.out)[row_out * p.ldo + col] = v;
         else

@@ -100,6 +100,16 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
         }
     }
 
+    auto store = [&](int64_t row, int64_t col, float v) {
+        if (p.splits > 1)
+            p.partial[(split * p.rows + row) * ((p.n_out + 3) & ~INT64_C(3)) + col] = v;
+        else if (p.out_f32)
+            static_cast<float *>(p.out)[row * p.ldo + col] = v;
+        else
+            static_cast<uint16_t *>(p.out)[row * p.ldo + col] = static_cast<uint16_t>(pack_rn(v, 0.0f));
+    };
+    uint32_t again = 0;  // of the lane's results, those out of range: stored once more at the end
+    static_assert(NT * MT * 4 <= 32, "a bit each");
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int64_t col = n0 + t * 16 + (lane & 15);
@@ -110,13 +120,14 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
                 const int64_t row = m0 + m * 16 + 4 * q + i;
                 if (row >= p.rows || col >= p.n_out) continue;
                 const float v = acc[t][m][i] * kCodeScale<BITS>;
-                if (p.splits > 1)
-                    p.partial[(split * p.rows + row) * ((p.n_out + 3) & ~INT64_C(3)) + col] = v;
-                else if (p.out_f32)
-                    static_cast<float *>(p.out)[row * p.ldo + col] = v;
-                else
-                    static_cast<uint16_t *>(p.out)[row * p.ldo + col] = static_cast<uint16_t>(pack_rn(v, 0.0f));
+                again |= out_of_range(v) ? 1u << ((t * MT + m) * 4 + i) : 0u;
+                store(row, col, v);
             }
+    }
+    for (; again != 0; again &= again - 1) {
+        const int b = __builtin_ctz(again), t = b / (4 * MT), m = b / 4 % MT;
+        const int64_t row = m0 + m * 16 + 4 * q + b % 4, col = n0 + t * 16 + (lane & 15);
+        store(row, col, scaled_sum<BITS, PA>(p, row, col, k0, k1));
     }
 }
 
