@@ -546,7 +546,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         raise TypeError("weight and bias must be of one dtype")
     out, ostride = _like(out, x)
     mean = _buffer(mean, x.shape[:-1], torch.float32, "mean", x)
-    rstd = _buffer(rstd, x.shape[:-1], torch.float32, "rstd", x)
+    rstd = torch.empty_like(mean) if rstd is None else _buffer(rstd, x.shape[:-1], torch.float32, "rstd", x)
     _call("zpp_layer_norm", x.data_ptr(), xdt, stride, rows, width, w, b, wdt or bdt or xdt, eps, out.data_ptr(),
           ostride, mean.data_ptr(), rstd.data_ptr(), _stream(stream))
     return out, mean, rstd
@@ -575,7 +575,7 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype
     xdt, wdt, dy_stride = _code(x.dtype), _code(wt), _rows(dy, "dy")[2]
     out, ostride = _like(out, x)
     dw = _buffer(dweight, (width,), wt, "dweight", x)
-    db = _buffer(dbias, (width,), wt, "dbias", x)
+    db = torch.empty_like(dw) if dbias is None else _buffer(dbias, (width,), wt, "dbias", x)
     need = _lib.zpp_layer_norm_grad_workspace(rows, width) if workspace is None else 0
     ws, ws_bytes, keep = _workspace(workspace, need, x)
     _call("zpp_layer_norm_grad", dy.data_ptr(), dy_stride, x.data_ptr(), xdt, stride, rows, width, w, wdt,
