@@ -332,11 +332,12 @@ zpp_status zpp_linear_blocks_grad(const void *dy, int32_t dy_dtype, int64_t dy_s
 
 /* Bytes of workspace that zpp_linear_blocks (grad == 0) or zpp_linear_blocks_grad
  * (grad != 0) needs for these types, sizes and row stride of its input (any
- * stride that is the row's length or more; it matters only whether rows lie on
- * 16-byte pieces): for the sums of a contraction that is split to share out few
- * tiles of results over the GPU, and for a packed copy of activations of
- * binary32 or of odd lengths or strides. 0 where neither is needed. It depends
- * on the arguments alone; 0 for sizes the calls refuse. */
+ * stride that is the row's length or more; pass the call's own, because rows on
+ * no 16-byte piece, and rows more than 2^22 elements apart, may need more than
+ * others): for the sums of a contraction that is split to share out few tiles of
+ * results over the GPU, and for a packed copy of activations of binary32 or of
+ * such rows. 0 where neither is needed. It depends on the arguments alone, and
+ * fewer rows may need more than many; 0 for sizes the calls refuse. */
 int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
                                     int64_t rows, int64_t out_features, int64_t in_features);
 

@@ -51,3 +51,16 @@ def test_norm_results_go_where_they_are_asked_for(z, monkeypatch):
         with pytest.raises(ValueError):
             z.layer_norm_grad(x, x, w, mean, rstd, dbias=bad)
     assert len(calls) == n
+
+
+def test_workspace_of_far_rows(z):
+    """Rows more than 2^22 elements apart are packed: a query with another stride is no answer for them."""
+    w = z.zpp_linear_blocks_workspace
+    near, edge, far = (w(0, z.ZPP_BF16, s, z.ZPP_BF16, 4096, 8192, 1024) for s in (1024, 1 << 22, (1 << 22) + 8))
+    assert near == edge == 0 and far == 4096 * 1024 * 2
+    # and a query for many rows is none for few: 8 rows have a split contraction, 4096 none
+    assert w(0, z.ZPP_BF16, 8192, z.ZPP_BF16, 8, 1024, 8192) > w(0, z.ZPP_BF16, 8192, z.ZPP_BF16, 4096, 8192, 8192) == 0
+    f = z.library().zpp_linear_blocks
+    a, g = 1 << 40, 1 << 36  # fake addresses: refused before any GPU call is made
+    assert f(a, z.ZPP_BF16, (1 << 22) + 8, 4096, a + g, a + 2 * g, 4, 8192, 1024, 128, a + 3 * g, z.ZPP_BF16, 8192,
+             a + 4 * g, far - 1, None) == z.ZPP_ERR_ARG
