@@ -484,7 +484,10 @@ def linear(x, codes, scales, bits: int, block: int, out_features: int, dtype=Non
            stream=None):
     """x @ W.T for x [..., in_features] and the [out_features, in_features] weight
     that ``quantize`` turned into codes and scales. The result is of ``dtype``
-    (x's by default), or written into ``out``. ``workspace``, if given, is a
+    (x's by default), or written into ``out``. From bf16 to bf16, weights may be
+    rounded to bf16 (past 64 rows, and in the gradient); with a float32 result
+    they are not. Autograd does not see the call: the result never requires a
+    gradient, :func:`linear_grad` gives it. ``workspace``, if given, is a
     device tensor of at least ``zpp_linear_blocks_workspace`` bytes."""
     if stream is not None:
         return _under(stream, linear, x, codes, scales, bits, block, out_features, dtype, out, workspace)
@@ -533,7 +536,8 @@ def _like(out, x):
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None, mean=None, rstd=None):
     """Layer norm over x's last dimension. Returns (y, mean, rstd): y of x's
     shape and dtype (or ``out``), mean and rstd float32, one each per row, as
-    :func:`layer_norm_grad` takes them (new tensors, or those passed in)."""
+    :func:`layer_norm_grad` takes them (new tensors, or those passed in).
+    Autograd does not see the call, as with :func:`linear`."""
     if stream is not None:
         return _under(stream, layer_norm, x, weight, bias, eps, out, None, mean, rstd)
     import torch

@@ -22,11 +22,14 @@
 // Precision. PA and PB are the numbers of bf16 parts of the activations and
 // of the weights. bf16 activations are one part, exactly; binary32 ones are
 // three (24 bits, exactly; packed beforehand, see linear.hip). Weights are
-// RN_bf16(code * s) for bf16 results (the value zpp_dequantize_blocks gives a
-// caller who multiplies in bf16; its rounding, 2^-8 relative at most per
-// product and independent over the contraction, changes a result by about as
-// much as the rounding of the result itself), and three parts of
-// RN(code * s) where input or result is binary32. Sums are binary32 throughout.
+// RN_bf16(code * s) for bf16 results: the value zpp_dequantize_blocks gives a
+// caller who multiplies in bf16. Each is off by at most 2^-8 of itself (equal codes
+// of a block alike), so a result by at most 2^-8 of its products' magnitudes and
+// usually by about as much as its own rounding: 4096 rows of 8192 -> 28672, 2.4e-3
+// of the results' norm in place of 1.7e-3. That is one product in place of the
+// three that a caller gets by asking for binary32 results: weights are three parts
+// of RN(code * s) where input or result is binary32 (forward, bf16 to binary32
+// takes exact codes instead, linear_mid.hip). Sums are binary32 throughout.
 //
 // A step is taken in two halves of 32 indices (one matrix instruction deep).
 // With 256 rows a wave has the SIMD to itself (256 sums a lane), so nothing but

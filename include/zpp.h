@@ -295,10 +295,14 @@ zpp_status zpp_dequant_reduce_average(const void *codes_in, int64_t codes_stride
  * of rows, from one token to a long sequence. Sums are binary32. Where input
  * and output are both ZPP_BF16, the weights may enter the products of more
  * than 64 rows, and enter those of every gradient, as bf16: exactly the values
- * zpp_dequantize_blocks writes as ZPP_BF16. Otherwise nothing is rounded below
- * binary32 but the result. The number of rows chooses kernels, so a row's
- * result can differ by roundings between calls of different numbers of rows;
- * calls of the same sizes give the same bits.
+ * zpp_dequantize_blocks writes as ZPP_BF16, each off by at most 2^-8 of itself.
+ * Otherwise nothing is rounded below binary32 but the result, so a caller who
+ * wants the weights in full asks for a ZPP_FP32 result (three products instead
+ * of one in the gradient). Both statements hold for weights and binary32
+ * activations of magnitude 2^-105 and more; smaller ones may enter with an
+ * absolute error of up to 2^-128. The number of rows chooses kernels, so a row's
+ * result can differ by these roundings between calls of different numbers of
+ * rows; calls of the same sizes give the same bits.
  *
  *   x / dy          in   rows of in_features (dy: out_features) elements of x_dtype, 16-B aligned
  *   x_stride        in   elements from one row to the next, >= the row's length; for x a
