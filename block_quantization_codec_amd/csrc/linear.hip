@@ -79,10 +79,12 @@ double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, i
 // weights in place of three (333 rows of 4096 x 11008 int8: 74 us so, 155 with
 // three parts in tiles). Other products do so where the estimate is below the
 // tiles' (with a binary32 x, the tiles' and their packing's: 10 bytes read and
-// written an element, and a launch of 3 us; with bf16, by a quarter, which is
-// what its estimate misses at 128 to 1024 rows). 70 rows of 1024 x 8192 int4 bf16,
-// 14 us against 21 in tiles; 256 of 8192 x 8192, 69 against 56; 1024 of
-// 4096 x 4096, 64 against 56. binary32: 4019 rows of 512 x 928 int8, 30 us against
+// written an element, and a launch of 3 us; with bf16, by a twelfth: of 120 shapes
+// whose estimates lie within a quarter of each other, all but two are faster so, or
+// equal, from there on, and most are slower below). Exact codes against tiles, bf16,
+// int4: 70 rows of 1024 x 8192, 14 us against 20; 200 of 1024 x 4096, 15 against
+// 22; 80 of 8192 x 2048, 21 against 25; 256 of 8192 x 8192, 62 against 58; 400 of
+// 11008 x 4096, 78 against 71. binary32: 4019 rows of 512 x 928 int8, 30 us against
 // 45; 200 of 4096 x 11008 int8, 131 against 115.
 Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
     Plan p{};
@@ -133,7 +135,7 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
         }
     }
     if (in_f32) least += 3.0 + static_cast<double>(rows * c_len) * 10 / 5.5e6;
-    if (mid.mt != 0 && mid_us * (in_f32 ? 1.0 : 1.25) < least) return mid;
+    if (mid.mt != 0 && mid_us * (in_f32 ? 1.0 : 1.08) < least) return mid;
     p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
     return p;
 }
