@@ -19,9 +19,9 @@
 // the rows and one down the columns.
 //
 // bf16, forward and backward (read + write over the time; the join included):
-// 8192 x 8192, 47 to 52 us (5.2 to 5.7 TB/s) and 84 us (4.8); 4001 x 8191, whose
-// rows start on no 16-byte piece, 39 and 81; 2048 x 28672, 48 and 106. binary32:
-// 8192 x 4096, 48 and 78; 1001 x 4099 backward 17 us, of which the join and its
+// 8192 x 8192, 48 to 52 us (5.2 to 5.6 TB/s) and 84 to 87 us (4.7); 4001 x 8191, whose
+// rows start on no 16-byte piece, 49 (2.7) and 83 (2.4); 2048 x 28672, 49 and 107.
+// binary32: 8192 x 4096, 41 to 48 and 78; 1001 x 4099 backward 17 us, of which the join and its
 // launch are 4. One row of 8192: 4 us, a launch and two round trips to memory.
 //
 // All sums are binary32.

@@ -48,13 +48,13 @@
 // is one guarded step more. Steps are short with few rows, so those go further
 // ahead.
 //
-// 4096 x 8192 by 28672 x 8192 int4, bf16: 1.50 to 1.59 ms, 1.21 to 1.29 PFLOP/s,
-// the matrix units busy for 0.56 of the cycles at the clock that the power
+// 4096 x 8192 by 28672 x 8192 int4, bf16: 1.53 to 1.56 ms, 1.23 to 1.25 PFLOP/s,
+// the matrix units busy for 0.57 of the cycles at the clock that the power
 // limit leaves (2.1 GHz); a library product of bf16 weights of that size takes
 // 1.37 ms. Tried: 128-row tiles (two workgroups a CU: 18% slower, the conversion
 // of each code is shared by half the rows), loads of a step in one burst (+13%),
 // a barrier that drains the loads (+9%). 4096 x 8192 by 8192 x 8192 int8,
-// gradient: 0.45 to 0.48 ms. With few rows one wave a SIMD waits for itself:
+// gradient: 0.46 to 0.48 ms. With few rows one wave a SIMD waits for itself:
 // gradient of 512 x 1024 through 1024 x 8192 int4, 24 us in 16 steps.
 #pragma once
 

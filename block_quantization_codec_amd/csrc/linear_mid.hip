@@ -9,9 +9,9 @@
 // linear_tile.h; few workgroups then cover the features, so the contraction is
 // split over workgroups to fill the GPU and a second kernel joins the parts.
 //
-// 16 rows of 8192 x 28672 int8: 56 us, 4.2 TB/s of codes, near what the memory
-// gives; 64 rows of 28672 x 8192 int4: 61 us, and 333 of 4096 x 11008 int8 to
-// binary32: 67 to 74 us, where conversion and matrix instructions of the two
+// 16 rows of 8192 x 28672 int8: 57 us, 4.2 TB/s of codes, near what the memory
+// gives; 64 rows of 28672 x 8192 int4: 61 to 65 us, and 333 of 4096 x 11008 int8 to
+// binary32: 68 to 75 us, where conversion and matrix instructions of the two
 // waves that a SIMD holds take the time (conversion is shared by 64 rows only).
 // Where the pieces of x lie is found once: found in every step it took 8% more.
 // Reading the operands from LDS an instruction ahead gained nothing.
