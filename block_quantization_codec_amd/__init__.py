@@ -11,7 +11,8 @@ non-OK status raises :class:`ZppError`.
 The short helpers (:func:`quantize`, :func:`dequantize`, :func:`reorder`,
 :func:`dequant_reduce_requant`, :func:`dequant_reduce_average`,
 :func:`quantize_reordered`, :func:`linear`, :func:`linear_grad`,
-:func:`layer_norm`, :func:`layer_norm_grad`) allocate their outputs with torch on the
+:func:`layer_norm`, :func:`layer_norm_grad`, :func:`rms_norm`,
+:func:`rms_norm_grad`) allocate their outputs with torch on the
 input's device and call the same entry points. With ``stream`` they do so as
 under ``torch.cuda.stream(stream)``: what they allocate is that stream's, so it
 is not handed out again while the stream still uses it. When the inputs are
@@ -53,6 +54,7 @@ EXPORTED = ("zpp_quantize_blocks", "zpp_quantize_reordered", "zpp_dequantize_blo
             "zpp_dequant_reduce_requant", "zpp_dequant_reduce_requant_split", "zpp_dequant_reduce_average",
             "zpp_linear_blocks", "zpp_linear_blocks_grad", "zpp_linear_blocks_workspace", "zpp_layer_norm",
             "zpp_layer_norm_grad", "zpp_layer_norm_grad_workspace",
+            "zpp_rms_norm", "zpp_rms_norm_grad", "zpp_rms_norm_grad_workspace",
             "zpp_set_pointer_checks", "zpp_status_string", "zpp_abi_version")
 
 
@@ -81,6 +83,8 @@ def _load() -> ctypes.CDLL:
         "zpp_linear_blocks_grad": [P, I32, I64, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
         "zpp_layer_norm": [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, P, I64, P, P, P],
         "zpp_layer_norm_grad": [P, I64, P, I32, I64, I64, I64, P, I32, P, P, P, I64, P, P, P, I64, P],
+        "zpp_rms_norm": [P, I32, I64, P, I64, I64, I64, P, I32, ctypes.c_float, P, I64, P, I64, P, P, I32, I32, P, P],
+        "zpp_rms_norm_grad": [P, I64, P, I32, I64, P, I64, I64, I64, P, I32, P, P, I64, P, P, I64, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -90,6 +94,8 @@ def _load() -> ctypes.CDLL:
     lib.zpp_linear_blocks_workspace.restype = I64
     lib.zpp_layer_norm_grad_workspace.argtypes = [I64, I64]
     lib.zpp_layer_norm_grad_workspace.restype = I64
+    lib.zpp_rms_norm_grad_workspace.argtypes = [I64, I64]
+    lib.zpp_rms_norm_grad_workspace.restype = I64
     lib.zpp_set_pointer_checks.argtypes = [ctypes.c_int32]
     lib.zpp_set_pointer_checks.restype = ctypes.c_int32
     lib.zpp_status_string.argtypes = [ctypes.c_int]
@@ -230,6 +236,24 @@ def zpp_layer_norm_grad(dy, dy_stride, x, x_dtype, x_stride, rows, width, weight
 
 def zpp_layer_norm_grad_workspace(rows, width) -> int:
     return int(_lib.zpp_layer_norm_grad_workspace(rows, width))
+
+
+def zpp_rms_norm(x, x_dtype, x_stride, residual, residual_stride, rows, width, weight, w_dtype, eps, sum, sum_stride, y,
+                 y_stride, codes, scales, bits, block, rstd, stream=None) -> None:
+    _call("zpp_rms_norm", _ptr(x), x_dtype, x_stride, _ptr(residual), residual_stride, rows, width, _ptr(weight),
+          w_dtype, eps, _ptr(sum), sum_stride, _ptr(y), y_stride, _ptr(codes), _ptr(scales), bits, block, _ptr(rstd),
+          _stream(stream))
+
+
+def zpp_rms_norm_grad(dy, dy_stride, h, x_dtype, h_stride, dsum, dsum_stride, rows, width, weight, w_dtype, rstd, dx,
+                      dx_stride, dweight, workspace, workspace_bytes, stream=None) -> None:
+    _call("zpp_rms_norm_grad", _ptr(dy), dy_stride, _ptr(h), x_dtype, h_stride, _ptr(dsum), dsum_stride, rows, width,
+          _ptr(weight), w_dtype, _ptr(rstd), _ptr(dx), dx_stride, _ptr(dweight), _ptr(workspace), workspace_bytes,
+          _stream(stream))
+
+
+def zpp_rms_norm_grad_workspace(rows, width) -> int:
+    return int(_lib.zpp_rms_norm_grad_workspace(rows, width))
 
 
 def zpp_set_pointer_checks(enabled: bool) -> bool:
@@ -586,3 +610,80 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype
           mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), ostride, dw.data_ptr(), db.data_ptr(), ws, ws_bytes,
           _stream(stream))
     return out, dw, db
+
+
+def _rows_of(t, x, name: str):
+    """(address, row stride) of a matrix of x's shape and dtype, (None, 0) of None."""
+    if t is None:
+        return None, 0
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError(f"{name} must be of x's shape and dtype")
+    return t.data_ptr(), _rows(t, name)[2]
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, bits: int = 0, block: int = 0, want_y: bool = True,
+             out=None, total=None, codes=None, scales=None, rstd=None, stream=None):
+    """Root-mean-square norm over the last dimension of x, or of x + ``residual``.
+    Returns (y, sum, rstd, codes, scales): y of x's shape and dtype (or ``out``;
+    None with ``want_y`` false), sum the x + residual that is normed, rounded to x's
+    dtype (None without a residual), rstd float32, one per row, and with ``bits``
+    the block-quantized y before its own rounding, as :func:`dequantize` takes it
+    (``block`` divides x's last dimension), else None. Results are new tensors, or
+    those passed in as ``out``, ``total``, ``rstd``, ``codes`` and ``scales``.
+    Autograd does not see the call, as with :func:`linear`."""
+    if stream is not None:
+        return _under(stream, rms_norm, x, weight, residual, eps, bits, block, want_y, out, total, codes, scales, rstd)
+    import torch
+
+    rows, width, stride = _rows(x, "x")
+    xdt = _code(x.dtype)
+    w, wdt = _vector(weight, width, "weight")
+    res, res_stride = _rows_of(residual, x, "residual")
+    if (total is not None and residual is None) or (out is not None and not want_y) or \
+            (not bits and (codes is not None or scales is not None)):
+        raise ValueError("a result is passed in that is not asked for")
+    y_ptr, y_stride, sum_ptr, sum_stride = None, 0, None, 0
+    if want_y:
+        out, y_stride = _like(out, x)
+        y_ptr = out.data_ptr()
+    if residual is not None:
+        total, sum_stride = _like(total, x)
+        sum_ptr = total.data_ptr()
+    rstd = _buffer(rstd, x.shape[:-1], torch.float32, "rstd", x)
+    if bits:
+        if block <= 0 or width % block or (bits != 4 and bits != 8):
+            raise ValueError(f"{bits}-bit blocks of {block} do not divide rows of {width}")
+        codes = _buffer(codes, (rows * width * bits // 8,), torch.uint8, "codes", x)
+        scales = _buffer(scales, (rows * width // block,), torch.float32, "scales", x)
+    _call("zpp_rms_norm", x.data_ptr(), xdt, stride, res, res_stride, rows, width, w, wdt or xdt, eps, sum_ptr,
+          sum_stride, y_ptr, y_stride, _ptr(codes), _ptr(scales), bits, block if bits else 0, rstd.data_ptr(),
+          _stream(stream))
+    return out, total, rstd, codes, scales
+
+
+def rms_norm_grad(dy, x, weight, rstd, dsum=None, out=None, workspace=None, w_dtype=None, dweight=None, stream=None):
+    """Backward pass of :func:`rms_norm`; x is what was normed (the sum, where there
+    was a residual) and ``dsum`` the gradient that reaches it by other ways. Returns
+    (dx, dweight): dx the gradient of x and of the residual alike, dweight in
+    weight's dtype (``w_dtype``, or x's, when weight is None).
+    ``workspace``, if given, is a device tensor of at least
+    ``zpp_rms_norm_grad_workspace(rows, width)`` bytes."""
+    if stream is not None:
+        return _under(stream, rms_norm_grad, dy, x, weight, rstd, dsum, out, workspace, w_dtype, dweight)
+    rows, width, stride = _rows(x, "x")
+    import torch
+
+    if not (rstd.is_contiguous() and rstd.numel() == rows and rstd.dtype == torch.float32):
+        raise ValueError("rstd must be contiguous float32, one element per row")
+    w, _ = _vector(weight, width, "weight")
+    wt = weight.dtype if weight is not None else (w_dtype or x.dtype)
+    xdt, wdt = _code(x.dtype), _code(wt)
+    dy_ptr, dy_stride = _rows_of(dy, x, "dy")
+    ds_ptr, ds_stride = _rows_of(dsum, x, "dsum")
+    out, ostride = _like(out, x)
+    dw = _buffer(dweight, (width,), wt, "dweight", x)
+    need = _lib.zpp_rms_norm_grad_workspace(rows, width) if workspace is None else 0
+    ws, ws_bytes, keep = _workspace(workspace, need, x)
+    _call("zpp_rms_norm_grad", dy_ptr, dy_stride, x.data_ptr(), xdt, stride, ds_ptr, ds_stride, rows, width, w, wdt,
+          rstd.data_ptr(), out.data_ptr(), ostride, dw.data_ptr(), ws, ws_bytes, _stream(stream))
+    return out, dw

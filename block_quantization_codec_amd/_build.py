@@ -23,9 +23,9 @@ DRR_UNITS = [f"drr_in{i}_out{o}.hip" for i in (4, 8) for o in (0, 4, 8)]
 LINEAR_UNITS = ["linear_few.hip", "linear_mid.hip",
                 *(f"linear_big_{d}{b}.hip" for d in ("fwd", "grad") for b in (4, 8))]
 SOURCES = ["quantize.hip", "dequantize.hip", "reorder.hip", "drr.hip", *DRR_UNITS, "linear.hip", *LINEAR_UNITS,
-           "layer_norm.hip", "zpp_api.hip"]
+           "layer_norm.hip", "rms_norm.hip", "zpp_api.hip"]
 HEADERS = ["zpp_device.h", "zpp_launch.h", "drr_kernel.h", "linear_device.h", "linear_codes.h",
-           "linear_tile.h", "linear_big.h"]
+           "linear_tile.h", "linear_big.h", "norm_device.h"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -65,7 +65,7 @@ def build(jobs: int | None = None) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     jobs = jobs or max(1, min(len(SOURCES), os.cpu_count() or 1, 16))
     # the units of many kernels take longest: start them first
-    order = sorted(SOURCES, key=lambda f: not f.startswith(("linear_", "layer_norm", "drr_in")))
+    order = sorted(SOURCES, key=lambda f: not f.startswith(("linear_", "layer_norm", "rms_norm", "drr_in")))
     with ThreadPoolExecutor(jobs) as ex:
         objs = list(ex.map(_compile, order))
     tmp = LIB + f".tmp{os.getpid()}"

@@ -525,6 +525,91 @@ int64_t zpp_layer_norm_grad_workspace(int64_t rows, int64_t width) {
     return is_norm_size(rows, width) ? zpp::layer_norm_grad_workspace(rows, width) : 0;
 }
 
+zpp_status zpp_rms_norm(const void *x, int32_t x_dtype, int64_t x_stride, const void *residual,
+                        int64_t residual_stride, int64_t rows, int64_t width, const void *weight, int32_t w_dtype,
+                        float eps, void *sum, int64_t sum_stride, void *y, int64_t y_stride, void *codes,
+                        float *scales, int32_t bits, int32_t block, float *rstd, void *stream) {
+    if (!is_dtype(x_dtype) || !is_dtype(w_dtype)) return ZPP_ERR_ARG;
+    if (bits != 0 && bits != 8 && bits != 4) return ZPP_ERR_ARG;
+    if (!is_norm_size(rows, width)) return ZPP_ERR_ARG;
+    if (!is_stride(x_stride, rows, width)) return ZPP_ERR_ARG;
+    if (residual && !is_stride(residual_stride, rows, width)) return ZPP_ERR_ARG;
+    if (sum && (!residual || !is_stride(sum_stride, rows, width))) return ZPP_ERR_ARG;
+    if (y && !is_stride(y_stride, rows, width)) return ZPP_ERR_ARG;
+    if (bits != 0 && (!is_pow2_block(block) || width % block != 0 || !is_stride(width, rows, width)))
+        return ZPP_ERR_ARG;
+    if (bits == 0 && (codes || scales || (rows > 0 && !y))) return ZPP_ERR_ARG;
+    if (!(eps >= 0.0f) || eps > 3.402823466e38f) return ZPP_ERR_ARG;
+    if (rows == 0) return ZPP_OK;
+    if (!x || !rstd || (bits != 0 && (!codes || !scales))) return ZPP_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) || !aligned(y, 16))
+        return ZPP_ERR_ALIGN;
+    if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(rstd, 4)) return ZPP_ERR_ALIGN;
+    const Range rx = matrix(x, rows, x_stride, width, x_dtype),
+        ri = matrix(residual, rows, residual_stride, width, x_dtype), rw = matrix(weight, 1, width, width, w_dtype),
+        ro = matrix(sum, rows, sum_stride, width, x_dtype), ry = matrix(y, rows, y_stride, width, x_dtype),
+        rc{codes, bits != 0 ? code_bytes(rows * width, bits) : 0},
+        rs{scales, bits != 0 ? 4 * (rows * width / block) : 0}, rr{rstd, 4 * rows};
+    const Range outs[] = {ro, ry, rc, rs, rr};
+    for (int i = 0; i < 5; ++i) {
+        for (const Range &r : {rx, ri, rw})
+            if (overlap(outs[i], r)) return ZPP_ERR_OVERLAP;
+        for (int j = i + 1; j < 5; ++j)
+            if (overlap(outs[i], outs[j])) return ZPP_ERR_OVERLAP;
+    }
+    const Range all[] = {rx, ri, rw, ro, ry, rc, rs, rr};
+    if (zpp_status s = check_all(all); s != ZPP_OK) return s;
+    return launch_checked([&] {
+        return zpp::launch_rms_norm(x, x_dtype == ZPP_FP32, x_stride, residual, residual_stride, rows, width, weight,
+                   w_dtype == ZPP_FP32, eps, sum, sum_stride, y, y_stride, codes, scales, bits,
+                   bits != 0 ? log2_of(block) : 0, rstd, static_cast<hipStream_t>(stream));
+    });
+}
+
+zpp_status zpp_rms_norm_grad(const void *dy, int64_t dy_stride, const void *h, int32_t x_dtype, int64_t h_stride,
+                             const void *dsum, int64_t dsum_stride, int64_t rows, int64_t width, const void *weight,
+                             int32_t w_dtype, const float *rstd, void *dx, int64_t dx_stride, void *dweight,
+                             void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!is_dtype(x_dtype) || !is_dtype(w_dtype)) return ZPP_ERR_ARG;
+    if (!is_norm_size(rows, width)) return ZPP_ERR_ARG;
+    if (!is_stride(dy_stride, rows, width) || !is_stride(h_stride, rows, width) || !is_stride(dx_stride, rows, width))
+        return ZPP_ERR_ARG;
+    if (dsum && !is_stride(dsum_stride, rows, width)) return ZPP_ERR_ARG;
+    const int64_t need = zpp::rms_norm_grad_workspace(rows, width);
+    if (workspace_bytes < need) return ZPP_ERR_ARG;
+    if (rows > 0 && (!dy || !h || !rstd || !dx)) return ZPP_ERR_NULL;
+    if (need > 0 && !workspace) return ZPP_ERR_NULL;
+    if (!aligned(dweight, 16)) return ZPP_ERR_ALIGN;
+    if (rows > 0) {
+        if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(dsum, 16) || !aligned(weight, 16) || !aligned(dx, 16))
+            return ZPP_ERR_ALIGN;
+        if (!aligned(rstd, 4) || !aligned(workspace, 16)) return ZPP_ERR_ALIGN;
+    }
+    const Range rd = matrix(dy, rows, dy_stride, width, x_dtype), rh = matrix(h, rows, h_stride, width, x_dtype),
+        ri = matrix(dsum, rows, dsum_stride, width, x_dtype), rw = matrix(weight, rows > 0, width, width, w_dtype),
+        rr{rstd, 4 * rows}, ro = matrix(dx, rows, dx_stride, width, x_dtype),
+        rdw = matrix(dweight, 1, width, width, w_dtype), rws{workspace, need};
+    const Range outs[] = {ro, rdw, rws};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range &r : {rd, rh, ri, rw, rr})
+            if (overlap(outs[i], r)) return ZPP_ERR_OVERLAP;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlap(outs[i], outs[j])) return ZPP_ERR_OVERLAP;
+    }
+    const Range all[] = {rd, rh, ri, rw, rr, ro, rdw, rws};
+    if (zpp_status s = check_all(all); s != ZPP_OK) return s;
+    if (rows == 0 && !dweight) return ZPP_OK;
+    return launch_checked([&] {
+        return zpp::launch_rms_norm_grad(dy, dy_stride, h, x_dtype == ZPP_FP32, h_stride, dsum, dsum_stride, rows,
+                   width, weight, w_dtype == ZPP_FP32, rstd, dx, dx_stride, dweight, workspace,
+                   static_cast<hipStream_t>(stream));
+    });
+}
+
+int64_t zpp_rms_norm_grad_workspace(int64_t rows, int64_t width) {
+    return is_norm_size(rows, width) ? zpp::rms_norm_grad_workspace(rows, width) : 0;
+}
+
 int32_t zpp_set_pointer_checks(int32_t enabled) {
     return g_pointer_checks.exchange(enabled != 0 ? 1 : 0, std::memory_order_relaxed);
 }

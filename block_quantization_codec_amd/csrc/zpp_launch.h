@@ -49,4 +49,15 @@ hipError_t launch_layer_norm_grad(const void *dy, int64_t dy_stride, const void 
                                   void *workspace, hipStream_t stream);
 int64_t layer_norm_grad_workspace(int64_t rows, int64_t width);
 
+// residual, sum, y and codes may be null (bits 0 without codes).
+hipError_t launch_rms_norm(const void *x, bool f32, int64_t x_stride, const void *residual, int64_t residual_stride,
+                           int64_t rows, int64_t width, const void *weight, bool w_f32, float eps, void *sum,
+                           int64_t sum_stride, void *y, int64_t y_stride, void *codes, float *scales, int bits,
+                           int log2b, float *rstd, hipStream_t stream);
+hipError_t launch_rms_norm_grad(const void *dy, int64_t dy_stride, const void *h, bool f32, int64_t h_stride,
+                                const void *dsum, int64_t dsum_stride, int64_t rows, int64_t width,
+                                const void *weight, bool w_f32, const float *rstd, void *dx, int64_t dx_stride,
+                                void *dweight, void *workspace, hipStream_t stream);
+int64_t rms_norm_grad_workspace(int64_t rows, int64_t width);
+
 }  // namespace zpp

@@ -398,6 +398,72 @@ zpp_status zpp_layer_norm_grad(const void *dy, int64_t dy_stride, const void *x,
 int64_t zpp_layer_norm_grad_workspace(int64_t rows, int64_t width);
 
 /*
+ * Root-mean-square norm over each row of `width` elements, with the addition
+ * that comes before it in a layer and the quantization that may come behind it:
+ *
+ *   h    = x + residual, rounded once to x_dtype (x itself without a residual)
+ *   rstd = 1 / sqrt(sum h^2 / width + eps)
+ *   y    = h * rstd * weight
+ *   codes, scales = the block quantization of the binary32 y (the rule above)
+ *
+ * The norm is that of the rounded h: of what `sum` holds. The codes are those of
+ * y before it is rounded to x_dtype, so with ZPP_FP32 they are exactly what
+ * zpp_quantize_blocks writes for y. Any of sum, y and the codes can be left out, but
+ * not both y and the codes.
+ *
+ *   x, residual  in   rows x width elements of x_dtype each, 16-B aligned; residual may be NULL
+ *   x_stride, residual_stride, sum_stride, y_stride
+ *                in   elements from one row to the next, width..ZPP_MAX_NUMEL (ignored for a NULL matrix)
+ *   rows         in   0..ZPP_MAX_ROWS; 0 is a no-op returning ZPP_OK
+ *   width        in   1..ZPP_MAX_FEATURES
+ *   weight       in   width elements of w_dtype, 16-B aligned, or NULL (ones)
+ *   eps          in   >= 0, finite
+ *   sum          out  h, 16-B aligned, or NULL; NULL without a residual (ZPP_ERR_ARG otherwise)
+ *   y            out  rows x width elements of x_dtype, 16-B aligned, or NULL
+ *   codes, scales, bits, block
+ *                out  as zpp_quantize_blocks writes them for rows * width elements, row after row without gaps:
+ *                     bits 8 or 4, block a block size B that divides width; or NULL, NULL, 0, 0
+ *   rstd         out  rows floats, 4-B aligned: what the backward pass needs
+ *   stream       in   hipStream_t
+ * Everything between the loads and the stores is binary32, but h. Codes and scales of
+ * a row that holds infinite or NaN elements are unspecified (those of other rows are not).
+ */
+zpp_status zpp_rms_norm(const void *x, int32_t x_dtype, int64_t x_stride, const void *residual,
+                        int64_t residual_stride, int64_t rows, int64_t width, const void *weight, int32_t w_dtype,
+                        float eps, void *sum, int64_t sum_stride, void *y, int64_t y_stride, void *codes,
+                        float *scales, int32_t bits, int32_t block, float *rstd, void *stream);
+
+/*
+ * The backward pass of zpp_rms_norm: with xh = h * rstd and g = dy * weight,
+ *
+ *   dx = rstd * (g - xh * sum (g * xh) / width) + dsum
+ *   dweight = sum over rows of dy * xh
+ *
+ * dx is the gradient of x and of residual alike. The sum over rows is binary32, in an
+ * order fixed by the sizes alone, and rounded once to w_dtype: the same inputs give the
+ * same bits.
+ *
+ *   dy, h       in   rows x width elements of x_dtype each, 16-B aligned, with their row strides; h is `sum`, or x
+ *                    where there was no residual
+ *   dsum        in   as dy: the gradient that reaches `sum` by other ways, or NULL (none); its stride is then ignored
+ *   weight      in   as in zpp_rms_norm (NULL: ones)
+ *   rstd        in   as zpp_rms_norm wrote it
+ *   dx          out  rows x width elements of x_dtype, 16-B aligned, dx_stride between rows
+ *   dweight     out  width elements of w_dtype, 16-B aligned, or NULL
+ *   workspace   in   workspace_bytes of memory for this call alone, 16-B aligned (NULL if 0 bytes are needed)
+ *   workspace_bytes  in  at least zpp_rms_norm_grad_workspace(rows, width) (ZPP_ERR_ARG otherwise)
+ *   stream      in   hipStream_t
+ * With rows == 0, dweight is set to zero (the empty sum).
+ */
+zpp_status zpp_rms_norm_grad(const void *dy, int64_t dy_stride, const void *h, int32_t x_dtype, int64_t h_stride,
+                             const void *dsum, int64_t dsum_stride, int64_t rows, int64_t width, const void *weight,
+                             int32_t w_dtype, const float *rstd, void *dx, int64_t dx_stride, void *dweight,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace zpp_rms_norm_grad needs; 0 for sizes it refuses. */
+int64_t zpp_rms_norm_grad_workspace(int64_t rows, int64_t width);
+
+/*
  * Switch the library's HIP-runtime pointer checks on (enabled != 0, the
  * default) or off for the whole process; returns the previous setting (1 or
  * 0). With the checks on, every call asks the HIP runtime, before it
