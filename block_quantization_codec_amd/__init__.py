@@ -11,6 +11,7 @@ non-OK status raises :class:`ZppError`.
 The short helpers (:func:`quantize`, :func:`dequantize`, :func:`reorder`,
 :func:`dequant_reduce_requant`, :func:`dequant_reduce_average`,
 :func:`quantize_reordered`, :func:`linear`, :func:`linear_grad`,
+:func:`linear_grouped`, :func:`linear_grouped_grad`,
 :func:`layer_norm`, :func:`layer_norm_grad`, :func:`rms_norm`,
 :func:`rms_norm_grad`) allocate their outputs with torch on the
 input's device and call the same entry points. With ``stream`` they do so as
@@ -49,10 +50,12 @@ ZPP_MAX_DIVISOR = 1 << 24
 ZPP_MAX_NUMEL = 1 << 40
 ZPP_MAX_FEATURES = 1 << 22
 ZPP_MAX_ROWS = 1 << 30
+ZPP_MAX_GROUPS = 4096
 
 EXPORTED = ("zpp_quantize_blocks", "zpp_quantize_reordered", "zpp_dequantize_blocks", "zpp_reorder_slices",
             "zpp_dequant_reduce_requant", "zpp_dequant_reduce_requant_split", "zpp_dequant_reduce_average",
-            "zpp_linear_blocks", "zpp_linear_blocks_grad", "zpp_linear_blocks_workspace", "zpp_layer_norm",
+            "zpp_linear_blocks", "zpp_linear_blocks_grad", "zpp_linear_blocks_workspace", "zpp_linear_grouped",
+            "zpp_linear_grouped_grad", "zpp_linear_grouped_workspace", "zpp_layer_norm",
             "zpp_layer_norm_grad", "zpp_layer_norm_grad_workspace",
             "zpp_rms_norm", "zpp_rms_norm_grad", "zpp_rms_norm_grad_workspace",
             "zpp_set_pointer_checks", "zpp_status_string", "zpp_abi_version")
@@ -81,6 +84,8 @@ def _load() -> ctypes.CDLL:
         "zpp_dequant_reduce_average": [P, I64, P, I64, I32, I32, I64, I32, I32, P, P],
         "zpp_linear_blocks": [P, I32, I64, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
         "zpp_linear_blocks_grad": [P, I32, I64, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
+        "zpp_linear_grouped": [P, I32, I64, I64, P, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
+        "zpp_linear_grouped_grad": [P, I32, I64, I64, P, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
         "zpp_layer_norm": [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, P, I64, P, P, P],
         "zpp_layer_norm_grad": [P, I64, P, I32, I64, I64, I64, P, I32, P, P, P, I64, P, P, P, I64, P],
         "zpp_rms_norm": [P, I32, I64, P, I64, I64, I64, P, I32, ctypes.c_float, P, I64, P, I64, P, P, I32, I32, P, P],
@@ -92,6 +97,8 @@ def _load() -> ctypes.CDLL:
         f.restype = ctypes.c_int
     lib.zpp_linear_blocks_workspace.argtypes = [I32, I32, I64, I32, I64, I64, I64]
     lib.zpp_linear_blocks_workspace.restype = I64
+    lib.zpp_linear_grouped_workspace.argtypes = [I32, I32, I64, I32, I64, I64, I64, I64]
+    lib.zpp_linear_grouped_workspace.restype = I64
     lib.zpp_layer_norm_grad_workspace.argtypes = [I64, I64]
     lib.zpp_layer_norm_grad_workspace.restype = I64
     lib.zpp_rms_norm_grad_workspace.argtypes = [I64, I64]
@@ -219,6 +226,26 @@ def zpp_linear_blocks_grad(dy, dy_dtype, dy_stride, rows, codes, scales, bits, o
 def zpp_linear_blocks_workspace(grad, in_dtype, in_stride, out_dtype, rows, out_features, in_features) -> int:
     return int(_lib.zpp_linear_blocks_workspace(grad, in_dtype, in_stride, out_dtype, rows, out_features,
                                                 in_features))
+
+
+def zpp_linear_grouped(x, x_dtype, x_stride, rows, offsets, groups, codes, scales, bits, out_features, in_features,
+                       block, y, y_dtype, y_stride, workspace, workspace_bytes, stream=None) -> None:
+    _call("zpp_linear_grouped", _ptr(x), x_dtype, x_stride, rows, _ptr(offsets), groups, _ptr(codes), _ptr(scales), bits,
+          out_features, in_features, block, _ptr(y), y_dtype, y_stride, _ptr(workspace), workspace_bytes,
+          _stream(stream))
+
+
+def zpp_linear_grouped_grad(dy, dy_dtype, dy_stride, rows, offsets, groups, codes, scales, bits, out_features,
+                            in_features, block, dx, dx_dtype, dx_stride, workspace, workspace_bytes,
+                            stream=None) -> None:
+    _call("zpp_linear_grouped_grad", _ptr(dy), dy_dtype, dy_stride, rows, _ptr(offsets), groups, _ptr(codes),
+          _ptr(scales), bits, out_features, in_features, block, _ptr(dx), dx_dtype, dx_stride, _ptr(workspace),
+          workspace_bytes, _stream(stream))
+
+
+def zpp_linear_grouped_workspace(grad, in_dtype, in_stride, out_dtype, rows, groups, out_features, in_features) -> int:
+    return int(_lib.zpp_linear_grouped_workspace(grad, in_dtype, in_stride, out_dtype, rows, groups, out_features,
+                                                 in_features))
 
 
 def zpp_layer_norm(x, x_dtype, x_stride, rows, width, weight, bias, w_dtype, eps, y, y_stride, mean, rstd,
@@ -484,10 +511,11 @@ def _workspace(workspace, need: int, like):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _linear(name: str, grad: int, a, codes, scales, bits, block, out_len, dtype, out, workspace, stream):
+def _linear(name: str, grad: int, a, codes, scales, bits, block, out_len, dtype, out, workspace, stream, offsets=None):
     rows, width, stride = _rows(a, "dy" if grad else "x")
     n_out, n_in = (width, out_len) if grad else (out_len, width)
-    _check_weight(codes, scales, bits, block, n_out * n_in)
+    groups = 1 if offsets is None else _check_offsets(offsets)
+    _check_weight(codes, scales, bits, block, groups * n_out * n_in)
     adt, ostride = _code(a.dtype), out_len
     if out is None:
         dtype = dtype or a.dtype
@@ -497,11 +525,26 @@ def _linear(name: str, grad: int, a, codes, scales, bits, block, out_len, dtype,
         if tuple(out.shape) != (*a.shape[:-1], out_len) or (dtype or out.dtype) != out.dtype:
             raise ValueError(f"out must be of shape {(*a.shape[:-1], out_len)} and of the dtype asked for")
         odt, ostride = _code(out.dtype), _rows(out, "out")[2]
-    need = _lib.zpp_linear_blocks_workspace(grad, adt, stride, odt, rows, n_out, n_in)
+    if offsets is None:
+        need, group_args = _lib.zpp_linear_blocks_workspace(grad, adt, stride, odt, rows, n_out, n_in), ()
+    else:
+        need = _lib.zpp_linear_grouped_workspace(grad, adt, stride, odt, rows, groups, n_out, n_in)
+        group_args = (offsets.data_ptr(), groups)
     ws, ws_bytes, keep = _workspace(workspace, need, a)
-    _call(name, a.data_ptr(), adt, stride, rows, codes.data_ptr(), scales.data_ptr(), bits, n_out, n_in, block,
-          out.data_ptr(), odt, ostride, ws, ws_bytes, _stream(stream))
+    _call(name, a.data_ptr(), adt, stride, rows, *group_args, codes.data_ptr(), scales.data_ptr(), bits, n_out, n_in,
+          block, out.data_ptr(), odt, ostride, ws, ws_bytes, _stream(stream))
     return out
+
+
+def _check_offsets(offsets) -> int:
+    """The number of groups that ``offsets`` begin and end."""
+    import torch
+
+    if offsets.dtype != torch.int32:
+        raise TypeError("offsets must be int32")
+    if offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous, of one dimension, one element more than groups")
+    return offsets.numel() - 1
 
 
 def linear(x, codes, scales, bits: int, block: int, out_features: int, dtype=None, out=None, workspace=None,
@@ -526,6 +569,31 @@ def linear_grad(dy, codes, scales, bits: int, block: int, in_features: int, dtyp
         return _under(stream, linear_grad, dy, codes, scales, bits, block, in_features, dtype, out, workspace)
     return _linear("zpp_linear_blocks_grad", 1, dy, codes, scales, bits, block, in_features, dtype, out, workspace,
                    stream)
+
+
+def linear_grouped(x, offsets, codes, scales, bits: int, block: int, out_features: int, dtype=None, out=None,
+                   workspace=None, stream=None):
+    """As :func:`linear`, each group of rows of x [rows, in_features] by a weight of
+    its own: rows offsets[e] to offsets[e + 1] - 1 by the e-th of the weights whose
+    codes, and scales, lie one behind the other. ``offsets`` is an ascending int32
+    device tensor of one element more than there are weights. Rows before its first
+    element and from its last on are in no group: in ``out`` they stay as they are
+    (in a new tensor they are unspecified)."""
+    if stream is not None:
+        return _under(stream, linear_grouped, x, offsets, codes, scales, bits, block, out_features, dtype, out, workspace)
+    return _linear("zpp_linear_grouped", 0, x, codes, scales, bits, block, out_features, dtype, out, workspace, stream,
+                   offsets)
+
+
+def linear_grouped_grad(dy, offsets, codes, scales, bits: int, block: int, in_features: int, dtype=None, out=None,
+                        workspace=None, stream=None):
+    """dy @ W, group by group: the gradient of :func:`linear_grouped` with respect
+    to x, for dy [rows, out_features]. Arguments as there."""
+    if stream is not None:
+        return _under(stream, linear_grouped_grad, dy, offsets, codes, scales, bits, block, in_features, dtype, out,
+                      workspace)
+    return _linear("zpp_linear_grouped_grad", 1, dy, codes, scales, bits, block, in_features, dtype, out, workspace,
+                   stream, offsets)
 
 
 def _vector(v, width: int, name: str):

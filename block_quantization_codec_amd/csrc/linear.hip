@@ -15,6 +15,11 @@ hipError_t launch_linear_big_fwd4(const LinArgs &p, int parts, int mt, hipStream
 hipError_t launch_linear_big_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream);
 hipError_t launch_linear_big_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
 hipError_t launch_linear_big_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_mid_group(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream);
+hipError_t launch_linear_big_group_fwd4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_group_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_group_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_group_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
 
 namespace {
 
@@ -33,7 +38,16 @@ struct Plan {
     int splits;   // parts of the contraction
     int64_t split_steps;
     int64_t rows; // rows of one launch
+    int64_t groups; // and groups
 };
+
+// Rows of tiles that `rows` rows make; in groups, each has a last tile of its own, on
+// average half full (and a group of few rows is one tile).
+int64_t row_tiles(int64_t rows, int64_t groups, int64_t tile) {
+    if (groups == 0) return ceil_div(rows, tile);
+    const int64_t held = std::min(rows, groups);
+    return std::max(held, rows / tile + held / 2);
+}
 
 // What the parts of a split contraction cost, in microseconds: their writing,
 // reading and joining (5.5 bytes a nanosecond and 4 us).
@@ -58,13 +72,23 @@ double mid_time(bool in_f32, int mt, int64_t tiles, int64_t splits, int64_t spli
 // times steps times a step's time, and the join. A step takes, with the
 // operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured at
 // 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
-double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, int64_t split_steps) {
+double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t groups, int64_t len, int64_t split_steps) {
     static constexpr double step_us[3][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0}};
     const int i = mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3;
-    const double tiles = static_cast<double>(ceil_div(rows, 16 * mt) * ceil_div(len, 256) * splits);
+    const double tiles = static_cast<double>(row_tiles(rows, groups, 16 * mt) * ceil_div(len, 256) * splits);
     // Workgroups that share a CU take about as long as one after the other.
     const double rounds = std::ceil(tiles / kCus);
     return rounds * static_cast<double>(split_steps) * step_us[parts][i] + join_time(splits, rows, len);
+}
+
+// How many rows, and groups, one launch takes: kMaxTiles workgroups.
+void bound_launch(Plan &p, int64_t groups, int64_t col_tiles) {
+    int64_t tiles = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 2);
+    if (groups > 0) {  // each group may have one tile more than its share
+        p.groups = std::min(groups, tiles / 2);
+        tiles -= p.groups;
+    }
+    p.rows = tiles * 16 * p.mt;
 }
 
 // The way of the least time. Measured on the way: 128 rows of 8192 x 8192 int4,
@@ -86,9 +110,13 @@ double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, i
 // 22; 80 of 8192 x 2048, 21 against 25; 256 of 8192 x 8192, 62 against 58; 400 of
 // 11008 x 4096, 78 against 71. binary32: 4019 rows of 512 x 928 int8, 30 us against
 // 45; 200 of 4096 x 11008 int8, 131 against 115.
-Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out, int64_t n_in) {
+//
+// Rows in groups (groups > 0) take the same kernels but the stream of few rows.
+Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t groups, int64_t n_out, int64_t n_in) {
     Plan p{};
-    if (!grad && rows <= kFewRows) {
+    // rows of one matrix, as far as the sizes say
+    const int64_t each_rows = groups == 0 ? rows : ceil_div(rows, std::min(rows, groups));
+    if (!grad && groups == 0 && rows <= kFewRows) {
         p.way = Way::few;
         p.rows = rows;
         p.splits = 1;
@@ -98,9 +126,9 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
     double mid_us = 0;
     if (!grad) {
         mid.way = Way::mid;
-        mid.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+        mid.mt = each_rows <= 16 ? 1 : each_rows <= 32 ? 2 : 4;
         const int64_t steps = ceil_div(n_in, 128 * kMidChunks), col_tiles = ceil_div(n_out, 64 * kMidTiles);
-        const int64_t tiles = col_tiles * ceil_div(rows, 16 * mid.mt);
+        const int64_t tiles = col_tiles * row_tiles(rows, groups, 16 * mid.mt);
         for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
             if (want > steps) break;
             const int64_t each = ceil_div(steps, want), n = ceil_div(steps, each);
@@ -111,8 +139,8 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
                 mid.split_steps = each;
             }
         }
-        mid.rows = std::max<int64_t>(kMaxTiles / col_tiles / mid.splits, 1) * 16 * mid.mt;
-        if (rows <= kMidRows || (out_f32 && !in_f32)) return mid;
+        bound_launch(mid, groups, col_tiles);
+        if (each_rows <= kMidRows || (out_f32 && !in_f32)) return mid;
     }
     p.way = Way::tile;
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
@@ -125,7 +153,7 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
             if (want > 1 && want > steps / 3) break;
             // the pipeline takes steps in pairs
             const int64_t each = want == 1 ? steps : ceil_div(ceil_div(steps, want), 2) * 2, n = ceil_div(steps, each);
-            const double t = tile_time(parts, mt, n, rows, len, each);
+            const double t = tile_time(parts, mt, n, rows, groups, len, each);
             if (p.mt == 0 || t < least) {
                 least = t;
                 p.mt = mt;
@@ -136,18 +164,25 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t n_out
     }
     if (in_f32) least += 3.0 + static_cast<double>(rows * c_len) * 10 / 5.5e6;
     if (mid.mt != 0 && mid_us * (in_f32 ? 1.0 : 1.08) < least) return mid;
-    p.rows = std::max<int64_t>(kMaxTiles / col_tiles / p.splits, 1) * 16 * p.mt;
+    bound_launch(p, groups, col_tiles);
     return p;
 }
 
-// out[r][c] = sum of the parts, in order, 4 columns a thread.
+// out[r][c] = sum of the parts, in order, 4 columns a thread. GROUPED: of rows
+// `first` to `last` of the whole call's, where row0 is this launch's first, alone.
+template <bool GROUPED>
 __global__ __launch_bounds__(kBlockThreads) void linear_join_kernel(const float *__restrict__ partial, int splits,
                                                                     int64_t rows, int64_t len, void *out,
-                                                                    int64_t ldo, int out_f32) {
+                                                                    int64_t ldo, int out_f32,
+                                                                    const int32_t *__restrict__ first,
+                                                                    const int32_t *__restrict__ last, int64_t row0) {
     const int64_t ldp = (len + 3) & ~INT64_C(3), per = ldp / 4;
+    int64_t r_first = 0, r_last = 0;
+    if constexpr (GROUPED) r_first = *first - row0, r_last = *last - row0;
     const int64_t n = static_cast<int64_t>(gridDim.x) * kBlockThreads;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlockThreads + threadIdx.x; i < rows * per; i += n) {
         const int64_t r = i / per, c = (i - r * per) * 4;
+        if (GROUPED && (r < r_first || r >= r_last)) continue;
         f32x4 v = {0, 0, 0, 0};
         const float *from = partial + r * ldp + c;
         int s = 0;
@@ -239,27 +274,27 @@ int64_t packed_bytes(const Plan &p, bool in_f32, int64_t rows, int64_t c_len) {
 
 }  // namespace
 
-int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int64_t rows, int64_t n_out,
-                         int64_t n_in) {
+int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int64_t rows, int64_t groups,
+                         int64_t n_out, int64_t n_in) {
     if (rows == 0) return 0;
-    const Plan p = make_plan(grad, in_f32, out_f32, rows, n_out, n_in);
+    const Plan p = make_plan(grad, in_f32, out_f32, rows, groups, n_out, n_in);
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     int64_t bytes = needs_pack(p, in_f32, lda, c_len) ? packed_bytes(p, in_f32, rows, c_len) : 0;
     if (p.splits > 1) bytes += p.splits * std::min(rows, p.rows) * ((len + 3) & ~INT64_C(3)) * 4;
     return bytes;
 }
 
-hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int64_t rows, const void *codes,
-                         const float *scales, int bits, int64_t n_out, int64_t n_in, int log2b, void *out,
-                         bool out_f32, int64_t ldo, void *workspace, hipStream_t stream) {
-    const Plan plan = make_plan(grad, in_f32, out_f32, rows, n_out, n_in);
+hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int64_t rows, const int32_t *offsets,
+                         int64_t groups, const void *codes, const float *scales, int bits, int64_t n_out, int64_t n_in,
+                         int log2b, void *out, bool out_f32, int64_t ldo, void *workspace, hipStream_t stream) {
+    const Plan plan = make_plan(grad, in_f32, out_f32, rows, groups, n_out, n_in);
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     const bool pack = needs_pack(plan, in_f32, lda, c_len);
     for (int64_t r0 = 0; r0 < rows; r0 += plan.rows) {
         LinArgs p{};
         p.a = static_cast<const uint8_t *>(a) + r0 * lda * (in_f32 ? 4 : 2);
         p.lda = lda;
-        p.rows = std::min(rows - r0, plan.rows);
+        p.rows = p.split_rows = std::min(rows - r0, plan.rows);
         p.codes = static_cast<const uint8_t *>(codes);
         p.scales = scales;
         p.n_out = n_out;
@@ -272,6 +307,7 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
                                               (pack ? packed_bytes(plan, in_f32, rows, c_len) : 0));
         p.splits = plan.splits;
         p.split_steps = plan.split_steps;
+        p.row0 = r0;
         hipError_t e = hipSuccess;
         if (pack) {
             const int64_t ldp = ceil_div(c_len, 64) * 64;
@@ -287,29 +323,48 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
             p.lda = ldp;
             p.plane = p.rows * ldp;
         }
-        if (plan.way == Way::few) {
+        p.row_tiles = ceil_div(p.rows, 16 * std::max(plan.mt, 1));
+        p.col_tiles = plan.way == Way::mid ? ceil_div(n_out, 64 * kMidTiles) : ceil_div(len, 256);
+        const int parts = in_f32 ? 2 : out_f32 ? 1 : 0;
+        if (groups > 0) {
+            for (int64_t g0 = 0; g0 < groups; g0 += plan.groups) {
+                LinArgs q = p;
+                q.offsets = offsets + g0;
+                q.groups = static_cast<int>(std::min(groups - g0, plan.groups));
+                q.row_tiles += q.groups;
+                q.codes += g0 * (n_out * n_in * bits / 8);
+                q.scales += g0 * (n_out * n_in >> log2b);
+                if (plan.way == Way::mid)
+                    e = launch_linear_mid_group(q, bits, in_f32, plan.mt, stream);
+                else if (grad)
+                    e = bits == 4 ? launch_linear_big_group_grad4(q, parts, plan.mt, stream)
+                                  : launch_linear_big_group_grad8(q, parts, plan.mt, stream);
+                else
+                    e = bits == 4 ? launch_linear_big_group_fwd4(q, parts, plan.mt, stream)
+                                  : launch_linear_big_group_fwd8(q, parts, plan.mt, stream);
+                if (e != hipSuccess) return e;
+            }
+        } else if (plan.way == Way::few) {
             e = launch_linear_few(p, bits, in_f32, stream);
         } else if (plan.way == Way::mid) {
-            p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
-            p.col_tiles = ceil_div(n_out, 64 * kMidTiles);
             e = launch_linear_mid(p, bits, in_f32, plan.mt, stream);
+        } else if (grad) {
+            e = bits == 4 ? launch_linear_big_grad4(p, parts, plan.mt, stream)
+                          : launch_linear_big_grad8(p, parts, plan.mt, stream);
         } else {
-            const int parts = in_f32 ? 2 : out_f32 ? 1 : 0;
-            p.row_tiles = ceil_div(p.rows, 16 * plan.mt);
-            p.col_tiles = ceil_div(len, 256);
-            if (grad)
-                e = bits == 4 ? launch_linear_big_grad4(p, parts, plan.mt, stream)
-                              : launch_linear_big_grad8(p, parts, plan.mt, stream);
-            else
-                e = bits == 4 ? launch_linear_big_fwd4(p, parts, plan.mt, stream)
-                              : launch_linear_big_fwd8(p, parts, plan.mt, stream);
+            e = bits == 4 ? launch_linear_big_fwd4(p, parts, plan.mt, stream)
+                          : launch_linear_big_fwd8(p, parts, plan.mt, stream);
         }
         if (e != hipSuccess) return e;
         if (plan.splits > 1) {
             const int64_t threads = p.rows * ((len + 3) / 4);
-            const int64_t grid = std::min<int64_t>(ceil_div(threads, kBlockThreads), 1 << 16);
-            linear_join_kernel<<<static_cast<unsigned>(grid), kBlockThreads, 0, stream>>>(
-                p.partial, p.splits, p.rows, len, p.out, ldo, out_f32);
+            const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ceil_div(threads, kBlockThreads), 1 << 16));
+            if (groups > 0)
+                linear_join_kernel<true><<<grid, kBlockThreads, 0, stream>>>(
+                    p.partial, p.splits, p.rows, len, p.out, ldo, out_f32, offsets, offsets + groups, r0);
+            else
+                linear_join_kernel<false><<<grid, kBlockThreads, 0, stream>>>(
+                    p.partial, p.splits, p.rows, len, p.out, ldo, out_f32, nullptr, nullptr, 0);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

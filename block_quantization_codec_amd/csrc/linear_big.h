@@ -29,7 +29,7 @@
 // of the results' norm in place of 1.7e-3. That is one product in place of the
 // three that a caller gets by asking for binary32 results: weights are three parts
 // of RN(code * s) where input or result is binary32 (forward, bf16 to binary32
-// takes exact codes instead, linear_mid.hip). Sums are binary32 throughout.
+// takes exact codes instead, linear_mid.h). Sums are binary32 throughout.
 //
 // A step is taken in two halves of 32 indices (one matrix instruction deep).
 // With 256 rows a wave has the SIMD to itself (256 sums a lane), so nothing but
@@ -463,7 +463,7 @@ struct LinBig {
     }
 };
 
-template <bool GRAD, int BITS, int PA, int PB, int MT>
+template <bool GRAD, int BITS, int PA, int PB, int MT, LinMode MODE>
 __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1 : 2) void linear_big_kernel(
     LinArgs p) {
     using L = LinBig<GRAD, BITS, PA, PB, MT>;
@@ -472,7 +472,12 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     const int q = lane >> 4;
     const int64_t c_len = GRAD ? p.n_out : p.n_in, len = GRAD ? p.n_in : p.n_out;
-    const LinPlace place = lin_place(p, L::kRows);
+    LinPlace place;
+    if constexpr (MODE == LinMode::grouped) {
+        if (!group_place<BITS, 2>(p, L::kRows, len, place)) return;
+    } else {
+        place = lin_place(p, L::kRows);
+    }
     const int64_t m0 = place.m0, wave_col = place.col * kTileCols + w * 64, col = wave_col + (lane & 15) * 4;
     const typename L::At at = L::place(p, m0, wave_col);
 
@@ -582,32 +587,32 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
     }
 }
 
-template <bool GRAD, int BITS, int PA, int PB, int MT>
+template <LinMode MODE, bool GRAD, int BITS, int PA, int PB, int MT>
 hipError_t launch_linear_big_one(const LinArgs &p, hipStream_t stream) {
     const int64_t grid = p.row_tiles * p.col_tiles * p.splits;
-    linear_big_kernel<GRAD, BITS, PA, PB, MT><<<static_cast<unsigned>(grid), kBlockThreads, 0, stream>>>(p);
+    linear_big_kernel<GRAD, BITS, PA, PB, MT, MODE><<<static_cast<unsigned>(grid), kBlockThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 // parts 0: bf16 to bf16; 1: bf16 to binary32; 2: binary32 activations. mt is the plan's.
-template <bool GRAD, int BITS>
+template <LinMode MODE, bool GRAD, int BITS>
 hipError_t launch_linear_big_as(const LinArgs &p, int parts, int mt, hipStream_t stream) {
     if (parts == 2) {
-        if (mt == 8) return launch_linear_big_one<GRAD, BITS, 3, 3, 8>(p, stream);
-        if (mt == 4) return launch_linear_big_one<GRAD, BITS, 3, 3, 4>(p, stream);
-        return launch_linear_big_one<GRAD, BITS, 3, 3, 1>(p, stream);
+        if (mt == 8) return launch_linear_big_one<MODE, GRAD, BITS, 3, 3, 8>(p, stream);
+        if (mt == 4) return launch_linear_big_one<MODE, GRAD, BITS, 3, 3, 4>(p, stream);
+        return launch_linear_big_one<MODE, GRAD, BITS, 3, 3, 1>(p, stream);
     }
-    if constexpr (GRAD) {  // forward, the exact codes do better (linear_mid.hip)
+    if constexpr (GRAD) {  // forward, the exact codes do better (linear_mid.h)
         if (parts == 1) {
-            if (mt == 8) return launch_linear_big_one<GRAD, BITS, 1, 3, 8>(p, stream);
-            if (mt == 4) return launch_linear_big_one<GRAD, BITS, 1, 3, 4>(p, stream);
-            return launch_linear_big_one<GRAD, BITS, 1, 3, 1>(p, stream);
+            if (mt == 8) return launch_linear_big_one<MODE, GRAD, BITS, 1, 3, 8>(p, stream);
+            if (mt == 4) return launch_linear_big_one<MODE, GRAD, BITS, 1, 3, 4>(p, stream);
+            return launch_linear_big_one<MODE, GRAD, BITS, 1, 3, 1>(p, stream);
         }
     }
-    if (mt == 16) return launch_linear_big_one<GRAD, BITS, 1, 1, 16>(p, stream);
-    if (mt == 8) return launch_linear_big_one<GRAD, BITS, 1, 1, 8>(p, stream);
-    if (mt == 4) return launch_linear_big_one<GRAD, BITS, 1, 1, 4>(p, stream);
-    return launch_linear_big_one<GRAD, BITS, 1, 1, 1>(p, stream);
+    if (mt == 16) return launch_linear_big_one<MODE, GRAD, BITS, 1, 1, 16>(p, stream);
+    if (mt == 8) return launch_linear_big_one<MODE, GRAD, BITS, 1, 1, 8>(p, stream);
+    if (mt == 4) return launch_linear_big_one<MODE, GRAD, BITS, 1, 1, 4>(p, stream);
+    return launch_linear_big_one<MODE, GRAD, BITS, 1, 1, 1>(p, stream);
 }
 
 }  // namespace zpp

@@ -4,7 +4,7 @@
 namespace zpp {
 
 hipError_t launch_linear_big_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream) {
-    return launch_linear_big_as<false, 8>(p, parts, mt, stream);
+    return launch_linear_big_as<LinMode::one, false, 8>(p, parts, mt, stream);
 }
 
 }  // namespace zpp

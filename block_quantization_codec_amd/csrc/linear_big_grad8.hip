@@ -4,7 +4,7 @@
 namespace zpp {
 
 hipError_t launch_linear_big_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream) {
-    return launch_linear_big_as<true, 8>(p, parts, mt, stream);
+    return launch_linear_big_as<LinMode::one, true, 8>(p, parts, mt, stream);
 }
 
 }  // namespace zpp

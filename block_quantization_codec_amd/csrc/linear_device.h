@@ -79,7 +79,7 @@ __device__ __forceinline__ f32x4 mfma_parts(const u32x4 (&a)[PA], const u32x4 (&
     return c;
 }
 
-// linear_mid.hip's shape: tiles of 16 features a wave, chunks of 128 indices a step.
+// linear_mid.h's shape: tiles of 16 features a wave, chunks of 128 indices a step.
 constexpr int kMidTiles = 2;
 constexpr int kMidChunks = 2;
 
@@ -107,11 +107,20 @@ struct LinArgs {
     void *out;
     int64_t ldo;
     int out_f32;
-    float *partial;       // splits x rows x ldp sums when splits > 1
+    float *partial;       // splits x split_rows x ldp sums when splits > 1
+    int64_t split_rows;   // rows of the launch
     int splits;
     int64_t split_steps;  // contraction steps of each split
     int64_t row_tiles, col_tiles;
     int64_t plane;        // elements from one part of packed activations to the next
+    // rows in groups, a weight matrix each: group e has rows offsets[e] .. offsets[e + 1] - 1,
+    // counted from row0 before the launch's first
+    const int32_t *offsets;
+    int groups;
+    int64_t row0;
 };
+
+// What a product's rows multiply by: one matrix, or that of the row's group.
+enum class LinMode { one, grouped };
 
 }  // namespace zpp

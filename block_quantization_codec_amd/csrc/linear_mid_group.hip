@@ -1,0 +1,10 @@
+// linear_mid_group.hip - y = x W^T on block codes, a matrix for each group of rows (linear_mid.h).
+#include "linear_mid.h"
+
+namespace zpp {
+
+hipError_t launch_linear_mid_group(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream) {
+    return launch_mid<LinMode::grouped>(p, bits, a_f32, mt, stream);
+}
+
+}  // namespace zpp

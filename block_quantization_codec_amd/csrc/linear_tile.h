@@ -3,6 +3,8 @@
 // stores of results.
 #pragma once
 
+#include <type_traits>
+
 #include "linear_device.h"
 
 namespace zpp {
@@ -25,16 +27,86 @@ struct LinPlace {
     int64_t split, m0, col;
 };
 
-__device__ __forceinline__ LinPlace lin_place(const LinArgs &p, int rows) {
+// `grid` workgroups, a launch's or its first ones, cover `row_tiles` rows of tiles of `rows` rows.
+__device__ __forceinline__ LinPlace lin_place_of(const LinArgs &p, int rows, uint32_t grid, uint32_t row_tiles) {
     // A launch has fewer than 2^24 workgroups. Divisions leave their results in
     // vector registers; read back, they and all that follows from them are scalar.
     auto div = [](uint32_t a, uint32_t b) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(a / b)); };
-    const uint32_t id = static_cast<uint32_t>(xcd_block(blockIdx.x, gridDim.x));
-    const uint32_t row_tiles = static_cast<uint32_t>(p.row_tiles), col_tiles = static_cast<uint32_t>(p.col_tiles);
+    const uint32_t id = static_cast<uint32_t>(xcd_block(blockIdx.x, grid));
+    const uint32_t col_tiles = static_cast<uint32_t>(p.col_tiles);
     const uint32_t split = div(id, row_tiles * col_tiles), tile = id - split * (row_tiles * col_tiles);
     const uint32_t g = div(tile, 8 * col_tiles), in_g = min(8u, row_tiles - g * 8), at = tile - g * 8 * col_tiles;
     const uint32_t col = div(at, in_g), row = g * 8 + (at - col * in_g);
     return LinPlace{split, static_cast<int64_t>(row) * rows, col};
+}
+
+__device__ __forceinline__ LinPlace lin_place(const LinArgs &p, int rows) {
+    return lin_place_of(p, rows, gridDim.x, static_cast<uint32_t>(p.row_tiles));
+}
+
+// Inclusive sums along the wave's lanes.
+__device__ __forceinline__ uint32_t scan_add(uint32_t v) {
+    auto moved = [](uint32_t from, auto ctrl, auto rows) {  // lanes without a source take 0
+        return static_cast<uint32_t>(
+            __builtin_amdgcn_update_dpp(0, static_cast<int>(from), ctrl.value, rows.value, 0xF, true));
+    };
+    using std::integral_constant;
+    using All = integral_constant<int, 0xF>;
+    v += moved(v, integral_constant<int, 0x111>{}, All{});  // row_shr 1, 2, 4, 8: within rows of 16
+    v += moved(v, integral_constant<int, 0x112>{}, All{});
+    v += moved(v, integral_constant<int, 0x114>{}, All{});
+    v += moved(v, integral_constant<int, 0x118>{}, All{});
+    v += moved(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // lane 15 to row 1, 47 to row 3
+    v += moved(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // lane 31 to rows 2 and 3
+    return v;
+}
+
+// The tile of a launch over groups: which group a workgroup's rows are of follows
+// from the offsets, which only the device knows. Every wave counts the groups' tiles
+// (64 groups at a time); workgroups past the last one have nothing to do, and the
+// others are dealt out as if the launch had no more. `p` becomes the group's own product.
+// Offsets are taken within the launch's rows and tiles, whatever they hold.
+template <int BITS, int ELEM>
+__device__ __forceinline__ bool group_place(LinArgs &p, int tile_rows, int64_t len, LinPlace &place) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int most = static_cast<int>(p.row_tiles);
+    auto clip = [&](int32_t v) {
+        return static_cast<int>(min(max(static_cast<int64_t>(v) - p.row0, INT64_C(0)), p.rows));
+    };
+    int begin, count;
+    auto tiles_of = [&](int e) {
+        const int at = min(e, p.groups - 1);
+        begin = clip(p.offsets[at]);
+        count = e < p.groups ? max(clip(p.offsets[at + 1]) - begin, 0) : 0;
+        return static_cast<uint32_t>(min((count + tile_rows - 1) / tile_rows, most));
+    };
+    auto last = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63)); };
+    uint32_t total = 0;
+    for (int e = 0; e < p.groups; e += kWave) total = min(total + last(scan_add(tiles_of(e + lane))), static_cast<uint32_t>(most));
+    const uint32_t grid = total * static_cast<uint32_t>(p.col_tiles * p.splits);
+    if (blockIdx.x >= grid) return false;
+    place = lin_place_of(p, 1, grid, total);
+    const uint32_t tile = static_cast<uint32_t>(place.m0);
+    uint32_t before = 0;
+    for (int e = 0; e < p.groups; e += kWave) {
+        const uint32_t own = tiles_of(e + lane), upto = before + scan_add(own);
+        const uint64_t past = __ballot(upto > tile);
+        if (past != 0) {
+            const int l = __builtin_ctzll(past);
+            auto read = [&](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l)); };
+            const int64_t group = e + l, first = read(static_cast<uint32_t>(begin)), weights = p.n_out * p.n_in;
+            place.m0 = static_cast<int64_t>(tile - (read(upto) - read(own))) * tile_rows;
+            p.a = static_cast<const uint8_t *>(p.a) + first * p.lda * ELEM;
+            p.rows = read(static_cast<uint32_t>(count));
+            p.codes += group * (weights * BITS / 8);
+            p.scales += group * (weights >> p.log2b);
+            p.out = static_cast<uint8_t *>(p.out) + first * p.ldo * (p.out_f32 ? 4 : 2);
+            p.partial += first * ((len + 3) & ~INT64_C(3));
+            return true;
+        }
+        before = last(upto);
+    }
+    return false;
 }
 
 // A tile of 16*MT rows x 64 activations in LDS, in PA planes of bf16 parts.
@@ -122,7 +194,7 @@ __device__ __forceinline__ void store4(const LinArgs &p, int64_t len, int64_t ro
     if (p.splits > 1) {  // columns of the sums are padded to whole fours
         const int64_t ldp = (len + 3) & ~INT64_C(3);
         if (col < ldp)
-            st<f32x4>(p.partial + (split * p.rows + row) * ldp + col, f32x4{v[0], v[1], v[2], v[3]});
+            st<f32x4>(p.partial + (split * p.split_rows + row) * ldp + col, f32x4{v[0], v[1], v[2], v[3]});
         return;
     }
     if (p.out_f32) {

@@ -204,43 +204,52 @@ bool is_norm_size(int64_t rows, int64_t width) {
     return rows >= 0 && rows <= ZPP_MAX_ROWS && width >= 1 && width <= ZPP_MAX_FEATURES;
 }
 
-// y = x W^T, or with `grad` dx = dy W: `a` and `out` are [rows, a_len] and [rows, out_len].
-zpp_status linear(bool grad, const void *a, int32_t a_dtype, int64_t a_stride, int64_t rows, const void *codes,
-                  const float *scales, int32_t bits, int64_t n_out, int64_t n_in, int32_t block, void *out,
-                  int32_t out_dtype, int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream) {
+// y = x W^T, or with `grad` dx = dy W: `a` and `out` are [rows, a_len] and [rows, out_len]. With `groups` > 0, rows
+// in groups by `offsets`, a weight each.
+zpp_status linear(bool grad, const void *a, int32_t a_dtype, int64_t a_stride, int64_t rows, const int32_t *offsets,
+                  int64_t groups, const void *codes, const float *scales, int32_t bits, int64_t n_out, int64_t n_in,
+                  int32_t block, void *out, int32_t out_dtype, int64_t out_stride, void *workspace,
+                  int64_t workspace_bytes, void *stream) {
     if (!is_dtype(a_dtype) || !is_dtype(out_dtype)) return ZPP_ERR_ARG;
     if (bits != 8 && bits != 4) return ZPP_ERR_ARG;
     if (!is_linear_size(rows, n_out, n_in)) return ZPP_ERR_ARG;
     if (!is_pow2_block(block) || n_out * n_in % block != 0) return ZPP_ERR_ARG;
-    const int64_t a_len = grad ? n_out : n_in, out_len = grad ? n_in : n_out;
+    const int64_t a_len = grad ? n_out : n_in, out_len = grad ? n_in : n_out, weights = n_out * n_in;
     if (!is_stride(a_stride, rows, a_len) || !is_stride(out_stride, rows, out_len)) return ZPP_ERR_ARG;
     if (workspace_bytes < 0) return ZPP_ERR_ARG;
     if (rows == 0) return ZPP_OK;
     // one row has no stride to speak of: it is its own length
     if (rows == 1) (grad ? out_stride : a_stride) = n_in;
     const int64_t need =
-        zpp::linear_workspace(grad, a_dtype == ZPP_FP32, a_stride, out_dtype == ZPP_FP32, rows, n_out, n_in);
+        zpp::linear_workspace(grad, a_dtype == ZPP_FP32, a_stride, out_dtype == ZPP_FP32, rows, groups, n_out, n_in);
     if (workspace_bytes < need) return ZPP_ERR_ARG;
-    if (!a || !codes || !scales || !out || (need > 0 && !workspace)) return ZPP_ERR_NULL;
-    if (!aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return ZPP_ERR_ALIGN;
+    if (!a || !codes || !scales || !out || (need > 0 && !workspace) || (groups > 0 && !offsets)) return ZPP_ERR_NULL;
+    if (!aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16) || !aligned(offsets, 4))
+        return ZPP_ERR_ALIGN;
     if (need > 0 && !aligned(workspace, 16)) return ZPP_ERR_ALIGN;
     // the side of in_features moves in 16-byte pieces
     const int64_t wide = grad ? out_stride * dtype_bytes(out_dtype) : a_stride * dtype_bytes(a_dtype);
     if (wide % 16 != 0) return ZPP_ERR_ALIGN;
-    const Range ra = matrix(a, rows, a_stride, a_len, a_dtype), rc{codes, code_bytes(n_out * n_in, bits)},
-        rs{scales, 4 * (n_out * n_in / block)}, ro = matrix(out, rows, out_stride, out_len, out_dtype),
-        rw{workspace, need};
-    for (const Range &r : {ra, rc, rs}) {
+    const int64_t matrices = groups > 0 ? groups : 1;
+    const Range ra = matrix(a, rows, a_stride, a_len, a_dtype), rc{codes, code_bytes(matrices * weights, bits)},
+        rs{scales, 4 * (matrices * (weights / block))}, rg{offsets, groups > 0 ? 4 * (groups + 1) : 0},
+        ro = matrix(out, rows, out_stride, out_len, out_dtype), rw{workspace, need};
+    for (const Range &r : {ra, rc, rs, rg}) {
         if (overlap(ro, r) || overlap(rw, r)) return ZPP_ERR_OVERLAP;
     }
     if (overlap(ro, rw)) return ZPP_ERR_OVERLAP;
-    const Range all[] = {ra, rc, rs, ro, rw};
+    const Range all[] = {ra, rc, rs, rg, ro, rw};
     if (zpp_status s = check_all(all); s != ZPP_OK) return s;
     return launch_checked([&] {
-        return zpp::launch_linear(grad, a, a_dtype == ZPP_FP32, a_stride, rows, codes, scales, bits, n_out, n_in,
-                   log2_of(block), out, out_dtype == ZPP_FP32, out_stride, workspace,
+        return zpp::launch_linear(grad, a, a_dtype == ZPP_FP32, a_stride, rows, offsets, groups, codes, scales, bits,
+                   n_out, n_in, log2_of(block), out, out_dtype == ZPP_FP32, out_stride, workspace,
                    static_cast<hipStream_t>(stream));
     });
+}
+
+// As many matrices of this size as the codes of one call may hold.
+bool is_groups(int64_t groups, int64_t n_out, int64_t n_in) {
+    return groups >= 1 && groups <= ZPP_MAX_GROUPS && (n_out < 1 || n_in < 1 || n_out <= ZPP_MAX_NUMEL / n_in / groups);
 }
 
 }  // namespace
@@ -437,7 +446,7 @@ zpp_status zpp_linear_blocks(const void *x, int32_t x_dtype, int64_t x_stride, i
                              const float *scales, int32_t bits, int64_t out_features, int64_t in_features,
                              int32_t block, void *y, int32_t y_dtype, int64_t y_stride, void *workspace,
                              int64_t workspace_bytes, void *stream) {
-    return linear(false, x, x_dtype, x_stride, rows, codes, scales, bits, out_features, in_features, block, y,
+    return linear(false, x, x_dtype, x_stride, rows, nullptr, 0, codes, scales, bits, out_features, in_features, block, y,
                   y_dtype, y_stride, workspace, workspace_bytes, stream);
 }
 
@@ -445,15 +454,43 @@ zpp_status zpp_linear_blocks_grad(const void *dy, int32_t dy_dtype, int64_t dy_s
                                   const void *codes, const float *scales, int32_t bits, int64_t out_features,
                                   int64_t in_features, int32_t block, void *dx, int32_t dx_dtype, int64_t dx_stride,
                                   void *workspace, int64_t workspace_bytes, void *stream) {
-    return linear(true, dy, dy_dtype, dy_stride, rows, codes, scales, bits, out_features, in_features, block, dx,
-                  dx_dtype, dx_stride, workspace, workspace_bytes, stream);
+    return linear(true, dy, dy_dtype, dy_stride, rows, nullptr, 0, codes, scales, bits, out_features, in_features, block,
+                  dx, dx_dtype, dx_stride, workspace, workspace_bytes, stream);
 }
 
 int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
                                     int64_t rows, int64_t out_features, int64_t in_features) {
     if (!is_dtype(in_dtype) || !is_dtype(out_dtype) || !is_linear_size(rows, out_features, in_features)) return 0;
     if (!is_stride(in_stride, rows, grad != 0 ? out_features : in_features)) return 0;
-    return zpp::linear_workspace(grad != 0, in_dtype == ZPP_FP32, in_stride, out_dtype == ZPP_FP32, rows,
+    return zpp::linear_workspace(grad != 0, in_dtype == ZPP_FP32, in_stride, out_dtype == ZPP_FP32, rows, 0,
+                                 out_features, in_features);
+}
+
+zpp_status zpp_linear_grouped(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, const int32_t *offsets,
+                              int64_t groups, const void *codes, const float *scales, int32_t bits,
+                              int64_t out_features, int64_t in_features, int32_t block, void *y, int32_t y_dtype,
+                              int64_t y_stride, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!is_groups(groups, out_features, in_features)) return ZPP_ERR_ARG;
+    return linear(false, x, x_dtype, x_stride, rows, offsets, groups, codes, scales, bits, out_features, in_features,
+                  block, y, y_dtype, y_stride, workspace, workspace_bytes, stream);
+}
+
+zpp_status zpp_linear_grouped_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, int64_t rows,
+                                   const int32_t *offsets, int64_t groups, const void *codes, const float *scales,
+                                   int32_t bits, int64_t out_features, int64_t in_features, int32_t block, void *dx,
+                                   int32_t dx_dtype, int64_t dx_stride, void *workspace, int64_t workspace_bytes,
+                                   void *stream) {
+    if (!is_groups(groups, out_features, in_features)) return ZPP_ERR_ARG;
+    return linear(true, dy, dy_dtype, dy_stride, rows, offsets, groups, codes, scales, bits, out_features, in_features,
+                  block, dx, dx_dtype, dx_stride, workspace, workspace_bytes, stream);
+}
+
+int64_t zpp_linear_grouped_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
+                                     int64_t rows, int64_t groups, int64_t out_features, int64_t in_features) {
+    if (!is_dtype(in_dtype) || !is_dtype(out_dtype) || !is_linear_size(rows, out_features, in_features)) return 0;
+    if (!is_groups(groups, out_features, in_features)) return 0;
+    if (!is_stride(in_stride, rows, grad != 0 ? out_features : in_features)) return 0;
+    return zpp::linear_workspace(grad != 0, in_dtype == ZPP_FP32, in_stride, out_dtype == ZPP_FP32, rows, groups,
                                  out_features, in_features);
 }
 

@@ -33,12 +33,13 @@ hipError_t launch_drr_average(const void *codes_in, int64_t codes_stride, const 
                               int64_t scales_stride, int n_inputs, int bits_in, int64_t numel, int log2b,
                               int divisor, float *avg_out, hipStream_t stream);
 
-// y = x W^T (grad false: a is x, rows of n_in) or dx = dy W (grad true: a is dy, rows of n_out).
-hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int64_t rows, const void *codes,
-                         const float *scales, int bits, int64_t n_out, int64_t n_in, int log2b, void *out,
-                         bool out_f32, int64_t ldo, void *workspace, hipStream_t stream);
-int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int64_t rows, int64_t n_out,
-                         int64_t n_in);
+// y = x W^T (grad false: a is x, rows of n_in) or dx = dy W (grad true: a is dy, rows of n_out). With groups > 0,
+// rows offsets[e] .. offsets[e + 1] - 1 (device memory) by the e-th of as many matrices.
+hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int64_t rows, const int32_t *offsets,
+                         int64_t groups, const void *codes, const float *scales, int bits, int64_t n_out, int64_t n_in,
+                         int log2b, void *out, bool out_f32, int64_t ldo, void *workspace, hipStream_t stream);
+int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int64_t rows, int64_t groups,
+                         int64_t n_out, int64_t n_in);
 
 hipError_t launch_layer_norm(const void *x, bool f32, int64_t x_stride, int64_t rows, int64_t width,
                              const void *weight, const void *bias, bool w_f32, float eps, void *y, int64_t y_stride,

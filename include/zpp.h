@@ -84,6 +84,7 @@ extern "C" {
 #define ZPP_MAX_DIVISOR 16777216 /* 2^24: every divisor up to it is exact in binary32 */
 #define ZPP_MAX_FEATURES 4194304 /* 2^22: the longest row of a weight matrix or of a norm */
 #define ZPP_MAX_ROWS 1073741824  /* 2^30: the most rows of one linear or norm call */
+#define ZPP_MAX_GROUPS 4096      /* the most weight matrices of one grouped linear call */
 /* 2^40: the largest element count, input stride (bytes for codes, floats
  * for scales), and reordered buffer (elements, or bytes / 4) accepted; far
  * beyond any GPU's memory, it keeps every byte range of a call exact in
@@ -344,6 +345,43 @@ zpp_status zpp_linear_blocks_grad(const void *dy, int32_t dy_dtype, int64_t dy_s
  * fewer rows may need more than many; 0 for sizes the calls refuse. */
 int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
                                     int64_t rows, int64_t out_features, int64_t in_features);
+
+/*
+ * Linear products of rows in groups, a block-quantized weight matrix for each (the
+ * experts of a layer, of which every row has been given one): `groups` matrices of
+ * out_features x in_features lie behind one another, codes and scales alike, as
+ * zpp_quantize_blocks writes them for groups * out_features * in_features elements.
+ * Row m of group e, offsets[e] <= m < offsets[e + 1], has
+ *
+ *   zpp_linear_grouped:       y[m][n]  = sum over k of x[m][k]  * W[e][n][k]
+ *   zpp_linear_grouped_grad:  dx[m][k] = sum over n of dy[m][n] * W[e][n][k]
+ *
+ *   offsets         in   groups + 1 int32, 4-B aligned, in device memory: ascending, from 0 to rows. A group may be
+ *                        empty; rows before offsets[0] and from offsets[groups] on are in no group, and what the output
+ *                        holds for them is left as it is. The library cannot check them before the launch: results of
+ *                        offsets that do not ascend are unspecified, but nothing outside of the call's rows is read or
+ *                        written, whatever the offsets hold.
+ *   groups          in   1..ZPP_MAX_GROUPS; groups * out_features * in_features <= ZPP_MAX_NUMEL
+ *   block           in   block size B; divides out_features * in_features
+ *   workspace_bytes in   at least zpp_linear_grouped_workspace(...) (ZPP_ERR_ARG otherwise)
+ * Everything else is as in zpp_linear_blocks: types, strides, precision (where that speaks of more than 64 rows:
+ * where rows / groups is more than 64), and rows that hold infinite or NaN elements.
+ */
+zpp_status zpp_linear_grouped(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, const int32_t *offsets,
+                              int64_t groups, const void *codes, const float *scales, int32_t bits,
+                              int64_t out_features, int64_t in_features, int32_t block, void *y, int32_t y_dtype,
+                              int64_t y_stride, void *workspace, int64_t workspace_bytes, void *stream);
+
+zpp_status zpp_linear_grouped_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, int64_t rows,
+                                   const int32_t *offsets, int64_t groups, const void *codes, const float *scales,
+                                   int32_t bits, int64_t out_features, int64_t in_features, int32_t block, void *dx,
+                                   int32_t dx_dtype, int64_t dx_stride, void *workspace, int64_t workspace_bytes,
+                                   void *stream);
+
+/* Bytes of workspace that zpp_linear_grouped (grad == 0) or zpp_linear_grouped_grad
+ * (grad != 0) needs, as zpp_linear_blocks_workspace; 0 for sizes the calls refuse. */
+int64_t zpp_linear_grouped_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
+                                     int64_t rows, int64_t groups, int64_t out_features, int64_t in_features);
 
 /*
  * Layer norm over each row of `width` elements, as it stands before the
