@@ -12,6 +12,7 @@ The short helpers (:func:`quantize`, :func:`dequantize`, :func:`reorder`,
 :func:`dequant_reduce_requant`, :func:`dequant_reduce_average`,
 :func:`quantize_reordered`, :func:`linear`, :func:`linear_grad`,
 :func:`linear_grouped`, :func:`linear_grouped_grad`,
+:func:`linear_adapters`, :func:`linear_adapters_grad`,
 :func:`layer_norm`, :func:`layer_norm_grad`, :func:`rms_norm`,
 :func:`rms_norm_grad`) allocate their outputs with torch on the
 input's device and call the same entry points. With ``stream`` they do so as
@@ -51,11 +52,13 @@ ZPP_MAX_NUMEL = 1 << 40
 ZPP_MAX_FEATURES = 1 << 22
 ZPP_MAX_ROWS = 1 << 30
 ZPP_MAX_GROUPS = 4096
+ZPP_MAX_RANK = 256
 
 EXPORTED = ("zpp_quantize_blocks", "zpp_quantize_reordered", "zpp_dequantize_blocks", "zpp_reorder_slices",
             "zpp_dequant_reduce_requant", "zpp_dequant_reduce_requant_split", "zpp_dequant_reduce_average",
             "zpp_linear_blocks", "zpp_linear_blocks_grad", "zpp_linear_blocks_workspace", "zpp_linear_grouped",
-            "zpp_linear_grouped_grad", "zpp_linear_grouped_workspace", "zpp_layer_norm",
+            "zpp_linear_grouped_grad", "zpp_linear_grouped_workspace", "zpp_linear_adapters",
+            "zpp_linear_adapters_grad", "zpp_linear_adapters_workspace", "zpp_layer_norm",
             "zpp_layer_norm_grad", "zpp_layer_norm_grad_workspace",
             "zpp_rms_norm", "zpp_rms_norm_grad", "zpp_rms_norm_grad_workspace",
             "zpp_set_pointer_checks", "zpp_status_string", "zpp_abi_version")
@@ -86,6 +89,10 @@ def _load() -> ctypes.CDLL:
         "zpp_linear_blocks_grad": [P, I32, I64, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
         "zpp_linear_grouped": [P, I32, I64, I64, P, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
         "zpp_linear_grouped_grad": [P, I32, I64, I64, P, I64, P, P, I32, I64, I64, I32, P, I32, I64, P, I64, P],
+        "zpp_linear_adapters": [P, I32, I64, I64, P, P, I32, I64, I64, I32, P, P, I32, I64, I64, P, P, P, P, I32, I64, P,
+                                I64, P],
+        "zpp_linear_adapters_grad": [P, I32, I64, P, I64, P, I64, P, P, I32, I64, I64, I32, P, P, I32, I64, I64, P, P, P,
+                                     I32, I64, P, P, P, I64, P],
         "zpp_layer_norm": [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, P, I64, P, P, P],
         "zpp_layer_norm_grad": [P, I64, P, I32, I64, I64, I64, P, I32, P, P, P, I64, P, P, P, I64, P],
         "zpp_rms_norm": [P, I32, I64, P, I64, I64, I64, P, I32, ctypes.c_float, P, I64, P, I64, P, P, I32, I32, P, P],
@@ -99,6 +106,8 @@ def _load() -> ctypes.CDLL:
     lib.zpp_linear_blocks_workspace.restype = I64
     lib.zpp_linear_grouped_workspace.argtypes = [I32, I32, I64, I32, I64, I64, I64, I64]
     lib.zpp_linear_grouped_workspace.restype = I64
+    lib.zpp_linear_adapters_workspace.argtypes = [I32, I32, I64, I32, I64, I64, I64, I64, I64]
+    lib.zpp_linear_adapters_workspace.restype = I64
     lib.zpp_layer_norm_grad_workspace.argtypes = [I64, I64]
     lib.zpp_layer_norm_grad_workspace.restype = I64
     lib.zpp_rms_norm_grad_workspace.argtypes = [I64, I64]
@@ -246,6 +255,29 @@ def zpp_linear_grouped_grad(dy, dy_dtype, dy_stride, rows, offsets, groups, code
 def zpp_linear_grouped_workspace(grad, in_dtype, in_stride, out_dtype, rows, groups, out_features, in_features) -> int:
     return int(_lib.zpp_linear_grouped_workspace(grad, in_dtype, in_stride, out_dtype, rows, groups, out_features,
                                                  in_features))
+
+
+def zpp_linear_adapters(x, x_dtype, x_stride, rows, codes, scales, bits, out_features, in_features, block, a, b,
+                        ab_dtype, adapters, rank, ids, scaling, reduced, y, y_dtype, y_stride, workspace,
+                        workspace_bytes, stream=None) -> None:
+    _call("zpp_linear_adapters", _ptr(x), x_dtype, x_stride, rows, _ptr(codes), _ptr(scales), bits, out_features,
+          in_features, block, _ptr(a), _ptr(b), ab_dtype, adapters, rank, _ptr(ids), _ptr(scaling), _ptr(reduced),
+          _ptr(y), y_dtype, y_stride, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def zpp_linear_adapters_grad(dy, dy_dtype, dy_stride, x, x_stride, reduced, rows, codes, scales, bits, out_features,
+                             in_features, block, a, b, ab_dtype, adapters, rank, ids, scaling, dx, dx_dtype, dx_stride,
+                             da, db, workspace, workspace_bytes, stream=None) -> None:
+    _call("zpp_linear_adapters_grad", _ptr(dy), dy_dtype, dy_stride, _ptr(x), x_stride, _ptr(reduced), rows,
+          _ptr(codes), _ptr(scales), bits, out_features, in_features, block, _ptr(a), _ptr(b), ab_dtype, adapters,
+          rank, _ptr(ids), _ptr(scaling), _ptr(dx), dx_dtype, dx_stride, _ptr(da), _ptr(db), _ptr(workspace),
+          workspace_bytes, _stream(stream))
+
+
+def zpp_linear_adapters_workspace(grad, in_dtype, in_stride, out_dtype, rows, out_features, in_features, adapters,
+                                  rank) -> int:
+    return int(_lib.zpp_linear_adapters_workspace(grad, in_dtype, in_stride, out_dtype, rows, out_features, in_features,
+                                                  adapters, rank))
 
 
 def zpp_layer_norm(x, x_dtype, x_stride, rows, width, weight, bias, w_dtype, eps, y, y_stride, mean, rstd,
@@ -594,6 +626,102 @@ def linear_grouped_grad(dy, offsets, codes, scales, bits: int, block: int, in_fe
                       workspace)
     return _linear("zpp_linear_grouped_grad", 1, dy, codes, scales, bits, block, in_features, dtype, out, workspace,
                    stream, offsets)
+
+
+def _adapters(a, b, ids, scaling, rows: int, n_out: int, n_in: int):
+    """The adapters' arguments of an entry point, from a on."""
+    import torch
+
+    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != n_in or b.shape[1] != n_out or a.shape[0] != b.shape[0] or \
+            a.shape[1] != b.shape[2]:
+        raise ValueError(f"a must be [adapters, rank, {n_in}] and b [adapters, {n_out}, rank]")
+    if a.dtype != b.dtype:
+        raise TypeError("a and b must be of one dtype")
+    if not (a.is_contiguous() and b.is_contiguous()):
+        raise ValueError("a and b must be contiguous")
+    if ids is not None and (ids.dtype != torch.int32 or not ids.is_contiguous() or ids.numel() != rows):
+        raise ValueError(f"ids must be contiguous int32, {rows} elements")
+    if scaling is not None and (scaling.dtype != torch.float32 or not scaling.is_contiguous()
+                                or scaling.numel() != a.shape[0]):
+        raise ValueError(f"scaling must be contiguous float32, {a.shape[0]} elements")
+    return (a.data_ptr(), b.data_ptr(), _code(a.dtype), a.shape[0], a.shape[1], _ptr(ids), _ptr(scaling))
+
+
+def linear_adapters(x, codes, scales, bits: int, block: int, out_features: int, a, b, ids=None, scaling=None, dtype=None,
+                    out=None, reduced=None, workspace=None, stream=None):
+    """As :func:`linear`, with a low-rank adapter beside the weight: y = x @ W.T + s * (x @ A.T) @ B.T,
+    where each row's A = a[g], B = b[g] and s = ``scaling[g]`` (1 without) are those of g = ``ids`` of the row.
+    ``a`` is [adapters, rank, in_features] and ``b`` [adapters, out_features, rank], of one dtype, the rank a
+    multiple of 8; ``ids`` has an int32 for each row, and a row whose number is no adapter's has none
+    (None: every row has adapter 0).
+    Returns (y, reduced): reduced float32 [rows..., rank] is s * x @ A.T, as :func:`linear_adapters_grad` takes it.
+    Autograd does not see the call, as with :func:`linear`. ``workspace``, if given, is a device tensor of at least
+    ``zpp_linear_adapters_workspace`` bytes."""
+    if stream is not None:
+        return _under(stream, linear_adapters, x, codes, scales, bits, block, out_features, a, b, ids, scaling, dtype,
+                      out, reduced, workspace)
+    import torch
+
+    rows, n_in, stride = _rows(x, "x")
+    _check_weight(codes, scales, bits, block, out_features * n_in)
+    adapters = _adapters(a, b, ids, scaling, rows, out_features, n_in)
+    xdt, shape = _code(x.dtype), (*x.shape[:-1], out_features)
+    if out is None:
+        out, ostride = x.new_empty(shape, dtype=dtype or x.dtype), out_features
+    else:
+        if tuple(out.shape) != shape or (dtype or out.dtype) != out.dtype:
+            raise ValueError(f"out must be of shape {shape} and of the dtype asked for")
+        ostride = _rows(out, "out")[2]
+    odt = _code(out.dtype)
+    reduced = _buffer(reduced, (*x.shape[:-1], a.shape[1]), torch.float32, "reduced", x)
+    need = _lib.zpp_linear_adapters_workspace(0, xdt, stride, odt, rows, out_features, n_in, a.shape[0], a.shape[1])
+    ws, ws_bytes, keep = _workspace(workspace, need, x)
+    _call("zpp_linear_adapters", x.data_ptr(), xdt, stride, rows, codes.data_ptr(), scales.data_ptr(), bits,
+          out_features, n_in, block, *adapters, reduced.data_ptr(), out.data_ptr(), odt, ostride, ws, ws_bytes,
+          _stream(stream))
+    return out, reduced
+
+
+def linear_adapters_grad(dy, x, reduced, codes, scales, bits: int, block: int, a, b, ids=None, scaling=None, dtype=None,
+                         out=None, want_adapters: bool = True, da=None, db=None, workspace=None, stream=None):
+    """Backward pass of :func:`linear_adapters`, with its x, ``reduced`` and adapters, for dy [..., out_features].
+    Returns (dx, da, db): dx of ``dtype`` (dy's by default), or in ``out``; da and db of a's and b's shapes and dtype
+    (new tensors, or those passed in), None with ``want_adapters`` false (x and ``reduced`` may then be None)."""
+    if stream is not None:
+        return _under(stream, linear_adapters_grad, dy, x, reduced, codes, scales, bits, block, a, b, ids, scaling, dtype,
+                      out, want_adapters, da, db, workspace)
+    import torch
+
+    rows, n_out, stride = _rows(dy, "dy")
+    n_in = a.shape[-1]
+    _check_weight(codes, scales, bits, block, n_out * n_in)
+    adapters = _adapters(a, b, ids, scaling, rows, n_out, n_in)
+    ddt, shape, rank = _code(dy.dtype), (*dy.shape[:-1], n_in), a.shape[1]
+    x_ptr, x_stride = None, n_in
+    if want_adapters:
+        if tuple(x.shape) != shape or x.dtype != dy.dtype:
+            raise ValueError(f"x must be of shape {shape} and of dy's dtype")
+        if tuple(reduced.shape) != (*dy.shape[:-1], rank) or reduced.dtype != torch.float32 or \
+                not reduced.is_contiguous():
+            raise ValueError(f"reduced must be contiguous float32, of shape {(*dy.shape[:-1], rank)}")
+        x_ptr, x_stride = x.data_ptr(), _rows(x, "x")[2]
+        da = _buffer(da, a.shape, a.dtype, "da", dy)
+        db = _buffer(db, b.shape, b.dtype, "db", dy)
+    elif da is not None or db is not None:
+        raise ValueError("a result is passed in that is not asked for")
+    if out is None:
+        out, ostride = dy.new_empty(shape, dtype=dtype or dy.dtype), n_in
+    else:
+        if tuple(out.shape) != shape or (dtype or out.dtype) != out.dtype:
+            raise ValueError(f"out must be of shape {shape} and of the dtype asked for")
+        ostride = _rows(out, "out")[2]
+    odt = _code(out.dtype)
+    need = _lib.zpp_linear_adapters_workspace(1, ddt, stride, odt, rows, n_out, n_in, a.shape[0], rank)
+    ws, ws_bytes, keep = _workspace(workspace, need, dy)
+    _call("zpp_linear_adapters_grad", dy.data_ptr(), ddt, stride, x_ptr, x_stride,
+          reduced.data_ptr() if want_adapters else None, rows, codes.data_ptr(), scales.data_ptr(), bits, n_out, n_in,
+          block, *adapters, out.data_ptr(), odt, ostride, _ptr(da), _ptr(db), ws, ws_bytes, _stream(stream))
+    return out, da, db
 
 
 def _vector(v, width: int, name: str):

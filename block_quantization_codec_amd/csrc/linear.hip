@@ -20,6 +20,11 @@ hipError_t launch_linear_big_group_fwd4(const LinArgs &p, int parts, int mt, hip
 hipError_t launch_linear_big_group_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream);
 hipError_t launch_linear_big_group_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
 hipError_t launch_linear_big_group_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_mid_adapt(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream);
+hipError_t launch_linear_big_adapt_fwd4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_adapt_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_adapt_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_big_adapt_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
 
 namespace {
 
@@ -286,7 +291,8 @@ int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int6
 
 hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int64_t rows, const int32_t *offsets,
                          int64_t groups, const void *codes, const float *scales, int bits, int64_t n_out, int64_t n_in,
-                         int log2b, void *out, bool out_f32, int64_t ldo, void *workspace, hipStream_t stream) {
+                         int log2b, void *out, bool out_f32, int64_t ldo, void *workspace, hipStream_t stream,
+                         const LinAdapters *ad, const float *low) {
     const Plan plan = make_plan(grad, in_f32, out_f32, rows, groups, n_out, n_in);
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     const bool pack = needs_pack(plan, in_f32, lda, c_len);
@@ -308,6 +314,14 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
         p.splits = plan.splits;
         p.split_steps = plan.split_steps;
         p.row0 = r0;
+        if (ad) {
+            p.low = low + r0 * ad->rank;
+            p.up = grad ? ad->a : ad->b;
+            p.up_f32 = ad->f32;
+            p.ids = ad->ids ? ad->ids + r0 : nullptr;
+            p.rank = static_cast<int>(ad->rank);
+            p.adapters = static_cast<int>(ad->adapters);
+        }
         hipError_t e = hipSuccess;
         if (pack) {
             const int64_t ldp = ceil_div(c_len, 64) * 64;
@@ -347,7 +361,14 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
         } else if (plan.way == Way::few) {
             e = launch_linear_few(p, bits, in_f32, stream);
         } else if (plan.way == Way::mid) {
-            e = launch_linear_mid(p, bits, in_f32, plan.mt, stream);
+            e = ad ? launch_linear_mid_adapt(p, bits, in_f32, plan.mt, stream)
+                   : launch_linear_mid(p, bits, in_f32, plan.mt, stream);
+        } else if (ad && grad) {
+            e = bits == 4 ? launch_linear_big_adapt_grad4(p, parts, plan.mt, stream)
+                          : launch_linear_big_adapt_grad8(p, parts, plan.mt, stream);
+        } else if (ad) {
+            e = bits == 4 ? launch_linear_big_adapt_fwd4(p, parts, plan.mt, stream)
+                          : launch_linear_big_adapt_fwd8(p, parts, plan.mt, stream);
         } else if (grad) {
             e = bits == 4 ? launch_linear_big_grad4(p, parts, plan.mt, stream)
                           : launch_linear_big_grad8(p, parts, plan.mt, stream);

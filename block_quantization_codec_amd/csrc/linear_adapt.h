@@ -1,0 +1,205 @@
+// linear_adapt.h - what a row's low-rank adapter adds to a product on block codes.
+//
+//   y[m][n]  += sum_r low[m][r] B[g][n][r]     low = s_g x A_g^T
+//   dx[m][k] += sum_r low[m][r] A[g][r][k]     low = s_g dy B_g         g = ids[m]
+//
+// The product's own kernels add it to their sums, before the result's one rounding:
+// a pass of its own would read and write the result again, and round it twice.
+//
+// Rows of a tile may have different adapters. Tiles whose rows all have one take it
+// into their sums by more matrix instructions. Others multiply 16 rows by each
+// adapter that one of them names, and each row keeps its own one's: so nothing of
+// an adapter, not its infinities or NaNs either, reaches another's rows.
+//
+// Precision: low is binary32 and enters as bf16 parts, like binary32 activations:
+// two of them (16 bits: off by 2^-17, against the 2^-9 of a bf16 result) from
+// bf16 to bf16, three otherwise; a bf16 adapter is one part, a binary32 one three.
+#pragma once
+
+#include "linear_device.h"
+
+namespace zpp {
+
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+// Two values as P bf16 pairs; of two parts, the first is cut off (which cannot
+// overflow) and the second rounded.
+template <int P>
+__device__ __forceinline__ void low_parts(float a, float b, uint32_t (&w)[P]) {
+    if constexpr (P == 2) {
+        const float ha = as_f(as_u(a) & 0xFFFF0000u), hb = as_f(as_u(b) & 0xFFFF0000u);
+        w[0] = pack_hi(a, b);
+        w[1] = pack_rn(ha == a ? 0.0f : a - ha, hb == b ? 0.0f : b - hb);
+    } else {
+        to_parts<P>(a, b, w);
+    }
+}
+
+// Eight binary32 values as parts of an operand.
+template <int P>
+__device__ __forceinline__ void operand_of(const float (&v)[8], u32x4 (&a)[P]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        uint32_t w[P];
+        low_parts<P>(v[2 * d], v[2 * d + 1], w);
+#pragma unroll
+        for (int x = 0; x < P; ++x) a[x][d] = w[x];
+    }
+}
+
+// Whether row `row` has an adapter, and which.
+__device__ __forceinline__ bool adapter_of(const LinArgs &p, int64_t row, int &id) {
+    id = p.ids ? p.ids[min(row, p.rows - 1)] : 0;
+    return row < p.rows && static_cast<uint32_t>(id) < static_cast<uint32_t>(p.adapters);
+}
+
+// The lane's part of `low` for indices r .. r + 7 of a row: zeros past the rank.
+template <int P>
+__device__ __forceinline__ void load_low(const LinArgs &p, int64_t row, int r, u32x4 (&a)[P]) {
+    float v[8];
+    const float *from = p.low + min(row, p.rows - 1) * p.rank + min(r, p.rank - 8);
+    const f32x4 x = ld<f32x4>(from), y = ld<f32x4>(from + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = r < p.rank ? x[i] : 0.0f;
+        v[4 + i] = r < p.rank ? y[i] : 0.0f;
+    }
+    operand_of<P>(v, a);
+}
+
+// The adapter's operands for NT tiles of columns, indices r .. r + 7: zeros past
+// the rank. Tile t's column is col + t (NEAR) or col + 16 t.
+template <bool GRAD, bool NEAR, int PB, int NT>
+__device__ __forceinline__ void load_up(const LinArgs &p, int64_t g, int64_t col, int r, u32x4 (&b)[NT][PB]) {
+    const bool in = r < p.rank;
+    if constexpr (GRAD) {  // [rank][in]: four neighbouring columns of eight rows, turned
+        static_assert(NEAR && NT == 4);
+        const int64_t c = min(col, p.n_in - 4), base = (g * p.rank + min(r, p.rank - 8)) * p.n_in + c;
+        if constexpr (PB == 3) {
+            f32x4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ld<f32x4>(static_cast<const float *>(p.up) + base + i * p.n_in);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float o[8] = {v[0][t], v[1][t], v[2][t], v[3][t], v[4][t], v[5][t], v[6][t], v[7][t]};
+                operand_of<PB>(o, b[t]);
+            }
+        } else {
+            u32x2 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ld<u32x2>(static_cast<const uint16_t *>(p.up) + base + i * p.n_in);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    b[t][0][d] = __builtin_amdgcn_perm(v[2 * d + 1][t / 2], v[2 * d][t / 2],
+                                                       t % 2 == 0 ? 0x05040100u : 0x07060302u);
+        }
+    } else {  // [out][rank]
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int64_t c = min(col + (NEAR ? t : 16 * t), p.n_out - 1);
+            const int64_t base = (g * p.n_out + c) * p.rank + min(r, p.rank - 8);
+            if constexpr (PB == 3) {
+                const float *from = static_cast<const float *>(p.up) + base;
+                const f32x4 x = ld<f32x4>(from), y = ld<f32x4>(from + 4);
+                const float o[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+                operand_of<PB>(o, b[t]);
+            } else {
+                b[t][0] = ld<u32x4>(static_cast<const uint16_t *>(p.up) + base);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < PB; ++x)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) b[t][x][d] = in ? b[t][x][d] : 0u;
+}
+
+// What 16 rows from `row` on get from their adapters, NT tiles of columns, as the
+// matrix instruction leaves its sums. The wave as a whole calls it.
+template <bool GRAD, bool NEAR, int PC, int PB, int NT>
+__device__ __forceinline__ void adapter_rows_by(const LinArgs &p, int64_t row, int64_t col, f32x4 (&d)[NT]) {
+    const int lane = threadIdx.x & (kWave - 1), q = lane >> 4, j = lane & 15;
+    int id;
+    const bool has = adapter_of(p, row + j, id);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) d[t] = f32x4{0, 0, 0, 0};
+    uint32_t pending = static_cast<uint32_t>(__ballot(has)) & 0xFFFFu;
+    while (pending != 0) {
+        const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(pending));
+        const uint32_t match = static_cast<uint32_t>(__ballot(has && id == g)) & 0xFFFFu;
+        pending &= ~match;
+        f32x4 e[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) e[t] = f32x4{0, 0, 0, 0};
+        for (int r0 = 0; r0 < p.rank; r0 += 32) {
+            u32x4 a[PC], b[NT][PB];
+            load_low<PC>(p, row + j, r0 + 8 * q, a);
+            load_up<GRAD, NEAR, PB, NT>(p, g, col, r0 + 8 * q, b);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) e[t] = mfma_parts<PC, PB>(a, b[t], e[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool mine = match >> (4 * q + i) & 1;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) d[t][i] = mine ? e[t][i] : d[t][i];
+        }
+    }
+}
+
+template <bool GRAD, bool NEAR, int PC, int NT>
+__device__ __forceinline__ void adapter_rows(const LinArgs &p, int64_t row, int64_t col, f32x4 (&d)[NT]) {
+    if (p.up_f32)
+        adapter_rows_by<GRAD, NEAR, 3, 3, NT>(p, row, col, d);
+    else
+        adapter_rows_by<GRAD, NEAR, PC, 1, NT>(p, row, col, d);
+}
+
+// low[m][r .. r + 7] . B[g][n][r .. r + 7] of one result, by one lane; zero past the rank.
+struct AdapterPiece {
+    f32x4 low[2];
+    u32x4 up[2];
+
+    __device__ __forceinline__ void load(const LinArgs &p, int64_t g, int64_t row, int64_t col, int r) {
+        const float *from = p.low + row * p.rank + r;
+        low[0] = ld<f32x4>(from), low[1] = ld<f32x4>(from + 4);
+        const int64_t base = (g * p.n_out + col) * p.rank + r;
+        if (p.up_f32) {
+            const float *b = static_cast<const float *>(p.up) + base;
+            up[0] = ld<u32x4>(b), up[1] = ld<u32x4>(b + 4);
+        } else {
+            up[0] = ld<u32x4>(static_cast<const uint16_t *>(p.up) + base);
+        }
+    }
+
+    __device__ __forceinline__ float dot(const LinArgs &p) const {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float b = p.up_f32 ? as_f(up[i / 4][i % 4]) : i % 2 == 0 ? bf16_lo(up[0][i / 2]) : bf16_hi(up[0][i / 2]);
+            v = __builtin_fmaf(low[i / 4][i % 4], b, v);
+        }
+        return v;
+    }
+};
+
+// What one result gets from its row's adapter, by one lane.
+__device__ __forceinline__ float adapter_dot(const LinArgs &p, int64_t row, int64_t col) {
+    int id;
+    float v = 0.0f;
+    if (!adapter_of(p, row, id)) return v;
+    for (int r = 0; r < p.rank; r += 8) {
+        AdapterPiece piece;
+        piece.load(p, id, row, col, r);
+        v += piece.dot(p);
+    }
+    return v;
+}
+
+}  // namespace zpp

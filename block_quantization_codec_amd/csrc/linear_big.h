@@ -60,6 +60,7 @@
 
 #include <type_traits>
 
+#include "linear_adapt.h"
 #include "linear_tile.h"
 
 namespace zpp {
@@ -461,6 +462,74 @@ struct LinBig {
         }
         if constexpr (M + 1 < MT) rows_from<HN, M + 1>(here, then, b, raw, s, bn, a, scale, acc, before);
     }
+
+    // Rows of tiles whose adapters' sums LDS holds at once, 64 bytes a lane each.
+    static constexpr int kHeld = kBufs * kBytes / (kBlockThreads * 64);
+    static constexpr int kApart = kHeld >= MT ? MT : kHeld >= 8 ? 8 : kHeld >= 4 ? 4 : kHeld >= 2 ? 2 : 1;
+
+    // Whether all rows of the tile have the same adapter (`one`; -1: none has any).
+    static __device__ __forceinline__ bool tile_adapter(const LinArgs &p, int64_t m0, int &one) {
+        const int lane = threadIdx.x & (kWave - 1);
+        one = -1;
+        bool same = true;
+#pragma unroll
+        for (int r = 0; r < kRows; r += kWave) {
+            const int64_t row = min(m0 + min(r + lane, kRows - 1), p.rows - 1);
+            int id;
+            if (!adapter_of(p, row, id)) id = -1;
+            const int first = __builtin_amdgcn_readfirstlane(id);
+            if (r == 0) one = first;
+            same = same && __ballot(id != one) == 0;
+        }
+        return same;
+    }
+
+    // acc += low up of adapter g, over the codes' factor. Low comes by buffer loads, whose
+    // range check gives zeros for rows past the end: addresses of 16 rows of tiles,
+    // kept over the loop, would not fit beside the sums.
+    template <int PC, int PU>
+    static __device__ __forceinline__ void add_adapter(const LinArgs &p, int64_t m0, int64_t col, int g,
+                                                       f32x4 (&acc)[MT][4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        const int lane = threadIdx.x & (kWave - 1), q = lane >> 4, j = lane & 15;
+        const int left = static_cast<int>(min(p.rows - m0, static_cast<int64_t>(kRows)));
+        const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<float *>(p.low + m0 * p.rank), 0, static_cast<uint32_t>(left * p.rank * 4), 0x27000);
+        const int mine = j * p.rank * 4;
+#pragma unroll 1
+        for (int r0 = 0; r0 < p.rank; r0 += 32) {
+            const int r = r0 + 8 * q;
+            // past the rank: an offset out of range
+            const int at = r < p.rank ? mine + r * 4 : 1 << 30;
+            u32x4 b[4][PU];
+            load_up<GRAD, true, PU, 4>(p, g, col, r, b);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int o = at + m * 16 * p.rank * 4;
+                const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(from, o, 0, 0),
+                            hi = __builtin_amdgcn_raw_buffer_load_b128(from, o, 16, 0);
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = as_f(lo[i]) * (1.0f / kCodeScale<BITS>);
+                    v[4 + i] = as_f(hi[i]) * (1.0f / kCodeScale<BITS>);
+                }
+                u32x4 a[PC];
+                operand_of<PC>(v, a);
+                operands_ready<kPin>();
+#pragma unroll
+                for (int x = PC - 1; x >= 0; --x)
+#pragma unroll
+                    for (int y = PU - 1; y >= 0; --y)
+                        if (x + y <= 2) {
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) mfma<kPin>(a[x], b[t][y], acc[m][t]);
+                        }
+                sums_ready<kPin>();
+            }
+        }
+#endif
+    }
 };
 
 template <bool GRAD, int BITS, int PA, int PB, int MT, LinMode MODE>
@@ -573,16 +642,67 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
         sums_ready<L::kPin>();
     }
 
+    // Adapters, with the first part of the contraction: into the sums where the tile's rows
+    // all have the same one, else apart, in rows of tiles that the free LDS holds.
+    // (256 sums a lane leave room for one way into them: binary32 adapters beside bf16
+    // activations and results, three parts each, take the other.)
+    [[maybe_unused]] bool apart = false;
+    if constexpr (MODE == LinMode::adapted) {
+        if (place.split == 0) {
+            int one;
+            apart = !L::tile_adapter(p, m0, one);
+            if constexpr (PA * PB == 1) {
+                apart = apart || (one >= 0 && p.up_f32);
+                if (!apart && one >= 0) L::template add_adapter<2, 1>(p, m0, col, one, acc);
+            } else {
+                if (!apart && one >= 0) {
+                    if (p.up_f32)
+                        L::template add_adapter<3, 3>(p, m0, col, one, acc);
+                    else
+                        L::template add_adapter<3, 1>(p, m0, col, one, acc);
+                }
+            }
+            if (apart) __syncthreads();  // no wave reads activations any more
+        }
+    }
+
+    constexpr int kTogether = MODE == LinMode::adapted ? L::kApart : MT;
+    f32x4 *const mine = reinterpret_cast<f32x4 *>(&tiles[0][0]) + threadIdx.x;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m1 = 0; m1 < MT; m1 += kTogether) {
+        if constexpr (MODE == LinMode::adapted) {
+            if (apart) {
+#pragma unroll 1
+                for (int m = 0; m < kTogether; ++m) {
+                    if (m0 + (m1 + m) * 16 >= p.rows) break;
+                    f32x4 d[4];
+                    adapter_rows<GRAD, true, PA * PB == 1 ? 2 : 3, 4>(p, m0 + (m1 + m) * 16, col, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = m0 + m * 16 + 4 * q + i;
-            if (row >= p.rows) continue;
-            float v[4];
+                    for (int t = 0; t < 4; ++t) mine[(m * 4 + t) * kBlockThreads] = d[t];
+                }
+            }
+        }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) v[t] = acc[m][t][i] * kCodeScale<BITS>;
-            store4(p, len, row, col, v, place.split);
+        for (int m = m1; m < m1 + kTogether; ++m) {
+            [[maybe_unused]] f32x4 d[4];
+            if constexpr (MODE == LinMode::adapted) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    d[t] = apart ? mine[((m - m1) * 4 + t) * kBlockThreads] : f32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = m0 + m * 16 + 4 * q + i;
+                if (row >= p.rows) continue;
+                float v[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) v[t] = acc[m][t][i] * kCodeScale<BITS>;
+                if constexpr (MODE == LinMode::adapted) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) v[t] = apart ? v[t] + d[t][i] : v[t];
+                }
+                store4(p, len, row, col, v, place.split);
+            }
         }
     }
 }

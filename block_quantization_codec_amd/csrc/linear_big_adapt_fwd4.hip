@@ -1,0 +1,10 @@
+// The tiled products on 4-bit codes: y = x W^T.
+#include "linear_big.h"
+
+namespace zpp {
+
+hipError_t launch_linear_big_adapt_fwd4(const LinArgs &p, int parts, int mt, hipStream_t stream) {
+    return launch_linear_big_as<LinMode::adapted, false, 4>(p, parts, mt, stream);
+}
+
+}  // namespace zpp

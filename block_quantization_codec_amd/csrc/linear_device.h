@@ -118,9 +118,15 @@ struct LinArgs {
     const int32_t *offsets;
     int groups;
     int64_t row0;
+    // rows with a low-rank adapter each (linear_adapt.h)
+    const float *low;    // [rows][rank]: what the row has become
+    const void *up;      // [adapters][out][rank] (y) or [adapters][rank][in] (dx)
+    const int32_t *ids;  // [rows]: which adapter, none if it is no number below `adapters`; null: the first, all of them
+    int up_f32, rank, adapters;
 };
 
-// What a product's rows multiply by: one matrix, or that of the row's group.
-enum class LinMode { one, grouped };
+// What a product's rows multiply by: one matrix, that of the row's group, or one
+// matrix and the row's adapter beside it.
+enum class LinMode { one, grouped, adapted };
 
 }  // namespace zpp

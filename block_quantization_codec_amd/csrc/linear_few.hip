@@ -14,6 +14,7 @@
 // x in registers and rotated into place takes one load for 16 instructions'
 // operands: loaded for each, x took as much of the path from L2 as the codes
 // and the first case 54 us. Non-temporal loads gained nothing.
+#include "linear_adapt.h"
 #include "linear_codes.h"
 
 namespace zpp {
@@ -74,11 +75,12 @@ struct Few {
     }
 };
 
-template <int BITS, int PA, int NT, int RM, int U, bool WIDE, int WK>
+template <int BITS, int PA, int NT, int RM, int U, bool WIDE, int WK, LinMode MODE>
 __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
     using F = Few<BITS, PA, NT, RM, U, WIDE>;
     using C = typename F::C;
     __shared__ float sums[WK][NT * 256];
+    [[maybe_unused]] __shared__ float added[MODE == LinMode::adapted ? WK : 1][kWave];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     const int64_t n0 = xcd_block(blockIdx.x, gridDim.x) * (16 * NT);
     const typename C::At at = C::place(p, n0);
@@ -88,6 +90,18 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
     f32x4 acc[NT][1];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t][0] = f32x4{0, 0, 0, 0};
+
+    // Adapters: wave w has indices 8 w .. 8 w + 7 of every 64, lane (row, column) as at the
+    // end. The first ones are asked for now.
+    constexpr bool kAdapted = MODE == LinMode::adapted;
+    [[maybe_unused]] AdapterPiece piece;
+    [[maybe_unused]] int adapter = 0;
+    [[maybe_unused]] bool has = false;
+    if constexpr (kAdapted) {
+        static_assert(NT == 1 && WK == 8);
+        has = adapter_of(p, lane >> 4, adapter) && n0 + (lane & 15) < p.n_out;
+        if (has && w * 8 < p.rank) piece.load(p, adapter, lane >> 4, n0 + (lane & 15), w * 8);
+    }
 
     // a wave's U chunks are neighbours: their codes fill whole cache lines
     for (int64_t k = static_cast<int64_t>(w) * U * kChunk; k < p.n_in; k += U * WK * kChunk) {
@@ -110,6 +124,14 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) sums[w][(t * 4 + i) * 16 + lane] = acc[t][0][i];
     }
+    if constexpr (kAdapted) {
+        float v = has && w * 8 < p.rank ? piece.dot(p) : 0.0f;
+        for (int r = w * 8 + 64; has && r < p.rank; r += 64) {
+            piece.load(p, adapter, lane >> 4, n0 + (lane & 15), r);
+            v += piece.dot(p);
+        }
+        added[w][lane] = v;
+    }
     __syncthreads();
     for (int o = threadIdx.x; o < NT * 64; o += WK * kWave) {
         const int64_t row_out = o >> 4 & 3, col = n0 + (o >> 6) * 16 + (o & 15);
@@ -119,6 +141,12 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
         for (int k = 0; k < WK; ++k) v += sums[k][o];
         v *= kCodeScale<BITS>;
         if (out_of_range(v)) v = scaled_sum<BITS, PA>(p, row_out, col, 0, p.n_in);
+        if constexpr (kAdapted) {
+            float more = 0.0f;
+#pragma unroll
+            for (int k = 0; k < WK; ++k) more += added[k][o];
+            v += more;
+        }
         if (p.out_f32)
             static_cast<float *>(p.out)[row_out * p.ldo + col] = v;
         else
@@ -126,30 +154,37 @@ __global__ __launch_bounds__(WK *kWave) void linear_few_kernel(LinArgs p) {
     }
 }
 
-template <int BITS, int PA, int RM>
+template <LinMode MODE, int BITS, int PA, int RM>
 hipError_t launch_as(const LinArgs &p, bool wide, hipStream_t stream) {
     constexpr int NT = 1, U = 4, WK = 8;
     const unsigned grid = static_cast<unsigned>((p.n_out + 16 * NT - 1) / (16 * NT));
     if (wide)
-        linear_few_kernel<BITS, PA, NT, RM, U, true, WK><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, true, WK, MODE><<<grid, WK * kWave, 0, stream>>>(p);
     else
-        linear_few_kernel<BITS, PA, NT, RM, U, false, WK><<<grid, WK * kWave, 0, stream>>>(p);
+        linear_few_kernel<BITS, PA, NT, RM, U, false, WK, MODE><<<grid, WK * kWave, 0, stream>>>(p);
     return hipGetLastError();
 }
 
-template <int BITS, int PA>
+template <LinMode MODE, int BITS, int PA>
 hipError_t launch_rows(const LinArgs &p, bool wide, hipStream_t stream) {
-    if (p.rows == 1) return launch_as<BITS, PA, 1>(p, wide, stream);
-    if (p.rows == 2) return launch_as<BITS, PA, 2>(p, wide, stream);
-    return launch_as<BITS, PA, 4>(p, wide, stream);
+    if (p.rows == 1) return launch_as<MODE, BITS, PA, 1>(p, wide, stream);
+    if (p.rows == 2) return launch_as<MODE, BITS, PA, 2>(p, wide, stream);
+    return launch_as<MODE, BITS, PA, 4>(p, wide, stream);
+}
+
+template <LinMode MODE>
+hipError_t launch_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream) {
+    const bool wide = p.log2b >= 7 && p.n_in % kChunk == 0;
+    if (bits == 4)
+        return a_f32 ? launch_rows<MODE, 4, 3>(p, wide, stream) : launch_rows<MODE, 4, 1>(p, wide, stream);
+    return a_f32 ? launch_rows<MODE, 8, 3>(p, wide, stream) : launch_rows<MODE, 8, 1>(p, wide, stream);
 }
 
 }  // namespace
 
 hipError_t launch_linear_few(const LinArgs &p, int bits, bool a_f32, hipStream_t stream) {
-    const bool wide = p.log2b >= 7 && p.n_in % kChunk == 0;
-    if (bits == 4) return a_f32 ? launch_rows<4, 3>(p, wide, stream) : launch_rows<4, 1>(p, wide, stream);
-    return a_f32 ? launch_rows<8, 3>(p, wide, stream) : launch_rows<8, 1>(p, wide, stream);
+    return p.adapters > 0 ? launch_few<LinMode::adapted>(p, bits, a_f32, stream)
+                          : launch_few<LinMode::one>(p, bits, a_f32, stream);
 }
 
 }  // namespace zpp

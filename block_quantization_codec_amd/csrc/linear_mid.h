@@ -17,6 +17,7 @@
 // Reading the operands from LDS an instruction ahead gained nothing.
 #pragma once
 
+#include "linear_adapt.h"
 #include "linear_codes.h"
 #include "linear_tile.h"
 
@@ -114,6 +115,17 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
         else
             static_cast<uint16_t *>(p.out)[row * p.ldo + col] = static_cast<uint16_t>(pack_rn(v, 0.0f));
     };
+    [[maybe_unused]] f32x4 more[MODE == LinMode::adapted ? MT : 1][NT];
+    if constexpr (MODE == LinMode::adapted) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) more[m][t] = f32x4{0, 0, 0, 0};
+            // once: with the first part of the contraction
+            if (split == 0 && m0 + m * 16 < p.rows)
+                adapter_rows<false, false, 3, NT>(p, m0 + m * 16, n0 + (lane & 15), more[m]);
+        }
+    }
     uint32_t again = 0;  // of the lane's results, those out of range: stored once more at the end
     static_assert(NT * MT * 4 <= 32, "a bit each");
 #pragma unroll
@@ -127,13 +139,18 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
                 if (row >= p.rows || col >= p.n_out) continue;
                 const float v = acc[t][m][i] * kCodeScale<BITS>;
                 again |= out_of_range(v) ? 1u << ((t * MT + m) * 4 + i) : 0u;
-                store(row, col, v);
+                if constexpr (MODE == LinMode::adapted)
+                    store(row, col, v + more[m][t][i]);
+                else
+                    store(row, col, v);
             }
     }
     for (; again != 0; again &= again - 1) {
         const int b = __builtin_ctz(again), t = b / (4 * MT), m = b / 4 % MT;
         const int64_t row = m0 + m * 16 + 4 * q + b % 4, col = n0 + t * 16 + (lane & 15);
-        store(row, col, scaled_sum<BITS, PA>(p, row, col, k0, k1));
+        float v = scaled_sum<BITS, PA>(p, row, col, k0, k1);
+        if constexpr (MODE == LinMode::adapted) v += split == 0 ? adapter_dot(p, row, col) : 0.0f;
+        store(row, col, v);
     }
 }
 

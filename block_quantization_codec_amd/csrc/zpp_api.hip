@@ -247,6 +247,28 @@ zpp_status linear(bool grad, const void *a, int32_t a_dtype, int64_t a_stride, i
     });
 }
 
+// What the adapters' calls have in common, and what they refuse.
+struct Adapters {
+    const void *a, *b;
+    int32_t dtype;
+    int64_t adapters, rank;
+    const int32_t *ids;
+    const float *scaling;
+
+    bool sizes(int64_t n_out, int64_t n_in) const {
+        return is_dtype(dtype) && adapters >= 1 && adapters <= ZPP_MAX_GROUPS && rank >= 8 && rank <= ZPP_MAX_RANK &&
+               rank % 8 == 0 && n_out <= ZPP_MAX_NUMEL / (adapters * rank) && n_in <= ZPP_MAX_NUMEL / (adapters * rank);
+    }
+    bool is_aligned() const { return aligned(a, 16) && aligned(b, 16) && aligned(ids, 4) && aligned(scaling, 4); }
+    Range range_a(int64_t n_in) const { return matrix(a, adapters * rank, n_in, n_in, dtype); }
+    Range range_b(int64_t n_out) const { return matrix(b, adapters * rank, n_out, n_out, dtype); }
+    Range range_ids(int64_t rows) const { return Range{ids, ids ? 4 * rows : 0}; }
+    Range range_scaling() const { return Range{scaling, scaling ? 4 * adapters : 0}; }
+    zpp::LinAdapters launch() const {
+        return zpp::LinAdapters{a, b, dtype == ZPP_FP32, adapters, rank, ids, scaling};
+    }
+};
+
 // As many matrices of this size as the codes of one call may hold.
 bool is_groups(int64_t groups, int64_t n_out, int64_t n_in) {
     return groups >= 1 && groups <= ZPP_MAX_GROUPS && (n_out < 1 || n_in < 1 || n_out <= ZPP_MAX_NUMEL / n_in / groups);
@@ -492,6 +514,113 @@ int64_t zpp_linear_grouped_workspace(int32_t grad, int32_t in_dtype, int64_t in_
     if (!is_stride(in_stride, rows, grad != 0 ? out_features : in_features)) return 0;
     return zpp::linear_workspace(grad != 0, in_dtype == ZPP_FP32, in_stride, out_dtype == ZPP_FP32, rows, groups,
                                  out_features, in_features);
+}
+
+zpp_status zpp_linear_adapters(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, const void *codes,
+                               const float *scales, int32_t bits, int64_t out_features, int64_t in_features,
+                               int32_t block, const void *a, const void *b, int32_t ab_dtype, int64_t adapters,
+                               int64_t rank, const int32_t *ids, const float *scaling, float *reduced, void *y,
+                               int32_t y_dtype, int64_t y_stride, void *workspace, int64_t workspace_bytes,
+                               void *stream) {
+    const Adapters ad{a, b, ab_dtype, adapters, rank, ids, scaling};
+    if (!is_dtype(x_dtype) || !is_dtype(y_dtype)) return ZPP_ERR_ARG;
+    if (bits != 8 && bits != 4) return ZPP_ERR_ARG;
+    if (!is_linear_size(rows, out_features, in_features) || !ad.sizes(out_features, in_features)) return ZPP_ERR_ARG;
+    if (!is_pow2_block(block) || out_features * in_features % block != 0) return ZPP_ERR_ARG;
+    if (!is_stride(x_stride, rows, in_features) || !is_stride(y_stride, rows, out_features)) return ZPP_ERR_ARG;
+    if (workspace_bytes < 0) return ZPP_ERR_ARG;
+    if (rows == 0) return ZPP_OK;
+    if (rows == 1) x_stride = in_features;
+    const int64_t need = zpp::linear_adapters_workspace(false, x_dtype == ZPP_FP32, x_stride, y_dtype == ZPP_FP32, rows,
+                                                        out_features, in_features, adapters, rank);
+    if (workspace_bytes < need) return ZPP_ERR_ARG;
+    if (!x || !codes || !scales || !a || !b || !reduced || !y || (need > 0 && !workspace)) return ZPP_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(reduced, 16) || !aligned(y, 16))
+        return ZPP_ERR_ALIGN;
+    if (!ad.is_aligned() || (need > 0 && !aligned(workspace, 16))) return ZPP_ERR_ALIGN;
+    if (x_stride * dtype_bytes(x_dtype) % 16 != 0) return ZPP_ERR_ALIGN;
+    const int64_t weights = out_features * in_features;
+    const Range rx = matrix(x, rows, x_stride, in_features, x_dtype), rc{codes, code_bytes(weights, bits)},
+        rs{scales, 4 * (weights / block)}, ra = ad.range_a(in_features), rb = ad.range_b(out_features),
+        ri = ad.range_ids(rows), rg = ad.range_scaling(), rr{reduced, 4 * rows * rank},
+        ry = matrix(y, rows, y_stride, out_features, y_dtype), rw{workspace, need};
+    for (const Range &o : {rr, ry, rw}) {
+        for (const Range &r : {rx, rc, rs, ra, rb, ri, rg})
+            if (overlap(o, r)) return ZPP_ERR_OVERLAP;
+    }
+    if (overlap(rr, ry) || overlap(rr, rw) || overlap(ry, rw)) return ZPP_ERR_OVERLAP;
+    const Range all[] = {rx, rc, rs, ra, rb, ri, rg, rr, ry, rw};
+    if (zpp_status s = check_all(all); s != ZPP_OK) return s;
+    return launch_checked([&] {
+        return zpp::launch_linear_adapters(x, x_dtype == ZPP_FP32, x_stride, rows, codes, scales, bits, out_features,
+                   in_features, log2_of(block), ad.launch(), reduced, y, y_dtype == ZPP_FP32, y_stride, workspace,
+                   static_cast<hipStream_t>(stream));
+    });
+}
+
+zpp_status zpp_linear_adapters_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, const void *x, int64_t x_stride,
+                                    const float *reduced, int64_t rows, const void *codes, const float *scales,
+                                    int32_t bits, int64_t out_features, int64_t in_features, int32_t block,
+                                    const void *a, const void *b, int32_t ab_dtype, int64_t adapters, int64_t rank,
+                                    const int32_t *ids, const float *scaling, void *dx, int32_t dx_dtype,
+                                    int64_t dx_stride, void *da, void *db, void *workspace, int64_t workspace_bytes,
+                                    void *stream) {
+    const Adapters ad{a, b, ab_dtype, adapters, rank, ids, scaling};
+    if (!is_dtype(dy_dtype) || !is_dtype(dx_dtype)) return ZPP_ERR_ARG;
+    if (bits != 8 && bits != 4) return ZPP_ERR_ARG;
+    if (!is_linear_size(rows, out_features, in_features) || !ad.sizes(out_features, in_features)) return ZPP_ERR_ARG;
+    if (!is_pow2_block(block) || out_features * in_features % block != 0) return ZPP_ERR_ARG;
+    if (!is_stride(dy_stride, rows, out_features) || !is_stride(x_stride, rows, in_features) ||
+        !is_stride(dx_stride, rows, in_features))
+        return ZPP_ERR_ARG;
+    if (rows == 1) dx_stride = in_features;
+    const int64_t need = zpp::linear_adapters_workspace(true, dy_dtype == ZPP_FP32, dy_stride, dx_dtype == ZPP_FP32,
+                                                        rows, out_features, in_features, adapters, rank);
+    if (workspace_bytes < need) return ZPP_ERR_ARG;
+    if (rows == 0 && !da && !db) return ZPP_OK;
+    if (rows > 0 && (!dy || !codes || !scales || !a || !b || !dx)) return ZPP_ERR_NULL;
+    if (rows > 0 && ((da && !x) || (db && !reduced))) return ZPP_ERR_NULL;
+    if (need > 0 && !workspace) return ZPP_ERR_NULL;
+    if (!aligned(da, 16) || !aligned(db, 16) || (need > 0 && !aligned(workspace, 16))) return ZPP_ERR_ALIGN;
+    if (rows > 0) {
+        if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(reduced, 16) || !aligned(codes, 16) || !aligned(scales, 4) ||
+            !aligned(dx, 16) || !ad.is_aligned())
+            return ZPP_ERR_ALIGN;
+        if (dx_stride * dtype_bytes(dx_dtype) % 16 != 0) return ZPP_ERR_ALIGN;
+    }
+    const int64_t weights = rows > 0 ? out_features * in_features : 0, n = rows > 0 ? 1 : 0;
+    const Range rd = matrix(dy, rows, dy_stride, out_features, dy_dtype),
+        rx = matrix(x, rows, x_stride, in_features, dy_dtype), rr{reduced, reduced ? 4 * rows * rank : 0},
+        rc{codes, code_bytes(weights, bits)}, rs{scales, 4 * (weights / block)},
+        ra{a, n * ad.range_a(in_features).bytes}, rb{b, n * ad.range_b(out_features).bytes}, ri = ad.range_ids(rows),
+        rg{scaling, n * ad.range_scaling().bytes}, ro = matrix(dx, rows, dx_stride, in_features, dx_dtype),
+        rda = matrix(da, adapters * rank, in_features, in_features, ab_dtype),
+        rdb = matrix(db, adapters * rank, out_features, out_features, ab_dtype), rw{workspace, need};
+    const Range outs[] = {ro, rda, rdb, rw};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range &r : {rd, rx, rr, rc, rs, ra, rb, ri, rg})
+            if (overlap(outs[i], r)) return ZPP_ERR_OVERLAP;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return ZPP_ERR_OVERLAP;
+    }
+    const Range all[] = {rd, rx, rr, rc, rs, ra, rb, ri, rg, ro, rda, rdb, rw};
+    if (zpp_status s = check_all(all); s != ZPP_OK) return s;
+    return launch_checked([&] {
+        return zpp::launch_linear_adapters_grad(dy, dy_dtype == ZPP_FP32, dy_stride, x, x_stride, reduced, rows, codes,
+                   scales, bits, out_features, in_features, log2_of(block), ad.launch(), dx, dx_dtype == ZPP_FP32,
+                   dx_stride, da, db, workspace, static_cast<hipStream_t>(stream));
+    });
+}
+
+int64_t zpp_linear_adapters_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
+                                      int64_t rows, int64_t out_features, int64_t in_features, int64_t adapters,
+                                      int64_t rank) {
+    const Adapters ad{nullptr, nullptr, ZPP_BF16, adapters, rank, nullptr, nullptr};
+    if (!is_dtype(in_dtype) || !is_dtype(out_dtype) || !is_linear_size(rows, out_features, in_features)) return 0;
+    if (!ad.sizes(out_features, in_features)) return 0;
+    if (!is_stride(in_stride, rows, grad != 0 ? out_features : in_features)) return 0;
+    return zpp::linear_adapters_workspace(grad != 0, in_dtype == ZPP_FP32, in_stride, out_dtype == ZPP_FP32, rows,
+                                          out_features, in_features, adapters, rank);
 }
 
 zpp_status zpp_layer_norm(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t width,

@@ -84,7 +84,8 @@ extern "C" {
 #define ZPP_MAX_DIVISOR 16777216 /* 2^24: every divisor up to it is exact in binary32 */
 #define ZPP_MAX_FEATURES 4194304 /* 2^22: the longest row of a weight matrix or of a norm */
 #define ZPP_MAX_ROWS 1073741824  /* 2^30: the most rows of one linear or norm call */
-#define ZPP_MAX_GROUPS 4096      /* the most weight matrices of one grouped linear call */
+#define ZPP_MAX_GROUPS 4096      /* the most weight matrices of one grouped linear call, and adapters of another */
+#define ZPP_MAX_RANK 256         /* the largest rank of an adapter */
 /* 2^40: the largest element count, input stride (bytes for codes, floats
  * for scales), and reordered buffer (elements, or bytes / 4) accepted; far
  * beyond any GPU's memory, it keeps every byte range of a call exact in
@@ -382,6 +383,75 @@ zpp_status zpp_linear_grouped_grad(const void *dy, int32_t dy_dtype, int64_t dy_
  * (grad != 0) needs, as zpp_linear_blocks_workspace; 0 for sizes the calls refuse. */
 int64_t zpp_linear_grouped_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
                                      int64_t rows, int64_t groups, int64_t out_features, int64_t in_features);
+
+/*
+ * Linear products on block-quantized weights with a low-rank adapter beside them: a
+ * weight that stays as codes serves many requests, and is trained, through adapters. Row
+ * m has adapter g = ids[m], a number in [0, adapters), or none (any other number):
+ *
+ *   reduced[m] = s_g * sum over k of x[m][k] * A[g][.][k]            (zeros without an adapter)
+ *   y[m][n]    = sum over k of x[m][k] * W[n][k] + sum over r of reduced[m][r] * B[g][n][r]
+ *
+ * Rows of one adapter need not be neighbours, though long prompts are faster if they are.
+ * The sum is rounded once, to y_dtype. What is said of zpp_linear_blocks holds for x, the
+ * codes, y, their strides and the first product's precision. Adapters enter exactly,
+ * `reduced` is binary32; where x, y and the adapters are all ZPP_BF16, it enters the
+ * second product with 16 bits or more. Nothing of an adapter, not its infinities or NaNs
+ * either, reaches rows that do not name it.
+ *
+ *   a         in   adapters x rank x in_features elements of ab_dtype, 16-B aligned, without gaps
+ *   b         in   adapters x out_features x rank elements of ab_dtype, 16-B aligned, without gaps
+ *   adapters  in   1..ZPP_MAX_GROUPS
+ *   rank      in   a multiple of 8, 8..ZPP_MAX_RANK (fill up smaller ones with zeros); adapters * rank times
+ *                  out_features, and times in_features, <= ZPP_MAX_NUMEL
+ *   ids       in   rows int32, 4-B aligned, in device memory; NULL: every row has adapter 0
+ *   scaling   in   adapters floats (s_g), 4-B aligned, in device memory; NULL: ones
+ *   reduced   out  rows x rank floats, 16-B aligned: what the backward pass needs
+ *   workspace_bytes  in  at least zpp_linear_adapters_workspace(0, ...) (ZPP_ERR_ARG otherwise)
+ */
+zpp_status zpp_linear_adapters(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, const void *codes,
+                               const float *scales, int32_t bits, int64_t out_features, int64_t in_features,
+                               int32_t block, const void *a, const void *b, int32_t ab_dtype, int64_t adapters,
+                               int64_t rank, const int32_t *ids, const float *scaling, float *reduced, void *y,
+                               int32_t y_dtype, int64_t y_stride, void *workspace, int64_t workspace_bytes,
+                               void *stream);
+
+/*
+ * The backward pass of zpp_linear_adapters: with u[m] = s_g * sum over n of dy[m][n] * B[g][n][.],
+ *
+ *   dx[m][k]    = sum over n of dy[m][n] * W[n][k] + sum over r of u[m][r] * A[g][r][k]
+ *   da[g][r][k] = sum over the rows m of adapter g of u[m][r] * x[m][k]
+ *   db[g][n][r] = sum over the rows m of adapter g of dy[m][n] * reduced[m][r]
+ *
+ * Sums are binary32, in an order fixed by the sizes and the ids, and rounded once: the same
+ * inputs give the same bits. An adapter without rows gets zeros.
+ *
+ *   dy        in   rows of out_features elements of dy_dtype, as in zpp_linear_blocks_grad
+ *   x         in   rows of in_features elements of dy_dtype, 16-B aligned, x_stride (any) between rows, as in the
+ *                  forward pass; may be NULL without da
+ *   reduced   in   as the forward pass wrote it; may be NULL without db
+ *   a, b, ab_dtype, adapters, rank, ids, scaling
+ *             in   as in the forward pass
+ *   dx        out  rows of in_features elements of dx_dtype, as in zpp_linear_blocks_grad
+ *   da        out  adapters x rank x in_features elements of ab_dtype, 16-B aligned, or NULL
+ *   db        out  adapters x out_features x rank elements of ab_dtype, 16-B aligned, or NULL
+ *   workspace_bytes  in  at least zpp_linear_adapters_workspace(1, ...) (ZPP_ERR_ARG otherwise)
+ * With rows == 0, da and db are set to zero (the empty sums).
+ */
+zpp_status zpp_linear_adapters_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, const void *x, int64_t x_stride,
+                                    const float *reduced, int64_t rows, const void *codes, const float *scales,
+                                    int32_t bits, int64_t out_features, int64_t in_features, int32_t block,
+                                    const void *a, const void *b, int32_t ab_dtype, int64_t adapters, int64_t rank,
+                                    const int32_t *ids, const float *scaling, void *dx, int32_t dx_dtype,
+                                    int64_t dx_stride, void *da, void *db, void *workspace, int64_t workspace_bytes,
+                                    void *stream);
+
+/* Bytes of workspace that zpp_linear_adapters (grad == 0) or zpp_linear_adapters_grad (grad != 0)
+ * needs for these types, sizes and row stride of x (dy); it depends on the arguments alone. 0 for sizes the
+ * calls refuse. */
+int64_t zpp_linear_adapters_workspace(int32_t grad, int32_t in_dtype, int64_t in_stride, int32_t out_dtype,
+                                      int64_t rows, int64_t out_features, int64_t in_features, int64_t adapters,
+                                      int64_t rank);
 
 /*
  * Layer norm over each row of `width` elements, as it stands before the
