@@ -21,7 +21,7 @@ ARCH = os.environ.get("ZPP_OFFLOAD_ARCH", "gfx950")
 
 DRR_UNITS = [f"drr_in{i}_out{o}.hip" for i in (4, 8) for o in (0, 4, 8)]
 LINEAR_UNITS = ["linear_few.hip", "linear_mid.hip", "linear_mid_group.hip", "linear_mid_adapt.hip", "linear_adapt.hip",
-                *(f"linear_big_{g}{d}{b}.hip" for g in ("", "group_", "adapt_")
+                *(f"linear_{g}_{d}{b}.hip" for g in ("big", "big_group", "adapt")
                   for d in ("fwd", "grad") for b in (4, 8))]
 SOURCES = ["quantize.hip", "dequantize.hip", "reorder.hip", "drr.hip", *DRR_UNITS, "linear.hip", *LINEAR_UNITS,
            "layer_norm.hip", "rms_norm.hip", "zpp_api.hip"]

@@ -21,10 +21,10 @@ hipError_t launch_linear_big_group_fwd8(const LinArgs &p, int parts, int mt, hip
 hipError_t launch_linear_big_group_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
 hipError_t launch_linear_big_group_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
 hipError_t launch_linear_mid_adapt(const LinArgs &p, int bits, bool a_f32, int mt, hipStream_t stream);
-hipError_t launch_linear_big_adapt_fwd4(const LinArgs &p, int parts, int mt, hipStream_t stream);
-hipError_t launch_linear_big_adapt_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream);
-hipError_t launch_linear_big_adapt_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
-hipError_t launch_linear_big_adapt_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_adapt_fwd4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_adapt_fwd8(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_adapt_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream);
+hipError_t launch_linear_adapt_grad8(const LinArgs &p, int parts, int mt, hipStream_t stream);
 
 namespace {
 
@@ -364,11 +364,11 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
             e = ad ? launch_linear_mid_adapt(p, bits, in_f32, plan.mt, stream)
                    : launch_linear_mid(p, bits, in_f32, plan.mt, stream);
         } else if (ad && grad) {
-            e = bits == 4 ? launch_linear_big_adapt_grad4(p, parts, plan.mt, stream)
-                          : launch_linear_big_adapt_grad8(p, parts, plan.mt, stream);
+            e = bits == 4 ? launch_linear_adapt_grad4(p, parts, plan.mt, stream)
+                          : launch_linear_adapt_grad8(p, parts, plan.mt, stream);
         } else if (ad) {
-            e = bits == 4 ? launch_linear_big_adapt_fwd4(p, parts, plan.mt, stream)
-                          : launch_linear_big_adapt_fwd8(p, parts, plan.mt, stream);
+            e = bits == 4 ? launch_linear_adapt_fwd4(p, parts, plan.mt, stream)
+                          : launch_linear_adapt_fwd8(p, parts, plan.mt, stream);
         } else if (grad) {
             e = bits == 4 ? launch_linear_big_grad4(p, parts, plan.mt, stream)
                           : launch_linear_big_grad8(p, parts, plan.mt, stream);

@@ -7,9 +7,9 @@
 // a pass of its own would read and write the result again, and round it twice.
 //
 // Rows of a tile may have different adapters. Tiles whose rows all have one take it
-// into their sums by more matrix instructions. Others multiply 16 rows by each
-// adapter that one of them names, and each row keeps its own one's: so nothing of
-// an adapter, not its infinities or NaNs either, reaches another's rows.
+// into their sums by more matrix instructions. In others the rows of each adapter are
+// gathered and multiplied by themselves, so that nothing of an adapter, not its
+// infinities or NaNs either, reaches another's rows.
 //
 // Precision: low is binary32 and enters as bf16 parts, like binary32 activations:
 // two of them (16 bits: off by 2^-17, against the 2^-9 of a bf16 result) from
@@ -120,45 +120,109 @@ __device__ __forceinline__ void load_up(const LinArgs &p, int64_t g, int64_t col
             for (int d = 0; d < 4; ++d) b[t][x][d] = in ? b[t][x][d] : 0u;
 }
 
-// What 16 rows from `row` on get from their adapters, NT tiles of columns, as the
-// matrix instruction leaves its sums. The wave as a whole calls it.
-template <bool GRAD, bool NEAR, int PC, int PB, int NT>
-__device__ __forceinline__ void adapter_rows_by(const LinArgs &p, int64_t row, int64_t col, f32x4 (&d)[NT]) {
-    const int lane = threadIdx.x & (kWave - 1), q = lane >> 4, j = lane & 15;
-    int id;
-    const bool has = adapter_of(p, row + j, id);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) d[t] = f32x4{0, 0, 0, 0};
-    uint32_t pending = static_cast<uint32_t>(__ballot(has)) & 0xFFFFu;
-    while (pending != 0) {
-        const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(pending));
-        const uint32_t match = static_cast<uint32_t>(__ballot(has && id == g)) & 0xFFFFu;
-        pending &= ~match;
-        f32x4 e[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) e[t] = f32x4{0, 0, 0, 0};
-        for (int r0 = 0; r0 < p.rank; r0 += 32) {
-            u32x4 a[PC], b[NT][PB];
-            load_low<PC>(p, row + j, r0 + 8 * q, a);
-            load_up<GRAD, NEAR, PB, NT>(p, g, col, r0 + 8 * q, b);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) e[t] = mfma_parts<PC, PB>(a, b[t], e[t]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool mine = match >> (4 * q + i) & 1;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) d[t][i] = mine ? e[t][i] : d[t][i];
-        }
-    }
+// The numbers of match's set bits, in order, one a lane: lane n has the n-th's. They move
+// between lanes without memory: one more array in LDS, and the compiler would wait in the
+// tiled products' loops for all of the loads into theirs (twice the time).
+__device__ __forceinline__ int list_bits(uint64_t match) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const uint64_t below = (1ull << lane) - 1;
+    // the other lanes' numbers go behind: every lane sends, and every lane gets one
+    const int at = match >> lane & 1 ? __popcll(match & below) : __popcll(match) + __popcll(~match & below);
+    return __builtin_amdgcn_ds_permute(at * 4, lane);
 }
 
-template <bool GRAD, bool NEAR, int PC, int NT>
-__device__ __forceinline__ void adapter_rows(const LinArgs &p, int64_t row, int64_t col, f32x4 (&d)[NT]) {
-    if (p.up_f32)
-        adapter_rows_by<GRAD, NEAR, 3, 3, NT>(p, row, col, d);
+// Entry n of such a list, n of the lane's own.
+__device__ __forceinline__ int listed(int list, int n) { return __builtin_amdgcn_ds_bpermute(n * 4, list); }
+
+// What ROWS (up to 64) rows from `row0` on get from their adapters in the wave's NT
+// tiles of columns, into LDS of the wave's own: held[row][columns], 16 NT a row, tile
+// t's at 16 t + (lane & 15), or, NEAR, at 4 (lane & 15) + t. Rows without an adapter get
+// zeros. Of the rows' adapters, in the order of their first rows, it takes every
+// `parts`-th from `part` on; the others' rows get zeros too.
+//
+// The rows of an adapter, wherever they stand, are the matrix instruction's rows. NB
+// adapters at a time: their operands' loads, each a trip to memory where every row
+// has an adapter of its own, are under way together. One by one, 48 rows of 28672 x
+// 8192 with 32 adapters of rank 64 took 75 us more than without adapters.
+template <bool GRAD, bool NEAR, int PC, int PB, int NT, int ROWS, int NB>
+__device__ __forceinline__ void adapter_gather(const LinArgs &p, int64_t row0, int64_t col, int part, int parts,
+                                               float *held) {
+    static_assert(ROWS <= kWave && ROWS % 16 == 0);
+    const int lane = threadIdx.x & (kWave - 1), q = lane >> 4, j = lane & 15;
+#pragma unroll
+    for (int i = 0; i < ROWS * NT / 16; ++i)
+        reinterpret_cast<f32x4 *>(held)[i * kWave + lane] = f32x4{0, 0, 0, 0};
+    int id;
+    const bool has = adapter_of(p, row0 + lane, id) && lane < ROWS;
+    uint64_t pending = __ballot(has);
+    int n = 0;
+    while (pending != 0) {
+        int g[NB], count[NB], list[NB], most = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            g[b] = b == 0 ? 0 : g[0];
+            count[b] = list[b] = 0;
+            while (pending != 0 && count[b] == 0) {
+                const int c = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
+                const uint64_t match = __ballot(has && id == c);
+                pending &= ~match;
+                if (n++ % parts != part) continue;
+                g[b] = c;
+                count[b] = __popcll(match);
+                list[b] = list_bits(match);
+            }
+            most = max(most, count[b]);
+        }
+        for (int l0 = 0; l0 < most; l0 += 16) {
+            int64_t row[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                row[b] = row0 + listed(list[b], l0 + j < count[b] ? l0 + j : 0);
+            f32x4 e[NB][NT];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) e[b][t] = f32x4{0, 0, 0, 0};
+            for (int r0 = 0; r0 < p.rank; r0 += 32) {
+                u32x4 low[NB][PC], up[NB][NT][PB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    load_up<GRAD, NEAR, PB, NT>(p, g[b], col, r0 + 8 * q, up[b]);
+                    load_low<PC>(p, row[b], r0 + 8 * q, low[b]);
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) e[b][t] = mfma_parts<PC, PB>(low[b], up[b][t], e[b][t]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = l0 + 4 * q + i, to_row = listed(list[b], at & (kWave - 1));
+                    if (at >= count[b]) continue;
+                    float *to = held + to_row * (16 * NT);
+                    if constexpr (NEAR) {
+                        static_assert(NT == 4);
+                        *reinterpret_cast<f32x4 *>(to + 4 * j) = f32x4{e[b][0][i], e[b][1][i], e[b][2][i], e[b][3][i]};
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) to[16 * t + j] = e[b][t][i];
+                    }
+                }
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <bool GRAD, bool NEAR, int PC, int NT, int ROWS, int NB>
+__device__ __forceinline__ void adapter_rows(const LinArgs &p, int64_t row0, int64_t col, int part, int parts,
+                                             float *held) {
+    if (p.up_f32)  // three parts each: half as many at a time fit
+        adapter_gather<GRAD, NEAR, 3, 3, NT, ROWS, (NB + 1) / 2>(p, row0, col, part, parts, held);
     else
-        adapter_rows_by<GRAD, NEAR, PC, 1, NT>(p, row, col, d);
+        adapter_gather<GRAD, NEAR, PC, 1, NT, ROWS, NB>(p, row0, col, part, parts, held);
 }
 
 // low[m][r .. r + 7] . B[g][n][r .. r + 7] of one result, by one lane; zero past the rank.
@@ -188,18 +252,5 @@ struct AdapterPiece {
         return v;
     }
 };
-
-// What one result gets from its row's adapter, by one lane.
-__device__ __forceinline__ float adapter_dot(const LinArgs &p, int64_t row, int64_t col) {
-    int id;
-    float v = 0.0f;
-    if (!adapter_of(p, row, id)) return v;
-    for (int r = 0; r < p.rank; r += 8) {
-        AdapterPiece piece;
-        piece.load(p, id, row, col, r);
-        v += piece.dot(p);
-    }
-    return v;
-}
 
 }  // namespace zpp

@@ -46,16 +46,6 @@ __device__ __forceinline__ bool has_adapter(const AdaptArgs &p, int64_t row, int
     return in && static_cast<uint32_t>(id) < static_cast<uint32_t>(p.adapters);
 }
 
-// The set bits of `match`, in order, as the numbers list[0] .. (of this wave alone).
-__device__ __forceinline__ int list_bits(uint64_t match, uint8_t *list) {
-    const int lane = threadIdx.x & (kWave - 1);
-    __builtin_amdgcn_wave_barrier();
-    if (match >> lane & 1) list[__popcll(match & ((1ull << lane) - 1))] = static_cast<uint8_t>(lane);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    return __popcll(match);
-}
-
 // ---- down -------------------------------------------------------------------------
 
 // 16 elements of a row from k on as operand parts of two matrix instructions:
@@ -148,13 +138,13 @@ __device__ __forceinline__ void load_w(const AdaptArgs &p, int64_t g, int r, int
 // workgroup's 4 waves take steps of 64 indices in turn and join their sums in LDS.
 template <bool GRAD, bool XF32, bool WF32, int MT>
 __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int64_t rank0, int split, int g, int count,
-                                          const uint8_t *list, f32x4 *sums) {
+                                          int list, f32x4 *sums) {
     constexpr int PX = XF32 ? 3 : 1, PW = WF32 ? 3 : 1;
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block(), q = lane >> 4, j = lane & 15;
     const int r = static_cast<int>(rank0) + 4 * j;
     int64_t at[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) at[m] = (chunk * 64 + list[min(16 * m + j, count - 1)]) * p.x_stride;
+    for (int m = 0; m < MT; ++m) at[m] = (chunk * 64 + listed(list, min(16 * m + j, count - 1))) * p.x_stride;
     f32x4 acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -189,9 +179,9 @@ __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int
         f32x4 v = {0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < 4; ++k) v += sums[(o * 4 + k) * kWave + lane];
-        const int row = o / 4 * 16 + 4 * q + o % 4;
+        const int row = o / 4 * 16 + 4 * q + o % 4, in_chunk = listed(list, row);
         if (row >= count || r >= p.rank) continue;
-        const int64_t to = (chunk * 64 + list[row]) * p.rank + r;
+        const int64_t to = (chunk * 64 + in_chunk) * p.rank + r;
         if (p.splits > 1)
             st<f32x4>(p.partial + split * p.rows * p.rank + to, v);
         else
@@ -205,7 +195,6 @@ __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int
 template <bool GRAD, bool XF32, bool WF32>
 __global__ __launch_bounds__(kBlockThreads) void adapter_down_kernel(AdaptArgs p) {
     __shared__ f32x4 sums[4 * 4 * 4 * kWave];
-    __shared__ uint8_t lists[4][kWave];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     auto div = [](uint32_t &a, uint32_t b) {  // a mod b, and a becomes a / b
         const uint32_t d = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(a / b)), m = a - d * b;
@@ -230,8 +219,7 @@ __global__ __launch_bounds__(kBlockThreads) void adapter_down_kernel(AdaptArgs p
         const uint64_t match = __ballot(has && mine == g);
         pending &= ~match;
         if (n % static_cast<int>(p.slots) != slot) continue;
-        uint8_t *list = lists[w];
-        const int count = list_bits(match, list);
+        const int count = __popcll(match), list = list_bits(match);
         if (count <= 16)
             down_rows<GRAD, XF32, WF32, 1>(p, chunk, rank0, split, g, count, list, sums);
         else if (count <= 32)
@@ -363,7 +351,6 @@ template <bool F32, int PC>
 __global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall p) {
     constexpr int PX = F32 ? 3 : 1;
     __shared__ f32x4 sums[kRowWaves / 2][16][kWave];
-    __shared__ uint8_t lists[kRowWaves][kWave];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block(), q = lane >> 4, j = lane & 15;
     auto div = [](uint32_t &a, uint32_t b) {
         const uint32_t d = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(a / b)), m = a - d * b;
@@ -395,15 +382,14 @@ __global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall
         const int mine = p.ids ? p.ids[in ? row : 0] : 0;
         const uint64_t match = __ballot(in && mine == g);
         if (match == 0) continue;
-        uint8_t *list = lists[w];
-        const int count = list_bits(match, list);
+        const int count = __popcll(match), list = list_bits(match);
         for (int n = 0; n < count; n += 32) {
             f32x4 low[8];
             uint32_t x[8][F32 ? 4 : 2];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int at = n + 8 * q + i;
-                const int64_t m = c * 64 + list[min(at, count - 1)];
+                const int64_t m = c * 64 + listed(list, min(at, count - 1));
                 low[i] = ld<f32x4>(o.low + m * p.rank + min(r, p.rank - 4));
                 load4<F32>(o.x, m * o.x_stride + min(col, o.len), o.len - col, x[i]);
                 if (at >= count) {  // zeros on both sides: a row past the last is in no sum, whatever it holds

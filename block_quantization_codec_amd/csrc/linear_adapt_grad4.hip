@@ -3,7 +3,7 @@
 
 namespace zpp {
 
-hipError_t launch_linear_big_adapt_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream) {
+hipError_t launch_linear_adapt_grad4(const LinArgs &p, int parts, int mt, hipStream_t stream) {
     return launch_linear_big_as<LinMode::adapted, true, 4>(p, parts, mt, stream);
 }
 

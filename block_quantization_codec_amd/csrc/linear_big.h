@@ -463,70 +463,57 @@ struct LinBig {
         if constexpr (M + 1 < MT) rows_from<HN, M + 1>(here, then, b, raw, s, bn, a, scale, acc, before);
     }
 
-    // Rows of tiles whose adapters' sums LDS holds at once, 64 bytes a lane each.
-    static constexpr int kHeld = kBufs * kBytes / (kBlockThreads * 64);
-    static constexpr int kApart = kHeld >= MT ? MT : kHeld >= 8 ? 8 : kHeld >= 4 ? 4 : kHeld >= 2 ? 2 : 1;
+    // Rows of tiles that adapters are added to at once: 64 rows, or all of a smaller tile's.
+    static constexpr int kTogether = MT > 4 ? 4 : MT;
 
-    // Whether all rows of the tile have the same adapter (`one`; -1: none has any).
-    static __device__ __forceinline__ bool tile_adapter(const LinArgs &p, int64_t m0, int &one) {
+    // Whether the kTogether rows of tiles from row `first` on have all the same adapter
+    // (`one`; -1: none has any).
+    static __device__ __forceinline__ bool one_adapter(const LinArgs &p, int64_t first, int &one) {
         const int lane = threadIdx.x & (kWave - 1);
-        one = -1;
-        bool same = true;
-#pragma unroll
-        for (int r = 0; r < kRows; r += kWave) {
-            const int64_t row = min(m0 + min(r + lane, kRows - 1), p.rows - 1);
-            int id;
-            if (!adapter_of(p, row, id)) id = -1;
-            const int first = __builtin_amdgcn_readfirstlane(id);
-            if (r == 0) one = first;
-            same = same && __ballot(id != one) == 0;
-        }
-        return same;
+        int id;
+        if (!adapter_of(p, min(first + min(lane, kTogether * 16 - 1), p.rows - 1), id)) id = -1;
+        one = __builtin_amdgcn_readfirstlane(id);
+        return __ballot(id != one) == 0;
     }
 
-    // acc += low up of adapter g, over the codes' factor. Low comes by buffer loads, whose
-    // range check gives zeros for rows past the end: addresses of 16 rows of tiles,
-    // kept over the loop, would not fit beside the sums.
-    template <int PC, int PU>
-    static __device__ __forceinline__ void add_adapter(const LinArgs &p, int64_t m0, int64_t col, int g,
-                                                       f32x4 (&acc)[MT][4]) {
+    // d += low up of adapter g, for kTogether rows of tiles from row `first` on. S steps of 32
+    // ranks at a time: all their loads are under way together. Low comes by buffer
+    // loads, whose range check gives zeros for rows past the end.
+    template <int PC, int PU, int S>
+    static __device__ __forceinline__ void add_adapter(const LinArgs &p, int64_t first, int64_t col, int g,
+                                                       f32x4 (&d)[kTogether][4]) {
 #if defined(__HIP_DEVICE_COMPILE__)
         const int lane = threadIdx.x & (kWave - 1), q = lane >> 4, j = lane & 15;
-        const int left = static_cast<int>(min(p.rows - m0, static_cast<int64_t>(kRows)));
+        const int left = static_cast<int>(min(p.rows - first, static_cast<int64_t>(kTogether * 16)));
         const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<float *>(p.low + m0 * p.rank), 0, static_cast<uint32_t>(left * p.rank * 4), 0x27000);
-        const int mine = j * p.rank * 4;
+            const_cast<float *>(p.low + first * p.rank), 0, static_cast<uint32_t>(left * p.rank * 4), 0x27000);
 #pragma unroll 1
-        for (int r0 = 0; r0 < p.rank; r0 += 32) {
-            const int r = r0 + 8 * q;
-            // past the rank: an offset out of range
-            const int at = r < p.rank ? mine + r * 4 : 1 << 30;
-            u32x4 b[4][PU];
-            load_up<GRAD, true, PU, 4>(p, g, col, r, b);
+        for (int r0 = 0; r0 < p.rank; r0 += 32 * S) {
+            u32x4 b[S][4][PU], low[S][kTogether][2];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int o = at + m * 16 * p.rank * 4;
-                const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(from, o, 0, 0),
-                            hi = __builtin_amdgcn_raw_buffer_load_b128(from, o, 16, 0);
-                float v[8];
+            for (int s = 0; s < S; ++s) {
+                const int r = r0 + 32 * s + 8 * q;
+                // past the rank: an offset out of range
+                const int at = r < p.rank ? (j * p.rank + r) * 4 : 1 << 30;
+                load_up<GRAD, true, PU, 4>(p, g, col, r, b[s]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] = as_f(lo[i]) * (1.0f / kCodeScale<BITS>);
-                    v[4 + i] = as_f(hi[i]) * (1.0f / kCodeScale<BITS>);
-                }
-                u32x4 a[PC];
-                operand_of<PC>(v, a);
-                operands_ready<kPin>();
+                for (int m = 0; m < kTogether; ++m)
 #pragma unroll
-                for (int x = PC - 1; x >= 0; --x)
-#pragma unroll
-                    for (int y = PU - 1; y >= 0; --y)
-                        if (x + y <= 2) {
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) mfma<kPin>(a[x], b[t][y], acc[m][t]);
-                        }
-                sums_ready<kPin>();
+                    for (int h = 0; h < 2; ++h)
+                        low[s][m][h] = __builtin_amdgcn_raw_buffer_load_b128(from, at + m * 16 * p.rank * 4, 16 * h, 0);
             }
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int m = 0; m < kTogether; ++m) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = as_f(low[s][m][i / 4][i % 4]);
+                    u32x4 a[PC];
+                    operand_of<PC>(v, a);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) d[m][t] = mfma_parts<PC, PU>(a, b[s][t], d[m][t]);
+                }
         }
 #endif
     }
@@ -642,67 +629,83 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
         sums_ready<L::kPin>();
     }
 
-    // Adapters, with the first part of the contraction: into the sums where the tile's rows
-    // all have the same one, else apart, in rows of tiles that the free LDS holds.
-    // (256 sums a lane leave room for one way into them: binary32 adapters beside bf16
-    // activations and results, three parts each, take the other.)
-    [[maybe_unused]] bool apart = false;
     if constexpr (MODE == LinMode::adapted) {
-        if (place.split == 0) {
-            int one;
-            apart = !L::tile_adapter(p, m0, one);
-            if constexpr (PA * PB == 1) {
-                apart = apart || (one >= 0 && p.up_f32);
-                if (!apart && one >= 0) L::template add_adapter<2, 1>(p, m0, col, one, acc);
-            } else {
-                if (!apart && one >= 0) {
-                    if (p.up_f32)
-                        L::template add_adapter<3, 3>(p, m0, col, one, acc);
-                    else
-                        L::template add_adapter<3, 1>(p, m0, col, one, acc);
-                }
+        // Some rows at a time, in a loop, through LDS: written out for each of the 256 sums, the stores
+        // and what the adapters add would be 100 KB of instructions. The next rows' sums move up.
+        // Adapters are added with the first part of the contraction.
+        constexpr int kTogether = L::kTogether, PC = PA * PB == 1 ? 2 : 3;
+        static_assert(L::kBufs * L::kBytes >= 4 * kTogether * 16 * 64 * 4 && MT % kTogether == 0);
+        float *const held = reinterpret_cast<float *>(&tiles[0][0] + w * (kTogether * 16 * 64 * 4));
+        __syncthreads();  // no wave reads activations any more
+        // Rows of tiles M0 .. M0 + kTogether - 1 of the sums, which are rows from `first` on.
+        auto finish = [&](auto at, int64_t first) {
+            constexpr int M0 = at.value;
+            bool apart = false;
+            f32x4 d[kTogether][4];
+#pragma unroll
+            for (int m = 0; m < kTogether; ++m)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
+            if (place.split == 0) {
+                int one;
+                apart = !L::one_adapter(p, first, one) || (one >= 0 && p.up_f32);
+                if (apart)
+                    adapter_rows<GRAD, true, PC, 4, kTogether * 16, 2>(p, first, col, 0, 1, held);
+                else if (one >= 0)
+                    L::template add_adapter<PC, 1, 1>(p, first, col, one, d);
             }
-            if (apart) __syncthreads();  // no wave reads activations any more
+#pragma unroll
+            for (int m = 0; m < kTogether; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x4 v = f32x4{acc[M0 + m][0][i], acc[M0 + m][1][i], acc[M0 + m][2][i], acc[M0 + m][3][i]};
+                    v = v * kCodeScale<BITS> + f32x4{d[m][0][i], d[m][1][i], d[m][2][i], d[m][3][i]};
+                    f32x4 *to = reinterpret_cast<f32x4 *>(held + (m * 16 + 4 * q + i) * 64 + 4 * (lane & 15));
+                    if (apart) v += *to;
+                    *to = v;
+                }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+            for (int r = 0; r < kTogether * 16; r += 4) {
+                const int64_t row = first + r + q;
+                const f32x4 s = *reinterpret_cast<const f32x4 *>(held + (r + q) * 64 + 4 * (lane & 15));
+                const float v[4] = {s[0], s[1], s[2], s[3]};
+                if (row < p.rows) store4(p, len, row, col, v, place.split);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        if constexpr (MT == 16) {
+#pragma unroll 1
+            for (int m1 = 0; m1 < MT; m1 += kTogether) {
+                if (m0 + m1 * 16 >= p.rows) break;
+                finish(std::integral_constant<int, 0>{}, m0 + m1 * 16);
+#pragma unroll
+                for (int m = 0; m + kTogether < MT; ++m)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) acc[m][t] = acc[m + kTogether][t];
+            }
+        } else {  // fewer sums, and no registers to move them through
+            finish(std::integral_constant<int, 0>{}, m0);
+            if constexpr (MT > kTogether) {
+                if (m0 + kTogether * 16 < p.rows) finish(std::integral_constant<int, kTogether>{}, m0 + kTogether * 16);
+            }
+            static_assert(MT <= 2 * kTogether);
         }
+        return;
     }
 
-    constexpr int kTogether = MODE == LinMode::adapted ? L::kApart : MT;
-    f32x4 *const mine = reinterpret_cast<f32x4 *>(&tiles[0][0]) + threadIdx.x;
 #pragma unroll
-    for (int m1 = 0; m1 < MT; m1 += kTogether) {
-        if constexpr (MODE == LinMode::adapted) {
-            if (apart) {
-#pragma unroll 1
-                for (int m = 0; m < kTogether; ++m) {
-                    if (m0 + (m1 + m) * 16 >= p.rows) break;
-                    f32x4 d[4];
-                    adapter_rows<GRAD, true, PA * PB == 1 ? 2 : 3, 4>(p, m0 + (m1 + m) * 16, col, d);
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) mine[(m * 4 + t) * kBlockThreads] = d[t];
-                }
-            }
-        }
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = m0 + m * 16 + 4 * q + i;
+            if (row >= p.rows) continue;
+            float v[4];
 #pragma unroll
-        for (int m = m1; m < m1 + kTogether; ++m) {
-            [[maybe_unused]] f32x4 d[4];
-            if constexpr (MODE == LinMode::adapted) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    d[t] = apart ? mine[((m - m1) * 4 + t) * kBlockThreads] : f32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t row = m0 + m * 16 + 4 * q + i;
-                if (row >= p.rows) continue;
-                float v[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) v[t] = acc[m][t][i] * kCodeScale<BITS>;
-                if constexpr (MODE == LinMode::adapted) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) v[t] = apart ? v[t] + d[t][i] : v[t];
-                }
-                store4(p, len, row, col, v, place.split);
-            }
+            for (int t = 0; t < 4; ++t) v[t] = acc[m][t][i] * kCodeScale<BITS>;
+            store4(p, len, row, col, v, place.split);
         }
     }
 }

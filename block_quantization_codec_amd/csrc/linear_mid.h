@@ -115,17 +115,20 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
         else
             static_cast<uint16_t *>(p.out)[row * p.ldo + col] = static_cast<uint16_t>(pack_rn(v, 0.0f));
     };
-    [[maybe_unused]] f32x4 more[MODE == LinMode::adapted ? MT : 1][NT];
+    // Adapters: each part of the contraction takes its share of them.
+    [[maybe_unused]] float *given = nullptr;
     if constexpr (MODE == LinMode::adapted) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) more[m][t] = f32x4{0, 0, 0, 0};
-            // once: with the first part of the contraction
-            if (split == 0 && m0 + m * 16 < p.rows)
-                adapter_rows<false, false, 3, NT>(p, m0 + m * 16, n0 + (lane & 15), more[m]);
-        }
+        static_assert(NT == 2 && sizeof(tiles) >= 4 * T::kRows * NT * 16 * 4);
+        __syncthreads();  // no wave reads activations any more
+        given = reinterpret_cast<float *>(&tiles[0][0][0] + w * (T::kRows * NT * 16 * 4));
+        adapter_rows<false, false, 3, NT, T::kRows, 4>(p, m0, n0 + (lane & 15), static_cast<int>(split), p.splits, given);
     }
+    auto more = [&](int m, int t, int i) {
+        if constexpr (MODE == LinMode::adapted)
+            return given[(m * 16 + 4 * q + i) * (16 * NT) + 16 * t + (lane & 15)];
+        else
+            return 0.0f;
+    };
     uint32_t again = 0;  // of the lane's results, those out of range: stored once more at the end
     static_assert(NT * MT * 4 <= 32, "a bit each");
 #pragma unroll
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
                 const float v = acc[t][m][i] * kCodeScale<BITS>;
                 again |= out_of_range(v) ? 1u << ((t * MT + m) * 4 + i) : 0u;
                 if constexpr (MODE == LinMode::adapted)
-                    store(row, col, v + more[m][t][i]);
+                    store(row, col, v + more(m, t, i));
                 else
                     store(row, col, v);
             }
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
         const int b = __builtin_ctz(again), t = b / (4 * MT), m = b / 4 % MT;
         const int64_t row = m0 + m * 16 + 4 * q + b % 4, col = n0 + t * 16 + (lane & 15);
         float v = scaled_sum<BITS, PA>(p, row, col, k0, k1);
-        if constexpr (MODE == LinMode::adapted) v += split == 0 ? adapter_dot(p, row, col) : 0.0f;
+        if constexpr (MODE == LinMode::adapted) v += more(m, t, b % 4);
         store(row, col, v);
     }
 }
