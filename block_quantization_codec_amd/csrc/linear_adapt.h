@@ -55,18 +55,19 @@ __device__ __forceinline__ bool adapter_of(const LinArgs &p, int64_t row, int &i
     return row < p.rows && static_cast<uint32_t>(id) < static_cast<uint32_t>(p.adapters);
 }
 
-// The lane's part of `low` for indices r .. r + 7 of a row: zeros past the rank.
-template <int P>
-__device__ __forceinline__ void load_low(const LinArgs &p, int64_t row, int r, u32x4 (&a)[P]) {
-    float v[8];
+// Indices r .. r + 7 of a row of low: any of the row's past the rank.
+__device__ __forceinline__ void load_low(const LinArgs &p, int64_t row, int r, f32x4 (&v)[2]) {
     const float *from = p.low + min(row, p.rows - 1) * p.rank + min(r, p.rank - 8);
-    const f32x4 x = ld<f32x4>(from), y = ld<f32x4>(from + 4);
+    v[0] = ld<f32x4>(from), v[1] = ld<f32x4>(from + 4);
+}
+
+// As operand parts: zeros unless `in`.
+template <int P>
+__device__ __forceinline__ void low_operand(const f32x4 (&v)[2], bool in, u32x4 (&a)[P]) {
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = r < p.rank ? x[i] : 0.0f;
-        v[4 + i] = r < p.rank ? y[i] : 0.0f;
-    }
-    operand_of<P>(v, a);
+    for (int i = 0; i < 8; ++i) f[i] = in ? v[i / 4][i % 4] : 0.0f;
+    operand_of<P>(f, a);
 }
 
 // The adapter's operands for NT tiles of columns, indices r .. r + 7: zeros past
@@ -142,9 +143,9 @@ __device__ __forceinline__ int listed(int list, int n) { return __builtin_amdgcn
 //
 // The rows of an adapter, wherever they stand, are the matrix instruction's rows. NB
 // adapters at a time: their operands' loads, each a trip to memory where every row
-// has an adapter of its own, are under way together. One by one, 48 rows of 28672 x
+// has an adapter of its own, are under way together, S steps of 32 ranks of each. One by one, 48 rows of 28672 x
 // 8192 with 32 adapters of rank 64 took 75 us more than without adapters.
-template <bool GRAD, bool NEAR, int PC, int PB, int NT, int ROWS, int NB>
+template <bool GRAD, bool NEAR, int PC, int PB, int NT, int ROWS, int NB, int S>
 __device__ __forceinline__ void adapter_gather(const LinArgs &p, int64_t row0, int64_t col, int part, int parts,
                                                float *held) {
     static_assert(ROWS <= kWave && ROWS % 16 == 0);
@@ -183,17 +184,25 @@ __device__ __forceinline__ void adapter_gather(const LinArgs &p, int64_t row0, i
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) e[b][t] = f32x4{0, 0, 0, 0};
-            for (int r0 = 0; r0 < p.rank; r0 += 32) {
-                u32x4 low[NB][PC], up[NB][NT][PB];
+            for (int r0 = 0; r0 < p.rank; r0 += 32 * S) {
+                f32x4 low[S][NB][2];
+                u32x4 up[S][NB][NT][PB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    load_up<GRAD, NEAR, PB, NT>(p, g[b], col, r0 + 8 * q, up[b]);
-                    load_low<PC>(p, row[b], r0 + 8 * q, low[b]);
-                }
+                for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                    for (int b = 0; b < NB; ++b) {
+                        load_up<GRAD, NEAR, PB, NT>(p, g[b], col, r0 + 32 * s + 8 * q, up[s][b]);
+                        load_low(p, row[b], r0 + 32 * s + 8 * q, low[s][b]);
+                    }
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) e[b][t] = mfma_parts<PC, PB>(low[b], up[b][t], e[b][t]);
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        u32x4 a[PC];
+                        low_operand<PC>(low[s][b], r0 + 32 * s + 8 * q < p.rank, a);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) e[b][t] = mfma_parts<PC, PB>(a, up[s][b][t], e[b][t]);
+                    }
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -216,13 +225,13 @@ __device__ __forceinline__ void adapter_gather(const LinArgs &p, int64_t row0, i
     __builtin_amdgcn_wave_barrier();
 }
 
-template <bool GRAD, bool NEAR, int PC, int NT, int ROWS, int NB>
+template <bool GRAD, bool NEAR, int PC, int NT, int ROWS, int NB, int S>
 __device__ __forceinline__ void adapter_rows(const LinArgs &p, int64_t row0, int64_t col, int part, int parts,
                                              float *held) {
     if (p.up_f32)  // three parts each: half as many at a time fit
-        adapter_gather<GRAD, NEAR, 3, 3, NT, ROWS, (NB + 1) / 2>(p, row0, col, part, parts, held);
+        adapter_gather<GRAD, NEAR, 3, 3, NT, ROWS, (NB + 1) / 2, 1>(p, row0, col, part, parts, held);
     else
-        adapter_gather<GRAD, NEAR, PC, 1, NT, ROWS, NB>(p, row0, col, part, parts, held);
+        adapter_gather<GRAD, NEAR, PC, 1, NT, ROWS, NB, S>(p, row0, col, part, parts, held);
 }
 
 // low[m][r .. r + 7] . B[g][n][r .. r + 7] of one result, by one lane; zero past the rank.

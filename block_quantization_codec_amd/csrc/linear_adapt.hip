@@ -48,100 +48,142 @@ __device__ __forceinline__ bool has_adapter(const AdaptArgs &p, int64_t row, int
 
 // ---- down -------------------------------------------------------------------------
 
-// 16 elements of a row from k on as operand parts of two matrix instructions:
-// zeros past the end. `whole`: all 16 are in the row.
-template <bool F32>
-__device__ __forceinline__ void load16(const void *base, int64_t e, int64_t left, u32x4 (&b)[2][F32 ? 3 : 1]) {
-    if constexpr (F32) {
-        float f[16];
-        const float *from = static_cast<const float *>(base) + e;
-        if (left >= 16) {
+// What a lane loads of a step of 64 contraction indices, of which it has k .. k + 15:
+// of the rows of MT tiles, and of four ranks (forward: their 16 elements each;
+// backward: four neighbouring ranks of 16 rows, to be turned).
+template <bool GRAD, bool XF32, bool WF32, int MT>
+struct Step {
+    static constexpr int kX = XF32 ? 4 : 2, kW = (WF32 ? 2 : 1) * 2;
+    u32x4 x[MT][kX];
+    u32x4 w[4][kW];
+
+    // 16 elements of a row from `base` on, of which the first `left` are in it.
+    template <bool F32, bool WHOLE>
+    static __device__ __forceinline__ void load16(const void *base, int64_t e, int64_t left, u32x4 *v) {
+        if constexpr (F32) {
+            const uint32_t *from = static_cast<const uint32_t *>(base) + e;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const u32x4 v = *reinterpret_cast<const u32x4_at4 *>(from + 4 * i);
+                if constexpr (WHOLE) {
+                    v[i] = *reinterpret_cast<const u32x4_at4 *>(from + 4 * i);
+                } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) f[4 * i + c] = as_f(v[c]);
+                    for (int c = 0; c < 4; ++c) v[i][c] = 4 * i + c < left ? from[4 * i + c] : 0u;
+                }
             }
         } else {
+            const uint16_t *from = static_cast<const uint16_t *>(base) + e;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = i < left ? from[i] : 0.0f;
-        }
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (WHOLE) {
+                    v[h] = *reinterpret_cast<const u32x4_any *>(from + 8 * h);
+                } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float v[8] = {f[8 * h], f[8 * h + 1], f[8 * h + 2], f[8 * h + 3],
-                                f[8 * h + 4], f[8 * h + 5], f[8 * h + 6], f[8 * h + 7]};
-            operand_of<3>(v, b[h]);
-        }
-    } else {
-        const uint16_t *from = static_cast<const uint16_t *>(base) + e;
-        if (left >= 16) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) b[h][0] = *reinterpret_cast<const u32x4_any *>(from + 8 * h);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const int i = 8 * h + 2 * d;
-                    b[h][0][d] = (i < left ? from[i] : 0u) | (i + 1 < left ? static_cast<uint32_t>(from[i + 1]) << 16 : 0u);
+                    for (int d = 0; d < 4; ++d) {
+                        const int i = 8 * h + 2 * d;
+                        v[h][d] = (i < left ? from[i] : 0u) | (i + 1 < left ? static_cast<uint32_t>(from[i + 1]) << 16 : 0u);
+                    }
                 }
+            }
         }
     }
-}
 
-// The adapter's operands of the step's two matrix instructions, four tiles of
-// ranks each: tile t's rank is r + t. The lane has contraction indices k .. k + 15.
-template <bool GRAD, bool F32>
-__device__ __forceinline__ void load_w(const AdaptArgs &p, int64_t g, int r, int64_t k, u32x4 (&b)[4][2][F32 ? 3 : 1]) {
-    constexpr int P = F32 ? 3 : 1;
-    if constexpr (!GRAD) {  // [rank][len]: the lane's indices lie side by side
+    // WHOLE: all 64 indices are below len.
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const AdaptArgs &p, const int64_t (&at)[MT], int64_t g, int r, int64_t k) {
+        const int64_t left = p.len - k;
+        if constexpr (!GRAD) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            load16<F32>(p.w, (g * p.rank + min(r + t, p.rank - 1)) * p.len + min(k, p.len), p.len - k, b[t]);
-    } else {  // [len][rank]: four neighbouring ranks of 16 rows, turned
-        const int64_t base = g * p.len * p.rank + min(r, p.rank - 4);
+            for (int t = 0; t < 4; ++t)
+                load16<WF32, WHOLE>(p.w, (g * p.rank + min(r + t, p.rank - 1)) * p.len + k, left, w[t]);
+        } else {
+            const int64_t base = g * p.len * p.rank + min(r, p.rank - 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (F32) {
-                f32x4 v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t n = k + 8 * h + i;
-                    v[i] = ld<f32x4>(static_cast<const float *>(p.w) + base + min(n, p.len - 1) * p.rank);
-                    if (n >= p.len) v[i] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < 16; ++i) {
+                const int64_t e = base + (WHOLE ? k + i : min(k + i, p.len - 1)) * p.rank;
+                const bool in = WHOLE || i < left;  // zeros past the end, whatever stands there
+                if constexpr (WF32) {
+                    const u32x4 v = ld<u32x4>(static_cast<const float *>(p.w) + e);
+                    w16(i) = in ? v : u32x4{0, 0, 0, 0};
+                } else {
+                    const u32x2 v = ld<u32x2>(static_cast<const uint16_t *>(p.w) + e);
+                    w[i / 4][i % 4 / 2][i % 2 * 2] = in ? v[0] : 0u;
+                    w[i / 4][i % 4 / 2][i % 2 * 2 + 1] = in ? v[1] : 0u;
                 }
+            }
+        }
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const float o[8] = {v[0][t], v[1][t], v[2][t], v[3][t], v[4][t], v[5][t], v[6][t], v[7][t]};
-                    operand_of<P>(o, b[t][h]);
-                }
-            } else {
-                u32x2 v[8];
+        for (int m = 0; m < MT; ++m) load16<XF32, WHOLE>(p.x, at[m] + k, left, x[m]);
+    }
+
+    __device__ __forceinline__ u32x4 &w16(int i) { return w[i / 4][i % 4]; }
+
+    // Half H of 16 elements as an operand's parts.
+    template <bool F32, int H>
+    static __device__ __forceinline__ void half(const u32x4 *v, u32x4 (&o)[F32 ? 3 : 1]) {
+        if constexpr (F32) {
+            float f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t n = k + 8 * h + i;
-                    v[i] = ld<u32x2>(static_cast<const uint16_t *>(p.w) + base + min(n, p.len - 1) * p.rank);
-                    if (n >= p.len) v[i] = u32x2{0, 0};
-                }
+            for (int i = 0; i < 8; ++i) f[i] = as_f(v[2 * H + i / 4][i % 4]);
+            operand_of<3>(f, o);
+        } else {
+            o[0] = v[H];
+        }
+    }
+
+    // Tile t of ranks, half H of the indices.
+    template <int H>
+    __device__ __forceinline__ void rank_tile(int t, u32x4 (&o)[WF32 ? 3 : 1]) const {
+        if constexpr (!GRAD) {
+            half<WF32, H>(w[t], o);
+        } else if constexpr (WF32) {
+            float f[8];
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+            for (int i = 0; i < 8; ++i) f[i] = as_f(w[(8 * H + i) / 4][i % 4][t]);
+            operand_of<3>(f, o);
+        } else {
 #pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        b[t][h][0][d] = __builtin_amdgcn_perm(v[2 * d + 1][t / 2], v[2 * d][t / 2],
-                                                              t % 2 == 0 ? 0x05040100u : 0x07060302u);
+            for (int d = 0; d < 4; ++d) {
+                // rows 8 H + 2 d and the next: elements t of two pairs of dwords
+                const int i = 8 * H + 2 * d;
+                const u32x4 &v = w[i / 4][i % 4 / 2];
+                o[0][d] = __builtin_amdgcn_perm(v[2 + t / 2], v[t / 2], t % 2 == 0 ? 0x05040100u : 0x07060302u);
             }
         }
     }
-}
+
+    template <int H>
+    __device__ __forceinline__ void use_half(f32x4 (&acc)[MT][4]) const {
+        constexpr int PX = XF32 ? 3 : 1, PW = WF32 ? 3 : 1;
+        u32x4 b[4][PW];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) rank_tile<H>(t, b[t]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            u32x4 a[PX];
+            half<XF32, H>(x[m], a);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[m][t] = mfma_parts<PX, PW>(a, b[t], acc[m][t]);
+        }
+    }
+
+    __device__ __forceinline__ void use(f32x4 (&acc)[MT][4]) const {
+        use_half<0>(acc);
+        use_half<1>(acc);
+    }
+};
 
 // One adapter's rows of a chunk (16 MT of them at most) by 64 of its ranks: the
-// workgroup's 4 waves take steps of 64 indices in turn and join their sums in LDS.
+// workgroup's 4 waves take steps of 64 indices in turn, the next one's loads under
+// way, and join their sums in LDS.
 template <bool GRAD, bool XF32, bool WF32, int MT>
 __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int64_t rank0, int split, int g, int count,
                                           int list, f32x4 *sums) {
-    constexpr int PX = XF32 ? 3 : 1, PW = WF32 ? 3 : 1;
+    using S = Step<GRAD, XF32, WF32, MT>;
+    constexpr bool AHEAD = !XF32 && !WF32;  // binary32 steps fill the registers
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block(), q = lane >> 4, j = lane & 15;
     const int r = static_cast<int>(rank0) + 4 * j;
+    const float scale = p.scaling && p.splits == 1 ? p.scaling[g] : 1.0f;
     int64_t at[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) at[m] = (chunk * 64 + listed(list, min(16 * m + j, count - 1))) * p.x_stride;
@@ -150,22 +192,27 @@ __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
-    const int64_t s0 = split * p.split_steps, s1 = min(s0 + p.split_steps, (p.len + 63) / 64);
-#pragma unroll 2
-    for (int64_t s = s0 + w; s < s1; s += 4) {
-        const int64_t k = s * 64 + 16 * q;
-        u32x4 b[4][2][PW];
-        load_w<GRAD, WF32>(p, g, r, k, b);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            u32x4 a[2][PX];
-            load16<XF32>(p.x, at[m] + min(k, p.len), p.len - k, a);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                acc[m][t] = mfma_parts<PX, PW>(a[0], b[t][0], acc[m][t]);
-                acc[m][t] = mfma_parts<PX, PW>(a[1], b[t][1], acc[m][t]);
-            }
+    const int64_t s0 = split * p.split_steps + w, s1 = min((split + 1) * p.split_steps, p.len / 64);
+    if constexpr (AHEAD) {
+        S now, next;
+        if (s0 < s1) now.template load<true>(p, at, g, r, s0 * 64 + 16 * q);
+        for (int64_t s = s0; s < s1; s += 4) {
+            if (s + 4 < s1) next.template load<true>(p, at, g, r, (s + 4) * 64 + 16 * q);
+            now.use(acc);
+            now = next;
         }
+    } else {
+        for (int64_t s = s0; s < s1; s += 4) {
+            S now;
+            now.template load<true>(p, at, g, r, s * 64 + 16 * q);
+            now.use(acc);
+        }
+    }
+    // what is left, less than 64 indices, is the last part's, and the wave's whose turn it is
+    if (const int64_t s = p.len / 64; p.len % 64 != 0 && s / p.split_steps == split && s % 4 == w) {
+        S last;
+        last.template load<false>(p, at, g, r, s * 64 + 16 * q);
+        last.use(acc);
     }
     // Lane (q, j) has rows 4 q + i and ranks 4 j + t: turned into one piece of four ranks a row.
 #pragma unroll
@@ -174,7 +221,6 @@ __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int
         for (int i = 0; i < 4; ++i)
             sums[((m * 4 + i) * 4 + w) * kWave + lane] = f32x4{acc[m][0][i], acc[m][1][i], acc[m][2][i], acc[m][3][i]};
     __syncthreads();
-    const float scale = p.scaling ? p.scaling[g] : 1.0f;
     for (int o = w; o < MT * 4; o += 4) {
         f32x4 v = {0, 0, 0, 0};
 #pragma unroll
@@ -193,7 +239,7 @@ __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int
 // Grid: chunks of 64 rows x slots x runs of 64 ranks x parts of the contraction. Of a
 // chunk's adapters, in the order of their first rows, slot s takes each slots-th.
 template <bool GRAD, bool XF32, bool WF32>
-__global__ __launch_bounds__(kBlockThreads) void adapter_down_kernel(AdaptArgs p) {
+__global__ __launch_bounds__(kBlockThreads, XF32 || WF32 ? 1 : 2) void adapter_down_kernel(AdaptArgs p) {
     __shared__ f32x4 sums[4 * 4 * 4 * kWave];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     auto div = [](uint32_t &a, uint32_t b) {  // a mod b, and a becomes a / b
@@ -242,8 +288,8 @@ __global__ __launch_bounds__(kBlockThreads) void adapter_join_kernel(AdaptArgs p
     }
 }
 
-// How a call's low is shared out: about 768 workgroups of 4 waves, with 4 steps of 64
-// or more each; in few rows a chunk's adapters have workgroups of their own.
+// How a call's low is shared out: up to 512 workgroups of 4 waves (two a CU), with 4 steps
+// of 64 or more each; in few rows a chunk's adapters have workgroups of their own.
 struct DownPlan {
     int64_t rows;  // of one launch
     int64_t slots, ranks, splits, split_steps;
@@ -255,7 +301,7 @@ DownPlan down_plan(int64_t rows, int64_t len, int64_t adapters, int64_t rank) {
     const int64_t chunks = ceil_div(d.rows, 64), steps = ceil_div(len, 64);
     d.ranks = ceil_div(rank, 64);
     d.slots = std::max<int64_t>(std::min({adapters, d.rows, 64 / chunks}), 1);
-    const int64_t most = std::max<int64_t>(768 / (chunks * d.ranks * d.slots), 1);
+    const int64_t most = std::max<int64_t>(512 / (chunks * d.ranks * d.slots), 1);
     d.split_steps = std::max<int64_t>(ceil_div(ceil_div(steps, most), 4) * 4, 4);
     d.splits = ceil_div(steps, d.split_steps);
     return d;
@@ -343,13 +389,120 @@ __device__ __forceinline__ void load4(const void *base, int64_t e, int64_t left,
     }
 }
 
+// What a lane loads of 32 of an adapter's rows: of the 8 that are its quarter's,
+// four neighbouring ranks of low and four neighbouring columns of x.
+template <bool F32, int PC>
+struct RowStep {
+    static constexpr int PX = F32 ? 3 : 1, kX = F32 ? 4 : 2;
+    f32x4 low[8];
+    uint32_t x[8][kX];
+
+    // Rows n .. n + 31 of `count`; zeros past the last, on both sides, since such a row is in
+    // no sum, whatever it holds. WHOLE: the columns are all in the row.
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const RowsArgs &o, int rank, int64_t row0, int list, int n, int count, int r,
+                                         int64_t col) {
+        const int q = (threadIdx.x & (kWave - 1)) >> 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = n + 8 * q + i;
+            const int64_t m = row0 + listed(list, min(at, count - 1));
+            low[i] = ld<f32x4>(o.low + m * rank + min(r, rank - 4));
+            if constexpr (WHOLE) {
+                if constexpr (F32) {
+                    const u32x4 v = *reinterpret_cast<const u32x4_at4 *>(static_cast<const float *>(o.x) + m * o.x_stride + col);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][e] = v[e];
+                } else {
+                    const u32x2 v = *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(o.x) + m * o.x_stride + col);
+                    x[i][0] = v[0], x[i][1] = v[1];
+                }
+            } else {
+                load4<F32>(o.x, m * o.x_stride + min(col, o.len), o.len - col, x[i]);
+            }
+            if (at >= count) {
+                low[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < kX; ++e) x[i][e] = 0;
+            }
+        }
+    }
+
+    // Turned: tile t has the lane's rank or column t.
+    __device__ __forceinline__ void use(f32x4 (&acc)[4][4]) const {
+        u32x4 b[4][PX];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (F32) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = as_f(x[i][t]);
+                operand_of<PX>(f, b[t]);
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    b[t][0][d] = __builtin_amdgcn_perm(x[2 * d + 1][t / 2], x[2 * d][t / 2],
+                                                       t % 2 == 0 ? 0x05040100u : 0x07060302u);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            float f[8];
+            u32x4 a[PC];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = low[i][s];
+            operand_of<PC>(f, a);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[s][t] = mfma_parts<PC, PX>(a, b[t], acc[s][t]);
+        }
+    }
+};
+
+// The sums of one wave: chunks c0 + w, c0 + w + 8, ... The next 32 rows' loads are under
+// way while these are multiplied, and the ids of the next chunk.
+template <bool F32, int PC, bool WHOLE>
+__device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &o, int g, int64_t c0, int64_t c1, int r,
+                                             int64_t col, f32x4 (&acc)[4][4]) {
+    using S = RowStep<F32, PC>;
+    const int lane = threadIdx.x & (kWave - 1);
+    auto id_of = [&](int64_t c) {
+        const int64_t row = c * 64 + lane;
+        if (row >= p.rows) return -1;
+        return p.ids ? p.ids[row] : 0;
+    };
+    int64_t c = c0 + wave_in_block();
+    int ids = c < c1 ? id_of(c) : -1, list = 0, count = 0, n = 0;
+    int64_t row0 = 0;
+    // The next 32 rows of the adapter: false if there are none.
+    auto advance = [&] {
+        n += 32;
+        while (n >= count) {
+            if (c >= c1) return false;
+            const uint64_t match = __ballot(ids == g);
+            row0 = c * 64;
+            c += kRowWaves;
+            ids = c < c1 ? id_of(c) : -1;
+            n = 0;
+            count = __popcll(match);
+            if (count > 0) list = list_bits(match);
+        }
+        return true;
+    };
+    S now, next;
+    bool more = advance();
+    if (more) now.template load<WHOLE>(o, p.rank, row0, list, n, count, r, col);
+    while (more) {
+        more = advance();
+        if (more) next.template load<WHOLE>(o, p.rank, row0, list, n, count, r, col);
+        now.use(acc);
+        now = next;
+    }
+}
+
 // One adapter's sums over its rows, 64 ranks x 64 columns a workgroup: the waves
-// take chunks of 64 rows in turn. A lane loads, of the 8 rows that are its quarter's
-// share of 32, four neighbouring ranks of low and four neighbouring columns of x,
-// and turns them: tile t has the lane's rank or column t. The waves' sums meet in LDS.
+// take chunks of 64 rows in turn, and their sums meet in LDS.
 template <bool F32, int PC>
 __global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall p) {
-    constexpr int PX = F32 ? 3 : 1;
     __shared__ f32x4 sums[kRowWaves / 2][16][kWave];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block(), q = lane >> 4, j = lane & 15;
     auto div = [](uint32_t &a, uint32_t b) {
@@ -376,50 +529,10 @@ __global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall
         for (int t = 0; t < 4; ++t) acc[a][t] = f32x4{0, 0, 0, 0};
 
     const int64_t c0 = split * p.split_chunks, c1 = min(c0 + p.split_chunks, (p.rows + 63) / 64);
-    for (int64_t c = c0 + w; c < c1; c += kRowWaves) {
-        const int64_t row = c * 64 + lane;
-        const bool in = row < p.rows;
-        const int mine = p.ids ? p.ids[in ? row : 0] : 0;
-        const uint64_t match = __ballot(in && mine == g);
-        if (match == 0) continue;
-        const int count = __popcll(match), list = list_bits(match);
-        for (int n = 0; n < count; n += 32) {
-            f32x4 low[8];
-            uint32_t x[8][F32 ? 4 : 2];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int at = n + 8 * q + i;
-                const int64_t m = c * 64 + listed(list, min(at, count - 1));
-                low[i] = ld<f32x4>(o.low + m * p.rank + min(r, p.rank - 4));
-                load4<F32>(o.x, m * o.x_stride + min(col, o.len), o.len - col, x[i]);
-                if (at >= count) {  // zeros on both sides: a row past the last is in no sum, whatever it holds
-                    low[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int e = 0; e < (F32 ? 4 : 2); ++e) x[i][e] = 0;
-                }
-            }
-            u32x4 a[4][PC], b[4][PX];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float v[8] = {low[0][t], low[1][t], low[2][t], low[3][t], low[4][t], low[5][t], low[6][t], low[7][t]};
-                operand_of<PC>(v, a[t]);
-                if constexpr (F32) {
-                    const float u[8] = {as_f(x[0][t]), as_f(x[1][t]), as_f(x[2][t]), as_f(x[3][t]),
-                                        as_f(x[4][t]), as_f(x[5][t]), as_f(x[6][t]), as_f(x[7][t])};
-                    operand_of<PX>(u, b[t]);
-                } else {
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        b[t][0][d] = __builtin_amdgcn_perm(x[2 * d + 1][t / 2], x[2 * d][t / 2],
-                                                           t % 2 == 0 ? 0x05040100u : 0x07060302u);
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) acc[s][t] = mfma_parts<PC, PX>(a[s], b[t], acc[s][t]);
-        }
-    }
+    if (tile * 64 + 64 <= o.len)
+        adapter_sums<F32, PC, true>(p, o, g, c0, c1, r, col, acc);
+    else
+        adapter_sums<F32, PC, false>(p, o, g, c0, c1, r, col, acc);
 
     // The upper half of the waves hand their sums to the lower half, until wave 0 has them all.
 #pragma unroll

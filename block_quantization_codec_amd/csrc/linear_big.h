@@ -650,7 +650,7 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
                 int one;
                 apart = !L::one_adapter(p, first, one) || (one >= 0 && p.up_f32);
                 if (apart)
-                    adapter_rows<GRAD, true, PC, 4, kTogether * 16, 2>(p, first, col, 0, 1, held);
+                    adapter_rows<GRAD, true, PC, 4, kTogether * 16, 2, 1>(p, first, col, 0, 1, held);
                 else if (one >= 0)
                     L::template add_adapter<PC, 1, 1>(p, first, col, one, d);
             }

@@ -24,7 +24,7 @@
 namespace zpp {
 
 template <int BITS, int PA, int NT, int MT, int U, bool WIDE, LinMode MODE>
-__global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
+__global__ __launch_bounds__(kBlockThreads, MODE == LinMode::adapted ? 2 : 1) void linear_mid_kernel(LinArgs p) {
     constexpr bool ASYNC = PA == 1;
     using C = CodeStream<BITS, NT, U, WIDE>;
     using T = LinTile<PA, MT>;
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kBlockThreads) void linear_mid_kernel(LinArgs p) {
         static_assert(NT == 2 && sizeof(tiles) >= 4 * T::kRows * NT * 16 * 4);
         __syncthreads();  // no wave reads activations any more
         given = reinterpret_cast<float *>(&tiles[0][0][0] + w * (T::kRows * NT * 16 * 4));
-        adapter_rows<false, false, 3, NT, T::kRows, 4>(p, m0, n0 + (lane & 15), static_cast<int>(split), p.splits, given);
+        adapter_rows<false, false, 3, NT, T::kRows, 4, 2>(p, m0, n0 + (lane & 15), static_cast<int>(split), p.splits, given);
     }
     auto more = [&](int m, int t, int i) {
         if constexpr (MODE == LinMode::adapted)
