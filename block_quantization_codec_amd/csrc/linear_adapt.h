@@ -25,13 +25,12 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
 // Two values as P bf16 pairs; of two parts, the first is cut off (which cannot
-// overflow) and the second rounded.
+// overflow) and the second rounded (NaN beside an infinite first).
 template <int P>
 __device__ __forceinline__ void low_parts(float a, float b, uint32_t (&w)[P]) {
     if constexpr (P == 2) {
-        const float ha = as_f(as_u(a) & 0xFFFF0000u), hb = as_f(as_u(b) & 0xFFFF0000u);
         w[0] = pack_hi(a, b);
-        w[1] = pack_rn(ha == a ? 0.0f : a - ha, hb == b ? 0.0f : b - hb);
+        w[1] = pack_rn(a - as_f(w[0] << 16), b - as_f(w[0] & 0xFFFF0000u));
     } else {
         to_parts<P>(a, b, w);
     }

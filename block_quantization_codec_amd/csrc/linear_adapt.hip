@@ -58,8 +58,8 @@ struct Step {
     u32x4 w[4][kW];
 
     // 16 elements of a row from `base` on, of which the first `left` are in it.
-    template <bool F32, bool WHOLE>
-    static __device__ __forceinline__ void load16(const void *base, int64_t e, int64_t left, u32x4 *v) {
+    template <bool F32, bool WHOLE, class Off>
+    static __device__ __forceinline__ void load16(const void *base, Off e, int64_t left, u32x4 *v) {
         if constexpr (F32) {
             const uint32_t *from = static_cast<const uint32_t *>(base) + e;
 #pragma unroll
@@ -88,32 +88,42 @@ struct Step {
         }
     }
 
-    // WHOLE: all 64 indices are below len.
-    template <bool WHOLE>
-    __device__ __forceinline__ void load(const AdaptArgs &p, const int64_t (&at)[MT], int64_t g, int r, int64_t k) {
-        const int64_t left = p.len - k;
+    // Step s of 64 indices; WHOLE: all of them are below len. x and w are those of the
+    // chunk's first row and of the adapter; a lane adds its offsets (Off: 32 bits where
+    // they suffice) to what is the same in all lanes.
+    template <bool WHOLE, class Off>
+    __device__ __forceinline__ void load(const AdaptArgs &p, const uint8_t *rows, const uint8_t *adapter,
+                                         const Off (&at)[MT], int r, int64_t s) {
+        const int k = 16 * static_cast<int>(threadIdx.x >> 4 & 3);  // the lane's first index of the step's
+        const int64_t left = p.len - s * 64 - k;
         if constexpr (!GRAD) {
+            const uint8_t *from = adapter + s * 64 * (WF32 ? 4 : 2);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                load16<WF32, WHOLE>(p.w, (g * p.rank + min(r + t, p.rank - 1)) * p.len + k, left, w[t]);
+                load16<WF32, WHOLE>(from, static_cast<Off>(min(r + t, p.rank - 1)) * static_cast<Off>(p.len) + k, left, w[t]);
         } else {
-            const int64_t base = g * p.len * p.rank + min(r, p.rank - 4);
+            const uint8_t *from = adapter + s * 64 * p.rank * (WF32 ? 4 : 2);
+            const uint32_t rr = static_cast<uint32_t>(min(r, p.rank - 4)), rank = static_cast<uint32_t>(p.rank);
+            const uint32_t first = k * rank + rr;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int64_t e = base + (WHOLE ? k + i : min(k + i, p.len - 1)) * p.rank;
                 const bool in = WHOLE || i < left;  // zeros past the end, whatever stands there
+                // the last one again past the end (of len, so not before this step's first)
+                const int64_t last = p.len - 1 - s * 64;
+                const uint32_t e = WHOLE ? first : static_cast<uint32_t>(min(static_cast<int64_t>(k + i), last)) * rank + rr;
+                const uint8_t *row = from + (WHOLE ? i * rank * (WF32 ? 4u : 2u) : 0u);
                 if constexpr (WF32) {
-                    const u32x4 v = ld<u32x4>(static_cast<const float *>(p.w) + e);
+                    const u32x4 v = ld<u32x4>(reinterpret_cast<const float *>(row) + e);
                     w16(i) = in ? v : u32x4{0, 0, 0, 0};
                 } else {
-                    const u32x2 v = ld<u32x2>(static_cast<const uint16_t *>(p.w) + e);
+                    const u32x2 v = ld<u32x2>(reinterpret_cast<const uint16_t *>(row) + e);
                     w[i / 4][i % 4 / 2][i % 2 * 2] = in ? v[0] : 0u;
                     w[i / 4][i % 4 / 2][i % 2 * 2 + 1] = in ? v[1] : 0u;
                 }
             }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m) load16<XF32, WHOLE>(p.x, at[m] + k, left, x[m]);
+        for (int m = 0; m < MT; ++m) load16<XF32, WHOLE>(rows + s * 64 * (XF32 ? 4 : 2), at[m] + k, left, x[m]);
     }
 
     __device__ __forceinline__ u32x4 &w16(int i) { return w[i / 4][i % 4]; }
@@ -176,7 +186,7 @@ struct Step {
 // One adapter's rows of a chunk (16 MT of them at most) by 64 of its ranks: the
 // workgroup's 4 waves take steps of 64 indices in turn, the next one's loads under
 // way, and join their sums in LDS.
-template <bool GRAD, bool XF32, bool WF32, int MT>
+template <bool GRAD, bool XF32, bool WF32, int MT, class Off>
 __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int64_t rank0, int split, int g, int count,
                                           int list, f32x4 *sums) {
     using S = Step<GRAD, XF32, WF32, MT>;
@@ -184,34 +194,46 @@ __device__ __forceinline__ void down_rows(const AdaptArgs &p, int64_t chunk, int
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block(), q = lane >> 4, j = lane & 15;
     const int r = static_cast<int>(rank0) + 4 * j;
     const float scale = p.scaling && p.splits == 1 ? p.scaling[g] : 1.0f;
-    int64_t at[MT];
+    const uint8_t *rows = static_cast<const uint8_t *>(p.x) + chunk * 64 * p.x_stride * (XF32 ? 4 : 2);
+    const uint8_t *adapter = static_cast<const uint8_t *>(p.w) + static_cast<int64_t>(g) * p.rank * p.len * (WF32 ? 4 : 2);
+    Off at[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) at[m] = (chunk * 64 + listed(list, min(16 * m + j, count - 1))) * p.x_stride;
+    for (int m = 0; m < MT; ++m) at[m] = static_cast<Off>(listed(list, min(16 * m + j, count - 1))) * static_cast<Off>(p.x_stride);
     f32x4 acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
     const int64_t s0 = split * p.split_steps + w, s1 = min((split + 1) * p.split_steps, p.len / 64);
-    if constexpr (AHEAD) {
+    if constexpr (AHEAD && !GRAD) {  // less code, which is fetched anew in every launch, than in turn
         S now, next;
-        if (s0 < s1) now.template load<true>(p, at, g, r, s0 * 64 + 16 * q);
+        if (s0 < s1) now.template load<true>(p, rows, adapter, at, r, s0);
         for (int64_t s = s0; s < s1; s += 4) {
-            if (s + 4 < s1) next.template load<true>(p, at, g, r, (s + 4) * 64 + 16 * q);
+            if (s + 4 < s1) next.template load<true>(p, rows, adapter, at, r, s + 4);
             now.use(acc);
             now = next;
         }
+    } else if constexpr (AHEAD) {
+        S a, b;
+        if (s0 < s1) a.template load<true>(p, rows, adapter, at, r, s0);
+        for (int64_t s = s0; s < s1; s += 8) {
+            if (s + 4 < s1) b.template load<true>(p, rows, adapter, at, r, s + 4);
+            a.use(acc);
+            if (s + 4 >= s1) break;
+            if (s + 8 < s1) a.template load<true>(p, rows, adapter, at, r, s + 8);
+            b.use(acc);
+        }
     } else {
         for (int64_t s = s0; s < s1; s += 4) {
-            S now;
-            now.template load<true>(p, at, g, r, s * 64 + 16 * q);
-            now.use(acc);
+            S a;
+            a.template load<true>(p, rows, adapter, at, r, s);
+            a.use(acc);
         }
     }
     // what is left, less than 64 indices, is the last part's, and the wave's whose turn it is
     if (const int64_t s = p.len / 64; p.len % 64 != 0 && s / p.split_steps == split && s % 4 == w) {
         S last;
-        last.template load<false>(p, at, g, r, s * 64 + 16 * q);
+        last.template load<false>(p, rows, adapter, at, r, s);
         last.use(acc);
     }
     // Lane (q, j) has rows 4 q + i and ranks 4 j + t: turned into one piece of four ranks a row.
@@ -266,12 +288,20 @@ __global__ __launch_bounds__(kBlockThreads, XF32 || WF32 ? 1 : 2) void adapter_d
         pending &= ~match;
         if (n % static_cast<int>(p.slots) != slot) continue;
         const int count = __popcll(match), list = list_bits(match);
-        if (count <= 16)
-            down_rows<GRAD, XF32, WF32, 1>(p, chunk, rank0, split, g, count, list, sums);
-        else if (count <= 32)
-            down_rows<GRAD, XF32, WF32, 2>(p, chunk, rank0, split, g, count, list, sums);
+        auto go = [&](auto off) {
+            using Off = decltype(off);
+            if (count <= 16)
+                down_rows<GRAD, XF32, WF32, 1, Off>(p, chunk, rank0, split, g, count, list, sums);
+            else if (count <= 32)
+                down_rows<GRAD, XF32, WF32, 2, Off>(p, chunk, rank0, split, g, count, list, sums);
+            else
+                down_rows<GRAD, XF32, WF32, 4, Off>(p, chunk, rank0, split, g, count, list, sums);
+        };
+        // in elements, and four bytes each: 64 rows of x, and an adapter's
+        if (GRAD && p.x_stride < (1 << 24) && p.rank * p.len < (1 << 30))
+            go(uint32_t{});
         else
-            down_rows<GRAD, XF32, WF32, 4>(p, chunk, rank0, split, g, count, list, sums);
+            go(int64_t{});
     }
 }
 
@@ -389,47 +419,79 @@ __device__ __forceinline__ void load4(const void *base, int64_t e, int64_t left,
     }
 }
 
-// What a lane loads of 32 of an adapter's rows: of the 8 that are its quarter's,
-// four neighbouring ranks of low and four neighbouring columns of x.
-template <bool F32, int PC>
-struct RowStep {
-    static constexpr int PX = F32 ? 3 : 1, kX = F32 ? 4 : 2;
-    f32x4 low[8];
+// 32 of an adapter's rows: which they are, and what a lane loads of the 8 that are its
+// quarter's, four neighbouring columns of x and four neighbouring ranks of low.
+template <bool F32>
+struct RowsOfX {
+    static constexpr int kX = F32 ? 4 : 2;
+    int64_t row0;        // of their chunk
+    int list, n, count;  // rows row0 + list[n] .. of `count` that the chunk has
     uint32_t x[8][kX];
 
-    // Rows n .. n + 31 of `count`; zeros past the last, on both sides, since such a row is in
-    // no sum, whatever it holds. WHOLE: the columns are all in the row.
-    template <bool WHOLE>
-    __device__ __forceinline__ void load(const RowsArgs &o, int rank, int64_t row0, int list, int n, int count, int r,
-                                         int64_t col) {
-        const int q = (threadIdx.x & (kWave - 1)) >> 4;
+    // The lane's first row; and its i-th, i rows on where the chunk has all of its rows.
+    __device__ __forceinline__ uint32_t first() const { return n + 8 * (threadIdx.x >> 4 & 3); }
+    __device__ __forceinline__ uint32_t row(int i) const {
+        return static_cast<uint32_t>(listed(list, min(static_cast<int>(first()) + i, count - 1)));
+    }
+
+    // FAST: the columns are all in the row, and 64 rows' offsets fit 32 bits.
+    template <bool FAST>
+    __device__ __forceinline__ void load(const RowsArgs &o, int64_t col) {
+        const uint8_t *rows = static_cast<const uint8_t *>(o.x) + row0 * o.x_stride * (F32 ? 4 : 2);
+        const uint32_t stride = static_cast<uint32_t>(o.x_stride) * (F32 ? 4 : 2);
+        const uint32_t at_col = static_cast<uint32_t>(col) * (F32 ? 4 : 2);
+        auto piece = [&](int i, const uint8_t *from, uint32_t at) {
+            if constexpr (F32) {
+                const u32x4 v = *reinterpret_cast<const u32x4_at4 *>(from + at);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = n + 8 * q + i;
-            const int64_t m = row0 + listed(list, min(at, count - 1));
-            low[i] = ld<f32x4>(o.low + m * rank + min(r, rank - 4));
-            if constexpr (WHOLE) {
-                if constexpr (F32) {
-                    const u32x4 v = *reinterpret_cast<const u32x4_at4 *>(static_cast<const float *>(o.x) + m * o.x_stride + col);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][e] = v[e];
-                } else {
-                    const u32x2 v = *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(o.x) + m * o.x_stride + col);
-                    x[i][0] = v[0], x[i][1] = v[1];
-                }
+                for (int e = 0; e < 4; ++e) x[i][e] = v[e];
             } else {
-                load4<F32>(o.x, m * o.x_stride + min(col, o.len), o.len - col, x[i]);
+                const u32x2 v = *reinterpret_cast<const u32x2_any *>(from + at);
+                x[i][0] = v[0], x[i][1] = v[1];
             }
-            if (at >= count) {
-                low[i] = f32x4{0, 0, 0, 0};
+        };
+        if (FAST && count == 64) {
+            const uint32_t at = first() * stride + at_col;
 #pragma unroll
-                for (int e = 0; e < kX; ++e) x[i][e] = 0;
+            for (int i = 0; i < 8; ++i) piece(i, rows + i * static_cast<uint64_t>(stride), at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (FAST)
+                    piece(i, rows, row(i) * stride + at_col);
+                else
+                    load4<F32>(rows, row(i) * o.x_stride + min(col, o.len), o.len - col, x[i]);
             }
         }
     }
 
+    __device__ __forceinline__ void load_low(const RowsArgs &o, int rank, int r, f32x4 (&low)[8]) const {
+        const float *lows = o.low + row0 * rank;
+        const uint32_t at = static_cast<uint32_t>(min(r, rank - 4)), stride = static_cast<uint32_t>(rank);
+        if (count == 64) {
+            const uint32_t from = first() * stride + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) low[i] = ld<f32x4>(lows + i * stride + from);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) low[i] = ld<f32x4>(lows + (row(i) * stride + at));
+        }
+    }
+
     // Turned: tile t has the lane's rank or column t.
-    __device__ __forceinline__ void use(f32x4 (&acc)[4][4]) const {
+    template <int PC>
+    __device__ __forceinline__ void use(f32x4 (&low)[8], f32x4 (&acc)[4][4]) {
+        constexpr int PX = F32 ? 3 : 1;
+        if (n + 32 > count) {  // zeros past the last, on both sides: such a row is in no sum, whatever it holds
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = n + 8 * static_cast<int>(threadIdx.x >> 4 & 3) + i < count;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) low[i][e] = in ? low[i][e] : 0.0f;
+#pragma unroll
+                for (int e = 0; e < kX; ++e) x[i][e] = in ? x[i][e] : 0u;
+            }
+        }
         u32x4 b[4][PX];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -459,11 +521,11 @@ struct RowStep {
 };
 
 // The sums of one wave: chunks c0 + w, c0 + w + 8, ... The next 32 rows' loads are under
-// way while these are multiplied, and the ids of the next chunk.
-template <bool F32, int PC, bool WHOLE>
+// way while these are multiplied (two steps ahead gained nothing), and the ids of the next chunk.
+template <bool F32, int PC, bool FAST>
 __device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &o, int g, int64_t c0, int64_t c1, int r,
                                              int64_t col, f32x4 (&acc)[4][4]) {
-    using S = RowStep<F32, PC>;
+    using S = RowsOfX<F32>;
     const int lane = threadIdx.x & (kWave - 1);
     auto id_of = [&](int64_t c) {
         const int64_t row = c * 64 + lane;
@@ -471,31 +533,39 @@ __device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &
         return p.ids ? p.ids[row] : 0;
     };
     int64_t c = c0 + wave_in_block();
-    int ids = c < c1 ? id_of(c) : -1, list = 0, count = 0, n = 0;
-    int64_t row0 = 0;
-    // The next 32 rows of the adapter: false if there are none.
-    auto advance = [&] {
-        n += 32;
-        while (n >= count) {
+    int ids = c < c1 ? id_of(c) : -1;
+    // The 32 rows of the adapter behind those of `s`, into `to`: false if there are none.
+    auto advance = [&](const S &s, S &to, f32x4(&low)[8]) {
+        to.row0 = s.row0, to.list = s.list, to.n = s.n + 32, to.count = s.count;
+        while (to.n >= to.count) {
             if (c >= c1) return false;
             const uint64_t match = __ballot(ids == g);
-            row0 = c * 64;
+            to.row0 = c * 64;
             c += kRowWaves;
             ids = c < c1 ? id_of(c) : -1;
-            n = 0;
-            count = __popcll(match);
-            if (count > 0) list = list_bits(match);
+            to.n = 0;
+            to.count = __popcll(match);
+            to.list = list_bits(match);
         }
+        to.template load<FAST>(o, col);
+        to.load_low(o, p.rank, r, low);
         return true;
     };
-    S now, next;
-    bool more = advance();
-    if (more) now.template load<WHOLE>(o, p.rank, row0, list, n, count, r, col);
-    while (more) {
-        more = advance();
-        if (more) next.template load<WHOLE>(o, p.rank, row0, list, n, count, r, col);
-        now.use(acc);
-        now = next;
+    S s0, s1;
+    f32x4 low0[8], low1[8];
+    s0.row0 = 0, s0.list = s0.n = s0.count = 0;
+    if constexpr (F32) {  // two sets of binary32 rows do not fit
+        while (advance(s0, s0, low0)) s0.template use<PC>(low0, acc);
+        return;
+    }
+    if (!advance(s0, s0, low0)) return;
+    for (;;) {  // in turn: copied from one to the other, they were a fifth of the instructions
+        const bool more1 = advance(s0, s1, low1);
+        s0.template use<PC>(low0, acc);
+        if (!more1) return;
+        const bool more0 = advance(s1, s0, low0);
+        s1.template use<PC>(low1, acc);
+        if (!more0) return;
     }
 }
 
@@ -529,7 +599,7 @@ __global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall
         for (int t = 0; t < 4; ++t) acc[a][t] = f32x4{0, 0, 0, 0};
 
     const int64_t c0 = split * p.split_chunks, c1 = min(c0 + p.split_chunks, (p.rows + 63) / 64);
-    if (tile * 64 + 64 <= o.len)
+    if (tile * 64 + 64 <= o.len && o.x_stride < (1 << 22))
         adapter_sums<F32, PC, true>(p, o, g, c0, c1, r, col, acc);
     else
         adapter_sums<F32, PC, false>(p, o, g, c0, c1, r, col, acc);
