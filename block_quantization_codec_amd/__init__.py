@@ -499,6 +499,19 @@ def _code(dtype) -> int:
     return c
 
 
+def _torch(name: str):
+    """torch's attribute of that name, without an import statement's time at each call."""
+    v = _TORCH.get(name)
+    if v is None:
+        import torch
+
+        v = _TORCH[name] = getattr(torch, name)
+    return v
+
+
+_TORCH: dict = {}
+
+
 def _rows(t, name: str):
     """(rows, width, row stride in elements) of a tensor whose leading dimensions
     follow one stride and whose last one is contiguous."""
@@ -808,13 +821,22 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, workspace=None, w_dtype
     return out, dw, db
 
 
-def _rows_of(t, x, name: str):
+def _rows_of(t, x, rows: int, width: int, name: str):
     """(address, row stride) of a matrix of x's shape and dtype, (None, 0) of None."""
     if t is None:
         return None, 0
-    if t.shape != x.shape or t.dtype != x.dtype:
+    if t.dtype != x.dtype or t.shape != x.shape:
         raise ValueError(f"{name} must be of x's shape and dtype")
-    return t.data_ptr(), _rows(t, name)[2]
+    return t.data_ptr(), width if t.is_contiguous() else _rows(t, name)[2]
+
+
+def _result(t, x, rows: int, width: int):
+    """``t`` (or a new tensor) of x's shape and dtype, its address and its row stride."""
+    if t is None:
+        like = _torch("empty_like")
+        t = like(x) if x.is_contiguous() else like(x, memory_format=_torch("contiguous_format"))
+        return t, t.data_ptr(), width
+    return (t, *_rows_of(t, x, rows, width, "out"))
 
 
 def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, bits: int = 0, block: int = 0, want_y: bool = True,
@@ -829,31 +851,31 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, bits: int = 0, bl
     Autograd does not see the call, as with :func:`linear`."""
     if stream is not None:
         return _under(stream, rms_norm, x, weight, residual, eps, bits, block, want_y, out, total, codes, scales, rstd)
-    import torch
-
     rows, width, stride = _rows(x, "x")
     xdt = _code(x.dtype)
     w, wdt = _vector(weight, width, "weight")
-    res, res_stride = _rows_of(residual, x, "residual")
+    res, res_stride = _rows_of(residual, x, rows, width, "residual")
     if (total is not None and residual is None) or (out is not None and not want_y) or \
             (not bits and (codes is not None or scales is not None)):
         raise ValueError("a result is passed in that is not asked for")
-    y_ptr, y_stride, sum_ptr, sum_stride = None, 0, None, 0
+    y_ptr = sum_ptr = codes_ptr = scales_ptr = None
+    y_stride = sum_stride = 0
     if want_y:
-        out, y_stride = _like(out, x)
-        y_ptr = out.data_ptr()
+        out, y_ptr, y_stride = _result(out, x, rows, width)
     if residual is not None:
-        total, sum_stride = _like(total, x)
-        sum_ptr = total.data_ptr()
-    rstd = _buffer(rstd, x.shape[:-1], torch.float32, "rstd", x)
+        total, sum_ptr, sum_stride = _result(total, x, rows, width)
+    f32 = _torch("float32")
+    rstd = x.new_empty(x.shape[:-1], dtype=f32) if rstd is None else _buffer(rstd, x.shape[:-1], f32, "rstd", x)
     if bits:
         if block <= 0 or width % block or (bits != 4 and bits != 8):
             raise ValueError(f"{bits}-bit blocks of {block} do not divide rows of {width}")
-        codes = _buffer(codes, (rows * width * bits // 8,), torch.uint8, "codes", x)
-        scales = _buffer(scales, (rows * width // block,), torch.float32, "scales", x)
+        codes = _buffer(codes, (rows * width * bits // 8,), _torch("uint8"), "codes", x)
+        scales = _buffer(scales, (rows * width // block,), f32, "scales", x)
+        codes_ptr, scales_ptr = codes.data_ptr(), scales.data_ptr()
+    else:
+        block = 0
     _call("zpp_rms_norm", x.data_ptr(), xdt, stride, res, res_stride, rows, width, w, wdt or xdt, eps, sum_ptr,
-          sum_stride, y_ptr, y_stride, _ptr(codes), _ptr(scales), bits, block if bits else 0, rstd.data_ptr(),
-          _stream(stream))
+          sum_stride, y_ptr, y_stride, codes_ptr, scales_ptr, bits, block, rstd.data_ptr(), _stream(stream))
     return out, total, rstd, codes, scales
 
 
@@ -867,19 +889,17 @@ def rms_norm_grad(dy, x, weight, rstd, dsum=None, out=None, workspace=None, w_dt
     if stream is not None:
         return _under(stream, rms_norm_grad, dy, x, weight, rstd, dsum, out, workspace, w_dtype, dweight)
     rows, width, stride = _rows(x, "x")
-    import torch
-
-    if not (rstd.is_contiguous() and rstd.numel() == rows and rstd.dtype == torch.float32):
+    if not (rstd.is_contiguous() and rstd.numel() == rows and rstd.dtype == _torch("float32")):
         raise ValueError("rstd must be contiguous float32, one element per row")
     w, _ = _vector(weight, width, "weight")
     wt = weight.dtype if weight is not None else (w_dtype or x.dtype)
     xdt, wdt = _code(x.dtype), _code(wt)
-    dy_ptr, dy_stride = _rows_of(dy, x, "dy")
-    ds_ptr, ds_stride = _rows_of(dsum, x, "dsum")
-    out, ostride = _like(out, x)
-    dw = _buffer(dweight, (width,), wt, "dweight", x)
+    dy_ptr, dy_stride = _rows_of(dy, x, rows, width, "dy")
+    ds_ptr, ds_stride = _rows_of(dsum, x, rows, width, "dsum")
+    out, out_ptr, ostride = _result(out, x, rows, width)
+    dw = x.new_empty((width,), dtype=wt) if dweight is None else _buffer(dweight, (width,), wt, "dweight", x)
     need = _lib.zpp_rms_norm_grad_workspace(rows, width) if workspace is None else 0
     ws, ws_bytes, keep = _workspace(workspace, need, x)
     _call("zpp_rms_norm_grad", dy_ptr, dy_stride, x.data_ptr(), xdt, stride, ds_ptr, ds_stride, rows, width, w, wdt,
-          rstd.data_ptr(), out.data_ptr(), ostride, dw.data_ptr(), ws, ws_bytes, _stream(stream))
+          rstd.data_ptr(), out_ptr, ostride, dw.data_ptr(), ws, ws_bytes, _stream(stream))
     return out, dw
