@@ -533,11 +533,9 @@ def _rows(t, name: str):
 
 
 def _check_weight(codes, scales, bits: int, block: int, numel: int) -> None:
-    import torch
-
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("codes and scales must be contiguous")
-    if codes.element_size() != 1 or scales.dtype != torch.float32:
+    if codes.element_size() != 1 or scales.dtype != _torch("float32"):
         raise TypeError("codes must be bytes and scales float32")
     if codes.numel() * 8 != numel * bits or scales.numel() * block != numel:
         raise ValueError(f"codes and scales do not hold {numel} weights in {bits}-bit blocks of {block}")
@@ -548,9 +546,7 @@ def _workspace(workspace, need: int, like):
     if workspace is None:
         if not need:
             return None, 0, None
-        import torch
-
-        workspace = like.new_empty(need, dtype=torch.uint8)
+        workspace = like.new_empty(need, dtype=_torch("uint8"))
     elif not workspace.is_contiguous():  # it would be taken for as many bytes from its first one on
         raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -561,15 +557,8 @@ def _linear(name: str, grad: int, a, codes, scales, bits, block, out_len, dtype,
     n_out, n_in = (width, out_len) if grad else (out_len, width)
     groups = 1 if offsets is None else _check_offsets(offsets)
     _check_weight(codes, scales, bits, block, groups * n_out * n_in)
-    adt, ostride = _code(a.dtype), out_len
-    if out is None:
-        dtype = dtype or a.dtype
-        odt = _code(dtype)
-        out = a.new_empty((*a.shape[:-1], out_len), dtype=dtype)
-    else:
-        if tuple(out.shape) != (*a.shape[:-1], out_len) or (dtype or out.dtype) != out.dtype:
-            raise ValueError(f"out must be of shape {(*a.shape[:-1], out_len)} and of the dtype asked for")
-        odt, ostride = _code(out.dtype), _rows(out, "out")[2]
+    adt = _code(a.dtype)
+    out, odt, ostride = _out(out, dtype, a, out_len)
     if offsets is None:
         need, group_args = _lib.zpp_linear_blocks_workspace(grad, adt, stride, odt, rows, n_out, n_in), ()
     else:
@@ -583,9 +572,7 @@ def _linear(name: str, grad: int, a, codes, scales, bits, block, out_len, dtype,
 
 def _check_offsets(offsets) -> int:
     """The number of groups that ``offsets`` begin and end."""
-    import torch
-
-    if offsets.dtype != torch.int32:
+    if offsets.dtype != _torch("int32"):
         raise TypeError("offsets must be int32")
     if offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
         raise ValueError("offsets must be contiguous, of one dimension, one element more than groups")
@@ -643,21 +630,39 @@ def linear_grouped_grad(dy, offsets, codes, scales, bits: int, block: int, in_fe
 
 def _adapters(a, b, ids, scaling, rows: int, n_out: int, n_in: int):
     """The adapters' arguments of an entry point, from a on."""
-    import torch
-
-    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != n_in or b.shape[1] != n_out or a.shape[0] != b.shape[0] or \
-            a.shape[1] != b.shape[2]:
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a and b must have three dimensions")
+    adapters, rank, a_in = a.shape
+    b_adapters, b_out, b_rank = b.shape
+    if a_in != n_in or b_out != n_out or adapters != b_adapters or rank != b_rank:
         raise ValueError(f"a must be [adapters, rank, {n_in}] and b [adapters, {n_out}, rank]")
-    if a.dtype != b.dtype:
+    dtype = a.dtype
+    if dtype != b.dtype:
         raise TypeError("a and b must be of one dtype")
     if not (a.is_contiguous() and b.is_contiguous()):
         raise ValueError("a and b must be contiguous")
-    if ids is not None and (ids.dtype != torch.int32 or not ids.is_contiguous() or ids.numel() != rows):
-        raise ValueError(f"ids must be contiguous int32, {rows} elements")
-    if scaling is not None and (scaling.dtype != torch.float32 or not scaling.is_contiguous()
-                                or scaling.numel() != a.shape[0]):
-        raise ValueError(f"scaling must be contiguous float32, {a.shape[0]} elements")
-    return (a.data_ptr(), b.data_ptr(), _code(a.dtype), a.shape[0], a.shape[1], _ptr(ids), _ptr(scaling))
+    ids_ptr = scaling_ptr = None
+    if ids is not None:
+        if ids.dtype != _torch("int32") or not ids.is_contiguous() or ids.numel() != rows:
+            raise ValueError(f"ids must be contiguous int32, {rows} elements")
+        ids_ptr = ids.data_ptr()
+    if scaling is not None:
+        if scaling.dtype != _torch("float32") or not scaling.is_contiguous() or scaling.numel() != adapters:
+            raise ValueError(f"scaling must be contiguous float32, {adapters} elements")
+        scaling_ptr = scaling.data_ptr()
+    return a.data_ptr(), b.data_ptr(), _code(dtype), adapters, rank, ids_ptr, scaling_ptr
+
+
+def _out(out, dtype, like, length: int):
+    """(``out`` or a new tensor of ``dtype``, ``like``'s shape but for a last dimension of ``length``; its dtype's
+    code; its row stride)."""
+    if out is None:
+        dtype = dtype or like.dtype
+        return like.new_empty((*like.shape[:-1], length), dtype=dtype), _code(dtype), length
+    shape = (*like.shape[:-1], length)
+    if tuple(out.shape) != shape or (dtype or out.dtype) != out.dtype:
+        raise ValueError(f"out must be of shape {shape} and of the dtype asked for")
+    return out, _code(out.dtype), _rows(out, "out")[2]
 
 
 def linear_adapters(x, codes, scales, bits: int, block: int, out_features: int, a, b, ids=None, scaling=None, dtype=None,
@@ -673,21 +678,14 @@ def linear_adapters(x, codes, scales, bits: int, block: int, out_features: int, 
     if stream is not None:
         return _under(stream, linear_adapters, x, codes, scales, bits, block, out_features, a, b, ids, scaling, dtype,
                       out, reduced, workspace)
-    import torch
-
     rows, n_in, stride = _rows(x, "x")
     _check_weight(codes, scales, bits, block, out_features * n_in)
     adapters = _adapters(a, b, ids, scaling, rows, out_features, n_in)
-    xdt, shape = _code(x.dtype), (*x.shape[:-1], out_features)
-    if out is None:
-        out, ostride = x.new_empty(shape, dtype=dtype or x.dtype), out_features
-    else:
-        if tuple(out.shape) != shape or (dtype or out.dtype) != out.dtype:
-            raise ValueError(f"out must be of shape {shape} and of the dtype asked for")
-        ostride = _rows(out, "out")[2]
-    odt = _code(out.dtype)
-    reduced = _buffer(reduced, (*x.shape[:-1], a.shape[1]), torch.float32, "reduced", x)
-    need = _lib.zpp_linear_adapters_workspace(0, xdt, stride, odt, rows, out_features, n_in, a.shape[0], a.shape[1])
+    xdt, f32, rank = _code(x.dtype), _torch("float32"), adapters[4]
+    out, odt, ostride = _out(out, dtype, x, out_features)
+    shape = (*x.shape[:-1], rank)
+    reduced = x.new_empty(shape, dtype=f32) if reduced is None else _buffer(reduced, shape, f32, "reduced", x)
+    need = _lib.zpp_linear_adapters_workspace(0, xdt, stride, odt, rows, out_features, n_in, adapters[3], rank)
     ws, ws_bytes, keep = _workspace(workspace, need, x)
     _call("zpp_linear_adapters", x.data_ptr(), xdt, stride, rows, codes.data_ptr(), scales.data_ptr(), bits,
           out_features, n_in, block, *adapters, reduced.data_ptr(), out.data_ptr(), odt, ostride, ws, ws_bytes,
@@ -703,37 +701,29 @@ def linear_adapters_grad(dy, x, reduced, codes, scales, bits: int, block: int, a
     if stream is not None:
         return _under(stream, linear_adapters_grad, dy, x, reduced, codes, scales, bits, block, a, b, ids, scaling, dtype,
                       out, want_adapters, da, db, workspace)
-    import torch
-
     rows, n_out, stride = _rows(dy, "dy")
     n_in = a.shape[-1]
     _check_weight(codes, scales, bits, block, n_out * n_in)
     adapters = _adapters(a, b, ids, scaling, rows, n_out, n_in)
-    ddt, shape, rank = _code(dy.dtype), (*dy.shape[:-1], n_in), a.shape[1]
-    x_ptr, x_stride = None, n_in
+    ddt, rank = _code(dy.dtype), adapters[4]
+    x_ptr, x_stride, reduced_ptr = None, n_in, None
     if want_adapters:
-        if tuple(x.shape) != shape or x.dtype != dy.dtype:
-            raise ValueError(f"x must be of shape {shape} and of dy's dtype")
-        if tuple(reduced.shape) != (*dy.shape[:-1], rank) or reduced.dtype != torch.float32 or \
-                not reduced.is_contiguous():
-            raise ValueError(f"reduced must be contiguous float32, of shape {(*dy.shape[:-1], rank)}")
-        x_ptr, x_stride = x.data_ptr(), _rows(x, "x")[2]
+        lead = dy.shape[:-1]
+        if tuple(x.shape) != (*lead, n_in) or x.dtype != dy.dtype:
+            raise ValueError(f"x must be of shape {(*lead, n_in)} and of dy's dtype")
+        if tuple(reduced.shape) != (*lead, rank) or reduced.dtype != _torch("float32") or not reduced.is_contiguous():
+            raise ValueError(f"reduced must be contiguous float32, of shape {(*lead, rank)}")
+        x_ptr, x_stride, reduced_ptr = x.data_ptr(), _rows(x, "x")[2], reduced.data_ptr()
         da = _buffer(da, a.shape, a.dtype, "da", dy)
         db = _buffer(db, b.shape, b.dtype, "db", dy)
     elif da is not None or db is not None:
         raise ValueError("a result is passed in that is not asked for")
-    if out is None:
-        out, ostride = dy.new_empty(shape, dtype=dtype or dy.dtype), n_in
-    else:
-        if tuple(out.shape) != shape or (dtype or out.dtype) != out.dtype:
-            raise ValueError(f"out must be of shape {shape} and of the dtype asked for")
-        ostride = _rows(out, "out")[2]
-    odt = _code(out.dtype)
-    need = _lib.zpp_linear_adapters_workspace(1, ddt, stride, odt, rows, n_out, n_in, a.shape[0], rank)
+    out, odt, ostride = _out(out, dtype, dy, n_in)
+    need = _lib.zpp_linear_adapters_workspace(1, ddt, stride, odt, rows, n_out, n_in, adapters[3], rank)
     ws, ws_bytes, keep = _workspace(workspace, need, dy)
-    _call("zpp_linear_adapters_grad", dy.data_ptr(), ddt, stride, x_ptr, x_stride,
-          reduced.data_ptr() if want_adapters else None, rows, codes.data_ptr(), scales.data_ptr(), bits, n_out, n_in,
-          block, *adapters, out.data_ptr(), odt, ostride, _ptr(da), _ptr(db), ws, ws_bytes, _stream(stream))
+    _call("zpp_linear_adapters_grad", dy.data_ptr(), ddt, stride, x_ptr, x_stride, reduced_ptr, rows, codes.data_ptr(),
+          scales.data_ptr(), bits, n_out, n_in, block, *adapters, out.data_ptr(), odt, ostride, _ptr(da), _ptr(db), ws,
+          ws_bytes, _stream(stream))
     return out, da, db
 
 
