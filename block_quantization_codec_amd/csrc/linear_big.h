@@ -463,59 +463,94 @@ struct LinBig {
         if constexpr (M + 1 < MT) rows_from<HN, M + 1>(here, then, b, raw, s, bn, a, scale, acc, before);
     }
 
-    // Rows of tiles that adapters are added to at once: 64 rows, or all of a smaller tile's.
-    static constexpr int kTogether = MT > 4 ? 4 : MT;
+    // Rows of tiles that adapters are added to at once: 64 rows, 32 where half the registers are
+    // there, or all of a smaller tile's.
+    static constexpr int kTogether = MT == 1 ? 1 : MT < 16 && PA * PB == 1 ? 2 : 4;
 
-    // Whether the kTogether rows of tiles from row `first` on have all the same adapter
-    // (`one`; -1: none has any).
-    static __device__ __forceinline__ bool one_adapter(const LinArgs &p, int64_t first, int &one) {
-        const int lane = threadIdx.x & (kWave - 1);
-        int id;
-        if (!adapter_of(p, min(first + min(lane, kTogether * 16 - 1), p.rows - 1), id)) id = -1;
-        one = __builtin_amdgcn_readfirstlane(id);
-        return __ballot(id != one) == 0;
-    }
-
-    // d += low up of adapter g, for kTogether rows of tiles from row `first` on. S steps of 32
-    // ranks at a time: all their loads are under way together. Low comes by buffer
-    // loads, whose range check gives zeros for rows past the end.
-    template <int PC, int PU, int S>
-    static __device__ __forceinline__ void add_adapter(const LinArgs &p, int64_t first, int64_t col, int g,
-                                                       f32x4 (&d)[kTogether][4]) {
+    // d += low up of adapter g, for those of kTogether rows of tiles from row `first` on that are
+    // in `match`. Low comes by buffer loads, whose range check gives zeros for the other
+    // rows, for rows past the end and ranks past the last. Zeros times infinities are NaN: false
+    // if the adapter holds any that another row would see.
+    template <int PC>
+    static __device__ __forceinline__ bool add_adapter(const LinArgs &p, int lane, int64_t first, int64_t col, int g,
+                                                       uint64_t match, f32x4 (&d)[kTogether][4]) {
+        uint32_t bad = 0;
 #if defined(__HIP_DEVICE_COMPILE__)
-        const int lane = threadIdx.x & (kWave - 1), q = lane >> 4, j = lane & 15;
-        const int left = static_cast<int>(min(p.rows - first, static_cast<int64_t>(kTogether * 16)));
+        constexpr int kRowsOf = kTogether * 16;
+        constexpr uint32_t kOut = 1u << 30;
+        const int q = lane >> 4, j = lane & 15;
+        const int left = static_cast<int>(min(p.rows - first, static_cast<int64_t>(kRowsOf)));
         const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<float *>(p.low + first * p.rank), 0, static_cast<uint32_t>(left * p.rank * 4), 0x27000);
+        const bool mixed = __popcll(match) != left;
+        uint32_t at[kTogether];
+#pragma unroll
+        for (int m = 0; m < kTogether; ++m)
+            at[m] = match >> (m * 16 + j) & 1 ? static_cast<uint32_t>((m * 16 + j) * p.rank * 4) : kOut;
 #pragma unroll 1
-        for (int r0 = 0; r0 < p.rank; r0 += 32 * S) {
-            u32x4 b[S][4][PU], low[S][kTogether][2];
+        for (int r0 = 0; r0 < p.rank; r0 += 32) {
+            const int r = r0 + 8 * q;
+            const uint32_t plus = r < p.rank ? static_cast<uint32_t>(r * 4) : kOut;
+            u32x4 b[4][1], low[kTogether][2];
+            load_up<GRAD, true, 1, 4>(p, g, col, r, b);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int r = r0 + 32 * s + 8 * q;
-                // past the rank: an offset out of range
-                const int at = r < p.rank ? (j * p.rank + r) * 4 : 1 << 30;
-                load_up<GRAD, true, PU, 4>(p, g, col, r, b[s]);
+            for (int m = 0; m < kTogether; ++m)
 #pragma unroll
-                for (int m = 0; m < kTogether; ++m)
+                for (int h = 0; h < 2; ++h)
+                    low[m][h] = __builtin_amdgcn_raw_buffer_load_b128(from, at[m] + plus, 16 * h, 0);
+            if (mixed) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        low[s][m][h] = __builtin_amdgcn_raw_buffer_load_b128(from, at + m * 16 * p.rank * 4, 16 * h, 0);
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // an exponent of ones in either half
+                        const uint32_t e = ~b[t][0][i];
+                        bad |= (e & 0x7F80u) == 0 || (e & 0x7F800000u) == 0 ? 1u : 0u;
+                    }
             }
 #pragma unroll
-            for (int s = 0; s < S; ++s)
+            for (int m = 0; m < kTogether; ++m) {
+                float v[8];
 #pragma unroll
-                for (int m = 0; m < kTogether; ++m) {
-                    float v[8];
+                for (int i = 0; i < 8; ++i) v[i] = as_f(low[m][i / 4][i % 4]);
+                u32x4 a[PC];
+                operand_of<PC>(v, a);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = as_f(low[s][m][i / 4][i % 4]);
-                    u32x4 a[PC];
-                    operand_of<PC>(v, a);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) d[m][t] = mfma_parts<PC, PU>(a, b[s][t], d[m][t]);
-                }
+                for (int t = 0; t < 4; ++t) d[m][t] = mfma_parts<PC, 1>(a, b[t], d[m][t]);
+            }
         }
 #endif
+        return __ballot(bad != 0) == 0;
+    }
+
+    // What the adapters add to kTogether rows of tiles from row `first` on. Up to four bf16
+    // adapters one after the other, each with all the rows; false, and zeros, where there are more,
+    // or an adapter's infinities or NaNs: then the rows have to be gathered.
+    template <int PC>
+    static __device__ __forceinline__ bool add_adapters(const LinArgs &p, int lane, int64_t first, int64_t col,
+                                                        f32x4 (&d)[kTogether][4]) {
+#pragma unroll
+        for (int m = 0; m < kTogether; ++m)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
+        int id;
+        const bool has = adapter_of(p, first + lane, id) && lane < kTogether * 16;
+        uint64_t pending = __ballot(has);
+        if (pending == 0) return true;
+        bool good = !p.up_f32;
+#pragma unroll 1
+        for (int n = 0; good && pending != 0; ++n) {
+            const int g = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
+            const uint64_t match = __ballot(has && id == g);
+            pending &= ~match;
+            good = n < 4 && add_adapter<PC>(p, lane, first, col, g, match, d);
+        }
+        if (good) return true;
+#pragma unroll
+        for (int m = 0; m < kTogether; ++m)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
+        return false;
     }
 };
 
@@ -630,29 +665,32 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
     }
 
     if constexpr (MODE == LinMode::adapted) {
-        // Some rows at a time, in a loop, through LDS: written out for each of the 256 sums, the stores
-        // and what the adapters add would be 100 KB of instructions. The next rows' sums move up.
-        // Adapters are added with the first part of the contraction.
+        // Some rows at a time, through LDS, from which a loop stores them. Adapters are added with
+        // the first part of the contraction. (Written out for all the sums, so that they stay where
+        // they are: in a loop that moves them up, they were moved in the products' loop too.)
         constexpr int kTogether = L::kTogether, PC = PA * PB == 1 ? 2 : 3;
         static_assert(L::kBufs * L::kBytes >= 4 * kTogether * 16 * 64 * 4 && MT % kTogether == 0);
         float *const held = reinterpret_cast<float *>(&tiles[0][0] + w * (kTogether * 16 * 64 * 4));
         __syncthreads();  // no wave reads activations any more
+        // The lane as the compiler cannot know it before: what follows from it is not worked out ahead
+        // of the loop, where no register is left to keep it in.
+        int lane = threadIdx.x & (kWave - 1);
+        asm volatile("" : "+v"(lane));
+        const int q = lane >> 4;
+        const int64_t col = wave_col + (lane & 15) * 4;
         // Rows of tiles M0 .. M0 + kTogether - 1 of the sums, which are rows from `first` on.
         auto finish = [&](auto at, int64_t first) {
             constexpr int M0 = at.value;
-            bool apart = false;
             f32x4 d[kTogether][4];
-#pragma unroll
-            for (int m = 0; m < kTogether; ++m)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
+            bool apart = false;
             if (place.split == 0) {
-                int one;
-                apart = !L::one_adapter(p, first, one) || (one >= 0 && p.up_f32);
-                if (apart)
-                    adapter_rows<GRAD, true, PC, 4, kTogether * 16, 2, 1>(p, first, col, 0, 1, held);
-                else if (one >= 0)
-                    L::template add_adapter<PC, 1, 1>(p, first, col, one, d);
+                apart = !L::template add_adapters<PC>(p, lane, first, col, d);
+                if (apart) adapter_rows<GRAD, true, PC, 4, kTogether * 16, 2, 1>(p, first, col, 0, 1, held);
+            } else {
+#pragma unroll
+                for (int m = 0; m < kTogether; ++m)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
             }
 #pragma unroll
             for (int m = 0; m < kTogether; ++m)
@@ -676,23 +714,17 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         };
-        if constexpr (MT == 16) {
-#pragma unroll 1
-            for (int m1 = 0; m1 < MT; m1 += kTogether) {
-                if (m0 + m1 * 16 >= p.rows) break;
-                finish(std::integral_constant<int, 0>{}, m0 + m1 * 16);
-#pragma unroll
-                for (int m = 0; m + kTogether < MT; ++m)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[m][t] = acc[m + kTogether][t];
-            }
-        } else {  // fewer sums, and no registers to move them through
-            finish(std::integral_constant<int, 0>{}, m0);
-            if constexpr (MT > kTogether) {
-                if (m0 + kTogether * 16 < p.rows) finish(std::integral_constant<int, kTogether>{}, m0 + kTogether * 16);
-            }
-            static_assert(MT <= 2 * kTogether);
+        finish(std::integral_constant<int, 0>{}, m0);
+        if constexpr (MT > kTogether) {
+            if (m0 + kTogether * 16 < p.rows) finish(std::integral_constant<int, kTogether>{}, m0 + kTogether * 16);
         }
+        if constexpr (MT > 2 * kTogether) {
+            if (m0 + 2 * kTogether * 16 < p.rows)
+                finish(std::integral_constant<int, 2 * kTogether>{}, m0 + 2 * kTogether * 16);
+            if (m0 + 3 * kTogether * 16 < p.rows)
+                finish(std::integral_constant<int, 3 * kTogether>{}, m0 + 3 * kTogether * 16);
+        }
+        static_assert(MT == kTogether || MT == 2 * kTogether || MT == 4 * kTogether);
         return;
     }
 
