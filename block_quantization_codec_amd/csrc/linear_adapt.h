@@ -6,10 +6,11 @@
 // The product's own kernels add it to their sums, before the result's one rounding:
 // a pass of its own would read and write the result again, and round it twice.
 //
-// Rows of a tile may have different adapters. Tiles whose rows all have one take it
-// into their sums by more matrix instructions. In others the rows of each adapter are
-// gathered and multiplied by themselves, so that nothing of an adapter, not its
-// infinities or NaNs either, reaches another's rows.
+// Rows of a tile may have different adapters. In tiles of many rows up to four bf16
+// adapters are multiplied in turn, low set to zero in the rows that have another; if
+// a sum is not finite, and in tiles of more adapters or of few rows, the rows of each
+// adapter are gathered and multiplied by themselves, so that nothing of an adapter,
+// not its infinities or NaNs either, reaches another's rows.
 //
 // Precision: low is binary32 and enters as bf16 parts, like binary32 activations:
 // two of them (16 bits: off by 2^-17, against the 2^-9 of a bf16 result) from

@@ -373,7 +373,8 @@ hipError_t launch_down(AdaptArgs p, bool x_f32, bool w_f32, hipStream_t stream) 
 
 // ---- the adapters' gradients --------------------------------------------------------
 
-constexpr int kRowWaves = 8;  // of a workgroup, on the same columns
+constexpr int kRowWaves = 8;    // of a workgroup, on the same columns
+constexpr int kAloneWaves = 4;  // each on its own
 
 struct RowsArgs {
     const void *x;       // rows of len elements: x (dA) or dy (dB)
@@ -381,7 +382,7 @@ struct RowsArgs {
     const float *low;    // [rows][rank]
     void *out;           // [adapters][rank][len] (dA), [adapters][len][rank] (dB)
     float *partial;
-    int64_t tiles;       // of 64 columns; 0: not wanted
+    int64_t tiles;       // of 64 columns (4 of them, ALONE); 0: not wanted
 };
 
 struct RowsCall {
@@ -520,11 +521,12 @@ struct RowsOfX {
     }
 };
 
-// The sums of one wave: chunks c0 + w, c0 + w + 8, ... The next 32 rows' loads are under
-// way while these are multiplied (two steps ahead gained nothing), and the ids of the next chunk.
-template <bool F32, int PC, bool FAST>
-__device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &o, int g, int64_t c0, int64_t c1, int r,
-                                             int64_t col, f32x4 (&acc)[4][4]) {
+// The sums of one wave over chunks c, c + step, ... below c1. The next 32 rows' loads are under
+// way while these are multiplied (AHEAD: two sets of binary32 rows do not fit, and few rows have
+// no next; two steps ahead gained nothing), and the ids of the next chunk.
+template <bool F32, int PC, bool FAST, bool AHEAD>
+__device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &o, int g, int64_t c, int64_t step,
+                                             int64_t c1, int r, int64_t col, f32x4 (&acc)[4][4]) {
     using S = RowsOfX<F32>;
     const int lane = threadIdx.x & (kWave - 1);
     auto id_of = [&](int64_t c) {
@@ -532,7 +534,6 @@ __device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &
         if (row >= p.rows) return -1;
         return p.ids ? p.ids[row] : 0;
     };
-    int64_t c = c0 + wave_in_block();
     int ids = c < c1 ? id_of(c) : -1;
     // The 32 rows of the adapter behind those of `s`, into `to`: false if there are none.
     auto advance = [&](const S &s, S &to, f32x4(&low)[8]) {
@@ -541,7 +542,7 @@ __device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &
             if (c >= c1) return false;
             const uint64_t match = __ballot(ids == g);
             to.row0 = c * 64;
-            c += kRowWaves;
+            c += step;
             ids = c < c1 ? id_of(c) : -1;
             to.n = 0;
             to.count = __popcll(match);
@@ -554,7 +555,7 @@ __device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &
     S s0, s1;
     f32x4 low0[8], low1[8];
     s0.row0 = 0, s0.list = s0.n = s0.count = 0;
-    if constexpr (F32) {  // two sets of binary32 rows do not fit
+    if constexpr (!AHEAD) {
         while (advance(s0, s0, low0)) s0.template use<PC>(low0, acc);
         return;
     }
@@ -570,10 +571,13 @@ __device__ __forceinline__ void adapter_sums(const RowsCall &p, const RowsArgs &
 }
 
 // One adapter's sums over its rows, 64 ranks x 64 columns a workgroup: the waves
-// take chunks of 64 rows in turn, and their sums meet in LDS.
-template <bool F32, int PC>
-__global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall p) {
-    __shared__ f32x4 sums[kRowWaves / 2][16][kWave];
+// take chunks of 64 rows in turn, and their sums meet in LDS. ALONE, where there are
+// enough sums for a wave each: a wave has all the rows of its own 64 columns, of the 256 of
+// a workgroup, and nothing to join (64 rows with 64 adapters of rank 32, 8192 x 8192: 126 us
+// for the backward pass in place of 514).
+template <bool F32, int PC, bool ALONE>
+__global__ __launch_bounds__(ALONE ? kAloneWaves *kWave : kRowWaves *kWave, 2) void adapter_rows_kernel(RowsCall p) {
+    [[maybe_unused]] __shared__ f32x4 sums[ALONE ? 1 : kRowWaves / 2][ALONE ? 1 : 16][kWave];
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block(), q = lane >> 4, j = lane & 15;
     auto div = [](uint32_t &a, uint32_t b) {
         const uint32_t d = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(a / b)), m = a - d * b;
@@ -589,6 +593,10 @@ __global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall
     const bool second = tile >= p.of[0].tiles;
     if (second) tile -= p.of[0].tiles;
     const RowsArgs &o = p.of[second ? 1 : 0];
+    if constexpr (ALONE) {
+        tile = tile * kAloneWaves + w;
+        if (tile * 64 >= o.len) return;
+    }
     const int64_t col = tile * 64 + 4 * j;
     const int r = static_cast<int>(rank0) + 4 * j;
 
@@ -600,25 +608,27 @@ __global__ __launch_bounds__(kRowWaves *kWave) void adapter_rows_kernel(RowsCall
 
     const int64_t c0 = split * p.split_chunks, c1 = min(c0 + p.split_chunks, (p.rows + 63) / 64);
     if (tile * 64 + 64 <= o.len && o.x_stride < (1 << 22))
-        adapter_sums<F32, PC, true>(p, o, g, c0, c1, r, col, acc);
+        adapter_sums<F32, PC, true, !F32 && !ALONE>(p, o, g, ALONE ? c0 : c0 + w, ALONE ? 1 : kRowWaves, c1, r, col, acc);
     else
-        adapter_sums<F32, PC, false>(p, o, g, c0, c1, r, col, acc);
+        adapter_sums<F32, PC, false, !F32 && !ALONE>(p, o, g, ALONE ? c0 : c0 + w, ALONE ? 1 : kRowWaves, c1, r, col, acc);
 
-    // The upper half of the waves hand their sums to the lower half, until wave 0 has them all.
+    if constexpr (!ALONE) {
+        // The upper half of the waves hand their sums to the lower half, until wave 0 has them all.
 #pragma unroll
-    for (int half = kRowWaves / 2; half > 0; half /= 2) {
-        __syncthreads();
-        if (w >= half && w < 2 * half) {
+        for (int half = kRowWaves / 2; half > 0; half /= 2) {
+            __syncthreads();
+            if (w >= half && w < 2 * half) {
 #pragma unroll
-            for (int s = 0; s < 16; ++s) sums[w - half][s][lane] = acc[s / 4][s % 4];
+                for (int s = 0; s < 16; ++s) sums[w - half][s][lane] = acc[s / 4][s % 4];
+            }
+            __syncthreads();
+            if (w < half) {
+#pragma unroll
+                for (int s = 0; s < 16; ++s) acc[s / 4][s % 4] += sums[w][s][lane];
+            }
         }
-        __syncthreads();
-        if (w < half) {
-#pragma unroll
-            for (int s = 0; s < 16; ++s) acc[s / 4][s % 4] += sums[w][s][lane];
-        }
+        if (w != 0) return;
     }
-    if (w != 0) return;
     // Lane (q, j) has ranks rank0 + 16 q + 4 i + s and columns col + t.
     const int64_t all = static_cast<int64_t>(p.rank) * o.len, base = g * all;
     float *part = p.splits > 1 ? o.partial + split * p.adapters * all : nullptr;
@@ -679,8 +689,15 @@ __global__ __launch_bounds__(kBlockThreads) void adapter_rows_join_kernel(const 
     }
 }
 
+// Whether there are as many sums as the GPU holds of these waves, or too few rows to share out
+// (4 rows with 4 adapters of rank 64, 8192 x 8192: 54 us for the backward pass in place of 73).
+bool rows_alone(int64_t rows, int64_t tiles, int64_t adapters, int64_t rank) {
+    return rows <= 128 || tiles * adapters * ceil_div(rank, 64) >= 2048;
+}
+
 // Parts of the rows: as many as give 256 workgroups, of 8 chunks of 64 rows or more.
 int64_t rows_splits(int64_t rows, int64_t tiles, int64_t adapters, int64_t rank) {
+    if (rows_alone(rows, tiles, adapters, rank)) return 1;
     const int64_t chunks = ceil_div(rows, 64), others = tiles * adapters * ceil_div(rank, 64);
     const int64_t want = std::max<int64_t>(256 / std::max<int64_t>(others, 1), 1);
     const int64_t each = std::max<int64_t>(ceil_div(ceil_div(chunks, want), kRowWaves) * kRowWaves, kRowWaves);
@@ -720,8 +737,10 @@ hipError_t launch_adapter_rows(const void *x, int64_t x_stride, const float *up,
     p.split_chunks = ceil_div(ceil_div(rows, 64), p.splits);
     float *second = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
                                               align16(p.splits * adapters * rank * n_in * 4));
-    p.of[0] = RowsArgs{x, x_stride, n_in, up, da, static_cast<float *>(workspace), da ? ceil_div(n_in, 64) : 0};
-    p.of[1] = RowsArgs{dy, dy_stride, n_out, reduced, db, second, db ? ceil_div(n_out, 64) : 0};
+    const bool alone = rows_alone(rows, tiles, adapters, rank);
+    const int64_t columns = alone ? 64 * kAloneWaves : 64;
+    p.of[0] = RowsArgs{x, x_stride, n_in, up, da, static_cast<float *>(workspace), da ? ceil_div(n_in, columns) : 0};
+    p.of[1] = RowsArgs{dy, dy_stride, n_out, reduced, db, second, db ? ceil_div(n_out, columns) : 0};
     p.ids = ids, p.rows = rows, p.adapters = static_cast<int>(adapters), p.rank = static_cast<int>(rank);
     p.ranks = ceil_div(rank, 64), p.out_f32 = w_f32;
     const int64_t each = (p.of[0].tiles + p.of[1].tiles) * p.ranks * p.splits;
@@ -729,12 +748,15 @@ hipError_t launch_adapter_rows(const void *x, int64_t x_stride, const float *up,
     for (int64_t g0 = 0; g0 < adapters; g0 += at_once) {
         p.first = static_cast<int>(g0);
         const unsigned grid = static_cast<unsigned>(each * std::min(adapters - g0, at_once));
+        auto go = [&](auto kernel, auto lonely) {
+            (alone ? lonely : kernel)<<<grid, (alone ? kAloneWaves : kRowWaves) * kWave, 0, stream>>>(p);
+        };
         if (f32)
-            adapter_rows_kernel<true, 3><<<grid, kRowWaves * kWave, 0, stream>>>(p);
+            go(adapter_rows_kernel<true, 3, false>, adapter_rows_kernel<true, 3, true>);
         else if (w_f32)
-            adapter_rows_kernel<false, 3><<<grid, kRowWaves * kWave, 0, stream>>>(p);
+            go(adapter_rows_kernel<false, 3, false>, adapter_rows_kernel<false, 3, true>);
         else
-            adapter_rows_kernel<false, 2><<<grid, kRowWaves * kWave, 0, stream>>>(p);
+            go(adapter_rows_kernel<false, 2, false>, adapter_rows_kernel<false, 2, true>);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     if (p.splits == 1) return hipSuccess;

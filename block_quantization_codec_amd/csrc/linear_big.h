@@ -523,27 +523,31 @@ struct LinBig {
         return __ballot(bad != 0) == 0;
     }
 
-    // What the adapters add to kTogether rows of tiles from row `first` on. Up to four bf16
-    // adapters one after the other, each with all the rows; false, and zeros, where there are more,
-    // or an adapter's infinities or NaNs: then the rows have to be gathered.
+    // How many adapters kTogether rows of tiles from row `first` on have, up to `most` + 1.
+    static __device__ __forceinline__ int count_adapters(const LinArgs &p, int lane, int64_t first, int most) {
+        int id, n = 0;
+        const bool has = adapter_of(p, first + lane, id) && lane < kTogether * 16;
+        for (uint64_t pending = __ballot(has); pending != 0 && n <= most; ++n)
+            pending &= ~__ballot(has && id == __builtin_amdgcn_readlane(id, __builtin_ctzll(pending)));
+        return n;
+    }
+
+    // What the adapters, all of them bf16, add to kTogether rows of tiles from row `first` on, one
+    // after the other, each with all the rows; false, and zeros, where an adapter's infinities or
+    // NaNs forbid it.
     template <int PC>
     static __device__ __forceinline__ bool add_adapters(const LinArgs &p, int lane, int64_t first, int64_t col,
                                                         f32x4 (&d)[kTogether][4]) {
-#pragma unroll
-        for (int m = 0; m < kTogether; ++m)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
         int id;
         const bool has = adapter_of(p, first + lane, id) && lane < kTogether * 16;
         uint64_t pending = __ballot(has);
-        if (pending == 0) return true;
-        bool good = !p.up_f32;
+        bool good = true;
 #pragma unroll 1
-        for (int n = 0; good && pending != 0; ++n) {
+        while (good && pending != 0) {
             const int g = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
             const uint64_t match = __ballot(has && id == g);
             pending &= ~match;
-            good = n < 4 && add_adapter<PC>(p, lane, first, col, g, match, d);
+            good = add_adapter<PC>(p, lane, first, col, g, match, d);
         }
         if (good) return true;
 #pragma unroll
@@ -665,10 +669,9 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
     }
 
     if constexpr (MODE == LinMode::adapted) {
-        // Some rows at a time, through LDS, from which a loop stores them. Adapters are added with
-        // the first part of the contraction. (Written out for all the sums, so that they stay where
+        // Some rows at a time, through LDS, from which a loop stores them. (Written out for all the sums, so that they stay where
         // they are: in a loop that moves them up, they were moved in the products' loop too.)
-        constexpr int kTogether = L::kTogether, PC = PA * PB == 1 ? 2 : 3;
+        constexpr int kTogether = L::kTogether, PC = PA * PB == 1 ? 2 : 3, kMany = 4;
         static_assert(L::kBufs * L::kBytes >= 4 * kTogether * 16 * 64 * 4 && MT % kTogether == 0);
         float *const held = reinterpret_cast<float *>(&tiles[0][0] + w * (kTogether * 16 * 64 * 4));
         __syncthreads();  // no wave reads activations any more
@@ -683,15 +686,21 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
             constexpr int M0 = at.value;
             f32x4 d[kTogether][4];
             bool apart = false;
-            if (place.split == 0) {
+#pragma unroll
+            for (int m = 0; m < kTogether; ++m)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
+            // Many adapters: rows gathered, each part of the contraction a share of them. Few: with
+            // the first part.
+            const int kinds = L::count_adapters(p, lane, first, kMany);
+            int part = 0, parts = 1;
+            if (kinds > kMany || (kinds > 0 && p.up_f32)) {
+                apart = true;
+                part = static_cast<int>(place.split), parts = p.splits;
+            } else if (kinds > 0 && place.split == 0) {
                 apart = !L::template add_adapters<PC>(p, lane, first, col, d);
-                if (apart) adapter_rows<GRAD, true, PC, 4, kTogether * 16, 2, 1>(p, first, col, 0, 1, held);
-            } else {
-#pragma unroll
-                for (int m = 0; m < kTogether; ++m)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) d[m][t] = f32x4{0, 0, 0, 0};
             }
+            if (apart) adapter_rows<GRAD, true, PC, 4, kTogether * 16, 2, 1>(p, first, col, part, parts, held);
 #pragma unroll
             for (int m = 0; m < kTogether; ++m)
 #pragma unroll
