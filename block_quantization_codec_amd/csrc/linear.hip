@@ -5,7 +5,7 @@
 #include <cmath>
 
 #include "../../include/zpp.h"
-#include "linear_device.h"
+#include "linear_tile.h"
 
 namespace zpp {
 
@@ -44,6 +44,7 @@ struct Plan {
     int64_t split_steps;
     int64_t rows; // rows of one launch
     int64_t groups; // and groups
+    int join_steps; // groups in tiles: what a round's parts cost, in steps (linear_tile.h)
 };
 
 // Rows of tiles that `rows` rows make; in groups, each has a last tile of its own, on
@@ -77,13 +78,31 @@ double mid_time(bool in_f32, int mt, int64_t tiles, int64_t splits, int64_t spli
 // times steps times a step's time, and the join. A step takes, with the
 // operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured at
 // 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
-double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t groups, int64_t len, int64_t split_steps) {
+double step_time(int parts, int mt) {
     static constexpr double step_us[3][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0}};
-    const int i = mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3;
-    const double tiles = static_cast<double>(row_tiles(rows, groups, 16 * mt) * ceil_div(len, 256) * splits);
+    return step_us[parts][mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3];
+}
+
+double tile_time(int parts, int mt, int64_t splits, int64_t rows, int64_t len, int64_t split_steps) {
+    const double tiles = static_cast<double>(ceil_div(rows, 16 * mt) * ceil_div(len, 256) * splits);
     // Workgroups that share a CU take about as long as one after the other.
     const double rounds = std::ceil(tiles / kCus);
-    return rounds * static_cast<double>(split_steps) * step_us[parts][i] + join_time(splits, rows, len);
+    return rounds * static_cast<double>(split_steps) * step_time(parts, mt) + join_time(splits, rows, len);
+}
+
+// The same for rows in groups, of which only the tiles past whole rounds are in parts.
+// join_steps: what kRound tiles' parts take in the kernel and the join, in steps; 0 where a round is too
+// short for the join's launch, unless the sizes alone say that there will be parts.
+double group_time(int parts, int mt, int64_t rows, int64_t groups, int64_t len, int64_t steps, int &join_steps) {
+    const double step = step_time(parts, mt), part_us = 16.0 * mt * kTileCols * 8 / 5.5e6;
+    const int64_t tiles = row_tiles(rows, groups, 16 * mt) * ceil_div(len, kTileCols);
+    join_steps = std::max(static_cast<int>(std::ceil(kRound * part_us / step)), 1);
+    const LinTail t = lin_tail(static_cast<uint32_t>(std::min(tiles, kMaxTiles)), static_cast<uint32_t>(steps),
+                               static_cast<uint32_t>(join_steps));
+    if (t.splits == 1 && (steps < 6 || static_cast<double>(steps) * step < 40)) join_steps = 0;
+    const int64_t last = ceil_div(static_cast<int64_t>(t.left) * t.splits, kRound) * t.steps;
+    return static_cast<double>(tiles / kRound * steps + last) * step +
+           (t.splits > 1 ? 4.0 + t.left * t.splits * part_us : 0);
 }
 
 // How many rows, and groups, one launch takes: kMaxTiles workgroups.
@@ -154,11 +173,17 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t group
     double least = 0;
     for (const int mt : {16, 8, 4, 1}) {
         if (mt == 16 && parts > 0) continue;
+        if (groups > 0) {
+            int join_steps;
+            const double t = group_time(parts, mt, rows, groups, len, steps, join_steps);
+            if (p.mt == 0 || t < least) least = t, p.mt = mt, p.splits = 1, p.split_steps = steps, p.join_steps = join_steps;
+            continue;
+        }
         for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
             if (want > 1 && want > steps / 3) break;
             // the pipeline takes steps in pairs
             const int64_t each = want == 1 ? steps : ceil_div(ceil_div(steps, want), 2) * 2, n = ceil_div(steps, each);
-            const double t = tile_time(parts, mt, n, rows, groups, len, each);
+            const double t = tile_time(parts, mt, n, rows, len, each);
             if (p.mt == 0 || t < least) {
                 least = t;
                 p.mt = mt;
@@ -219,6 +244,38 @@ __global__ __launch_bounds__(kBlockThreads) void linear_join_kernel(const float 
                     if (c + t < len) o[t] = static_cast<uint16_t>((t < 2 ? a : b) >> (16 * (t & 1)));
             }
         }
+    }
+}
+
+// The same for groups in tiles: of the tiles that are in parts (linear_tile.h), 16 rows a workgroup.
+__global__ __launch_bounds__(kBlockThreads) void linear_join_tail_kernel(LinArgs p, int tile_rows, int64_t len) {
+    const uint32_t total = group_tiles(p, tile_rows);
+    const LinTail t = group_tail(p, total);
+    if (t.splits == 1) return;
+    const uint32_t slabs = static_cast<uint32_t>(tile_rows) / 16, left = scalar_div(blockIdx.x, slabs);
+    if (left >= t.left) return;
+    LinPlace place = lin_tile(p, 1, t.whole + left, total);
+    int64_t first;
+    if (!group_at<8, 2>(p, tile_rows, static_cast<uint32_t>(place.m0), place.m0, first)) return;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int64_t row = (blockIdx.x - left * slabs) * 16 + wave_in_block() * 4, col = place.col * kTileCols + 4 * lane;
+    const float *from = p.partial + (static_cast<int64_t>(left) * tile_rows + row) * kTileCols + 4 * lane;
+    const int64_t next = static_cast<int64_t>(t.left) * tile_rows * kTileCols;
+    if (place.m0 + row >= p.rows || col >= len) return;
+    f32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f32x4{0, 0, 0, 0};
+#pragma unroll 2
+    for (uint32_t s = 0; s < t.splits; ++s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // rows past the group's last lie in the tile's part all the same
+            v[i] += ld<f32x4>(from + s * next + i * kTileCols);
+    }
+    p.splits = 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float o[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
+        if (place.m0 + row + i < p.rows) store4(p, len, place.m0 + row + i, col, o, 0);
     }
 }
 
@@ -286,6 +343,10 @@ int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int6
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     int64_t bytes = needs_pack(p, in_f32, lda, c_len) ? packed_bytes(p, in_f32, rows, c_len) : 0;
     if (p.splits > 1) bytes += p.splits * std::min(rows, p.rows) * ((len + 3) & ~INT64_C(3)) * 4;
+    if (p.join_steps > 0)
+        bytes += std::min<int64_t>(kParts, (ceil_div(std::min(rows, p.rows), 16 * p.mt) + std::min(groups, p.groups)) *
+                                               ceil_div(len, kTileCols) * p.split_steps) *
+                 16 * p.mt * kTileCols * 4;
     return bytes;
 }
 
@@ -313,6 +374,7 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
                                               (pack ? packed_bytes(plan, in_f32, rows, c_len) : 0));
         p.splits = plan.splits;
         p.split_steps = plan.split_steps;
+        p.join_steps = plan.join_steps;
         p.row0 = r0;
         if (ad) {
             p.low = low + r0 * ad->rank;
@@ -356,6 +418,11 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
                 else
                     e = bits == 4 ? launch_linear_big_group_fwd4(q, parts, plan.mt, stream)
                                   : launch_linear_big_group_fwd8(q, parts, plan.mt, stream);
+                if (e == hipSuccess && q.join_steps > 0) {
+                    linear_join_tail_kernel<<<static_cast<unsigned>((kRound - 1) * plan.mt), kBlockThreads, 0, stream>>>(
+                        q, 16 * plan.mt, len);
+                    e = hipGetLastError();
+                }
                 if (e != hipSuccess) return e;
             }
         } else if (plan.way == Way::few) {

@@ -569,7 +569,7 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
     const int64_t c_len = GRAD ? p.n_out : p.n_in, len = GRAD ? p.n_in : p.n_out;
     LinPlace place;
     if constexpr (MODE == LinMode::grouped) {
-        if (!group_place<BITS, 2>(p, L::kRows, len, place)) return;
+        if (!group_place_tail<BITS, 2>(p, L::kRows, place)) return;
     } else {
         place = lin_place(p, L::kRows);
     }
@@ -746,14 +746,14 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
             float v[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) v[t] = acc[m][t][i] * kCodeScale<BITS>;
-            store4(p, len, row, col, v, place.split);
+            store4<MODE == LinMode::grouped ? kTileCols : 0>(p, len, row, col, v, place.split);
         }
     }
 }
 
 template <LinMode MODE, bool GRAD, int BITS, int PA, int PB, int MT>
 hipError_t launch_linear_big_one(const LinArgs &p, hipStream_t stream) {
-    const int64_t grid = p.row_tiles * p.col_tiles * p.splits;
+    const int64_t grid = p.row_tiles * p.col_tiles * p.splits + (MODE == LinMode::grouped && p.join_steps ? kParts : 0);
     linear_big_kernel<GRAD, BITS, PA, PB, MT, MODE><<<static_cast<unsigned>(grid), kBlockThreads, 0, stream>>>(p);
     return hipGetLastError();
 }

@@ -1,4 +1,4 @@
-// The tiled products on 8-bit codes: y = x W^T.
+// The tiled products on 8-bit codes, a matrix for each group of rows: y = x W^T.
 #include "linear_big.h"
 
 namespace zpp {

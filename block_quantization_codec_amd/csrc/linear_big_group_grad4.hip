@@ -1,4 +1,4 @@
-// The tiled products on 4-bit codes: dx = dy W.
+// The tiled products on 4-bit codes, a matrix for each group of rows: dx = dy W.
 #include "linear_big.h"
 
 namespace zpp {

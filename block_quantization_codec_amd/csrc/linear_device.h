@@ -123,6 +123,7 @@ struct LinArgs {
     const void *up;      // [adapters][out][rank] (y) or [adapters][rank][in] (dx)
     const int32_t *ids;  // [rows]: which adapter, none if it is no number below `adapters`; null: the first, all of them
     int up_f32, rank, adapters;
+    int join_steps;  // rows in groups, in tiles (linear_tile.h): what kRound tiles' parts cost, in steps; 0: no parts
 };
 
 // What a product's rows multiply by: one matrix, that of the row's group, or one

@@ -1,4 +1,6 @@
 // linear_mid_group.hip - y = x W^T on block codes, a matrix for each group of rows (linear_mid.h).
+// Memory bounds it: 32 rows over 16 matrices of 11008 x 4096 int4, 79 to 87 us with the join
+// (the codes of the matrices that have rows: 59 us as a copy).
 #include "linear_mid.h"
 
 namespace zpp {

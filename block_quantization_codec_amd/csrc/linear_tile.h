@@ -27,17 +27,28 @@ struct LinPlace {
     int64_t split, m0, col;
 };
 
+// Divisions leave their results in vector registers; read back, they and all that
+// follows from them are scalar. (A launch has fewer than 2^24 workgroups.)
+__device__ __forceinline__ uint32_t scalar_div(uint32_t a, uint32_t b) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(a / b));
+}
+
+// Tile number `tile` of `row_tiles` rows of tiles of `rows` rows.
+__device__ __forceinline__ LinPlace lin_tile(const LinArgs &p, int rows, uint32_t tile, uint32_t row_tiles) {
+    const uint32_t col_tiles = static_cast<uint32_t>(p.col_tiles);
+    const uint32_t g = scalar_div(tile, 8 * col_tiles), in_g = min(8u, row_tiles - g * 8), at = tile - g * 8 * col_tiles;
+    const uint32_t col = scalar_div(at, in_g), row = g * 8 + (at - col * in_g);
+    return LinPlace{0, static_cast<int64_t>(row) * rows, col};
+}
+
 // `grid` workgroups, a launch's or its first ones, cover `row_tiles` rows of tiles of `rows` rows.
 __device__ __forceinline__ LinPlace lin_place_of(const LinArgs &p, int rows, uint32_t grid, uint32_t row_tiles) {
-    // A launch has fewer than 2^24 workgroups. Divisions leave their results in
-    // vector registers; read back, they and all that follows from them are scalar.
-    auto div = [](uint32_t a, uint32_t b) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(a / b)); };
     const uint32_t id = static_cast<uint32_t>(xcd_block(blockIdx.x, grid));
-    const uint32_t col_tiles = static_cast<uint32_t>(p.col_tiles);
-    const uint32_t split = div(id, row_tiles * col_tiles), tile = id - split * (row_tiles * col_tiles);
-    const uint32_t g = div(tile, 8 * col_tiles), in_g = min(8u, row_tiles - g * 8), at = tile - g * 8 * col_tiles;
-    const uint32_t col = div(at, in_g), row = g * 8 + (at - col * in_g);
-    return LinPlace{split, static_cast<int64_t>(row) * rows, col};
+    const uint32_t tiles = row_tiles * static_cast<uint32_t>(p.col_tiles);
+    const uint32_t split = scalar_div(id, tiles);
+    LinPlace place = lin_tile(p, rows, id - split * tiles, row_tiles);
+    place.split = split;
+    return place;
 }
 
 __device__ __forceinline__ LinPlace lin_place(const LinArgs &p, int rows) {
@@ -61,52 +72,151 @@ __device__ __forceinline__ uint32_t scan_add(uint32_t v) {
     return v;
 }
 
-// The tile of a launch over groups: which group a workgroup's rows are of follows
-// from the offsets, which only the device knows. Every wave counts the groups' tiles
-// (64 groups at a time); workgroups past the last one have nothing to do, and the
-// others are dealt out as if the launch had no more. `p` becomes the group's own product.
+// A launch over groups: which group a tile's rows are of follows from the offsets, which
+// only the device knows. Every wave counts the groups' tiles, 64 groups at a time.
 // Offsets are taken within the launch's rows and tiles, whatever they hold.
-template <int BITS, int ELEM>
-__device__ __forceinline__ bool group_place(LinArgs &p, int tile_rows, int64_t len, LinPlace &place) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int most = static_cast<int>(p.row_tiles);
+struct GroupRows {
+    int begin, count;
+    uint32_t tiles;
+};
+
+__device__ __forceinline__ GroupRows group_rows(const LinArgs &p, int tile_rows, int e) {
     auto clip = [&](int32_t v) {
         return static_cast<int>(min(max(static_cast<int64_t>(v) - p.row0, INT64_C(0)), p.rows));
     };
-    int begin, count;
-    auto tiles_of = [&](int e) {
-        const int at = min(e, p.groups - 1);
-        begin = clip(p.offsets[at]);
-        count = e < p.groups ? max(clip(p.offsets[at + 1]) - begin, 0) : 0;
-        return static_cast<uint32_t>(min((count + tile_rows - 1) / tile_rows, most));
-    };
-    auto last = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63)); };
+    const int at = min(e, p.groups - 1);
+    GroupRows o;
+    o.begin = clip(p.offsets[at]);
+    o.count = e < p.groups ? max(clip(p.offsets[at + 1]) - o.begin, 0) : 0;
+    o.tiles = static_cast<uint32_t>(min((o.count + tile_rows - 1) / tile_rows, static_cast<int>(p.row_tiles)));
+    return o;
+}
+
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+// The groups' rows of tiles, together.
+__device__ __forceinline__ uint32_t group_tiles(const LinArgs &p, int tile_rows) {
+    const int lane = threadIdx.x & (kWave - 1);
     uint32_t total = 0;
-    for (int e = 0; e < p.groups; e += kWave) total = min(total + last(scan_add(tiles_of(e + lane))), static_cast<uint32_t>(most));
-    const uint32_t grid = total * static_cast<uint32_t>(p.col_tiles * p.splits);
-    if (blockIdx.x >= grid) return false;
-    place = lin_place_of(p, 1, grid, total);
-    const uint32_t tile = static_cast<uint32_t>(place.m0);
+    for (int e = 0; e < p.groups; e += kWave)
+        total = min(total + last_lane(scan_add(group_rows(p, tile_rows, e + lane).tiles)),
+                    static_cast<uint32_t>(p.row_tiles));
+    return total;
+}
+
+// The group that row of tiles `tile` is of: `p` becomes its own product, m0 is the tile's
+// first row in it, `first` the group's first row of the launch's.
+template <int BITS, int ELEM>
+__device__ __forceinline__ bool group_at(LinArgs &p, int tile_rows, uint32_t tile, int64_t &m0, int64_t &first) {
+    const int lane = threadIdx.x & (kWave - 1);
     uint32_t before = 0;
     for (int e = 0; e < p.groups; e += kWave) {
-        const uint32_t own = tiles_of(e + lane), upto = before + scan_add(own);
+        const GroupRows o = group_rows(p, tile_rows, e + lane);
+        const uint32_t own = o.tiles, upto = before + scan_add(own);
         const uint64_t past = __ballot(upto > tile);
         if (past != 0) {
             const int l = __builtin_ctzll(past);
             auto read = [&](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l)); };
-            const int64_t group = e + l, first = read(static_cast<uint32_t>(begin)), weights = p.n_out * p.n_in;
-            place.m0 = static_cast<int64_t>(tile - (read(upto) - read(own))) * tile_rows;
+            const int64_t group = e + l, weights = p.n_out * p.n_in;
+            first = read(static_cast<uint32_t>(o.begin));
+            m0 = static_cast<int64_t>(tile - (read(upto) - read(own))) * tile_rows;
             p.a = static_cast<const uint8_t *>(p.a) + first * p.lda * ELEM;
-            p.rows = read(static_cast<uint32_t>(count));
+            p.rows = read(static_cast<uint32_t>(o.count));
             p.codes += group * (weights * BITS / 8);
             p.scales += group * (weights >> p.log2b);
             p.out = static_cast<uint8_t *>(p.out) + first * p.ldo * (p.out_f32 ? 4 : 2);
-            p.partial += first * ((len + 3) & ~INT64_C(3));
             return true;
         }
-        before = last(upto);
+        before = last_lane(upto);
     }
     return false;
+}
+
+// A workgroup's tile, the contraction in p.splits parts. Workgroups past the groups' tiles have
+// nothing to do, and the others are dealt out as if the launch had no more.
+template <int BITS, int ELEM>
+__device__ __forceinline__ bool group_place(LinArgs &p, int tile_rows, int64_t len, LinPlace &place) {
+    const uint32_t total = group_tiles(p, tile_rows);
+    const uint32_t grid = total * static_cast<uint32_t>(p.col_tiles * p.splits);
+    if (blockIdx.x >= grid) return false;
+    place = lin_place_of(p, 1, grid, total);
+    int64_t first;
+    if (!group_at<BITS, ELEM>(p, tile_rows, static_cast<uint32_t>(place.m0), place.m0, first)) return false;
+    p.partial += first * ((len + 3) & ~INT64_C(3));
+    return true;
+}
+
+// The tiles in rounds of one a CU: whole rounds take the whole contraction a tile, those
+// that are left over, which would leave CUs idle for as long, take it in parts. How
+// many follows from what is left, which only the device knows: the least steps, the
+// parts' writing, reading and joining counted too. 8 groups with 4096 rows of 11008 x 4096,
+// backward: 407 us, 463 with the contraction in 2 parts for every tile.
+constexpr uint32_t kRound = 256;  // CUs
+constexpr uint32_t kParts = 512;  // tiles of parts, at most
+
+struct LinTail {
+    uint32_t whole, left;  // tiles
+    uint32_t splits;       // of those that are left; 1: they are no different
+    uint32_t steps;        // of a part
+};
+
+__host__ __device__ __forceinline__ LinTail lin_tail(uint32_t tiles, uint32_t steps, uint32_t join_steps) {
+    LinTail o{tiles / kRound * kRound, tiles % kRound, 1, steps};
+    if (o.left == 0 || join_steps == 0) return o;
+    uint32_t least = steps;
+    auto consider = [&](uint32_t want) {
+        if (want < 2 || want > steps / 3 || want * o.left > kParts) return;
+        const uint32_t each = ((steps + want - 1) / want + 1) & ~1u;  // the pipeline takes steps in pairs
+        const uint32_t n = (steps + each - 1) / each, parts = n * o.left;
+        const uint32_t cost = (parts + kRound - 1) / kRound * each + join_steps * parts / kRound;
+        if (cost < least) least = cost, o.splits = n, o.steps = each;
+    };
+    for (uint32_t want = 2; want <= 4; ++want) consider(want);
+    consider(kRound / o.left);
+    consider(kRound / o.left / 2);
+    return o;
+}
+
+__device__ __forceinline__ LinTail group_tail(const LinArgs &p, uint32_t row_tiles) {
+    LinTail o = lin_tail(row_tiles * static_cast<uint32_t>(p.col_tiles), static_cast<uint32_t>(p.split_steps),
+                         static_cast<uint32_t>(p.join_steps));
+    o.splits = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(o.splits));
+    o.steps = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(o.steps));
+    return o;
+}
+
+// A workgroup's tile; `p` becomes the group's own product, in as many parts as the tile has.
+// A part's sums lie at [part][tile that is left][row of the tile][kTileCols].
+template <int BITS, int ELEM>
+__device__ __forceinline__ bool group_place_tail(LinArgs &p, int tile_rows, LinPlace &place) {
+    const uint32_t total = group_tiles(p, tile_rows);
+    const LinTail t = group_tail(p, total);
+    const uint32_t whole = t.splits == 1 ? t.whole + t.left : t.whole, parts = t.splits == 1 ? 0 : t.left * t.splits;
+    if (blockIdx.x >= whole + parts) return false;
+    uint32_t tile, split = 0, left = 0;
+    const bool part = blockIdx.x >= whole;
+    if (part) {
+        const uint32_t id = static_cast<uint32_t>(xcd_block(blockIdx.x - whole, parts));
+        split = scalar_div(id, t.left);
+        left = id - split * t.left;
+        tile = whole + left;
+    } else {
+        tile = static_cast<uint32_t>(xcd_block(blockIdx.x, whole));
+    }
+    place = lin_tile(p, 1, tile, total);
+    place.split = split;
+    int64_t first;
+    if (!group_at<BITS, ELEM>(p, tile_rows, static_cast<uint32_t>(place.m0), place.m0, first)) return false;
+    p.splits = 1;
+    if (part) {
+        p.splits = static_cast<int>(t.splits);
+        p.split_steps = t.steps;
+        p.split_rows = static_cast<int64_t>(t.left) * tile_rows;
+        p.partial += (static_cast<int64_t>(left) * tile_rows - place.m0 - place.col) * kTileCols;
+    }
+    return true;
 }
 
 // A tile of 16*MT rows x 64 activations in LDS, in PA planes of bf16 parts.
@@ -188,12 +298,14 @@ struct LinTile {
     }
 };
 
-// 4 neighbouring results of a row, or a split's sums of them.
+// 4 neighbouring results of a row, or a split's sums of them. LDP: between rows of those, if it is
+// not the result's width.
+template <int LDP = 0>
 __device__ __forceinline__ void store4(const LinArgs &p, int64_t len, int64_t row, int64_t col,
                                               const float (&v)[4], int64_t split) {
     if (p.splits > 1) {  // columns of the sums are padded to whole fours
-        const int64_t ldp = (len + 3) & ~INT64_C(3);
-        if (col < ldp)
+        const int64_t width = (len + 3) & ~INT64_C(3), ldp = LDP ? LDP : width;
+        if (col < width)
             st<f32x4>(p.partial + (split * p.split_rows + row) * ldp + col, f32x4{v[0], v[1], v[2], v[3]});
         return;
     }

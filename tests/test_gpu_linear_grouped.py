@@ -73,6 +73,20 @@ def test_many_tiles_and_split_sums(z, grad):
             assert torch.equal(got, want), (counts, n, k, block)
 
 
+@pytest.mark.parametrize("counts", [[300, 0, 70, 129], [1, 2, 3], [900, 257], [65] * 9, [2000], [1290, 800, 1]],
+                         ids=lambda c: "-".join(map(str, c[:4])))
+@pytest.mark.parametrize("grad", [False, True], ids=["y", "dx"])
+def test_whole_rounds_of_tiles_and_what_is_left(z, grad, counts):
+    """Tiles past whole rounds of the GPU take the contraction in parts, whose number follows from the offsets."""
+    for long, (across, block) in [(1024, (16384, 128)), (1087 if grad else 1088, (7904 if grad else 7903, 32))]:
+        n, k = (long, across) if grad else (across, long)
+        for types in ((BF, BF), (F32, F32), (BF, F32)) if grad else ((BF, BF), (F32, F32)):
+            if types[0] == F32 and sum(counts) > 1500:
+                continue
+            got, want, gap = case(z, 4, grad, counts, n, k, 8, block, *types, first=1, tail=2, pad_out=8)
+            assert torch.equal(got, want) and bool((gap == 77).all()), (long, across, types)
+
+
 @pytest.mark.parametrize("grad", [False, True], ids=["y", "dx"])
 def test_row_strides_leave_gaps_alone(z, grad):
     for it, ot in [(BF, BF), (F32, F32)]:
