@@ -9,7 +9,9 @@
  * requantize step between the two hops of its hierarchical all-to-all).
  * Next to it stand the operators that use those weights on the GPU that holds
  * their codes: linear products and their input gradient straight from codes
- * and scales, and layer norm, forward and backward.
+ * and scales, layer norm, RMS norm (with a residual's addition and codes of its
+ * result), low-rank adapters beside a product, and products of rows grouped by
+ * weight matrix, all forward and backward.
  * It moves no data between GPUs: the caller's collectives do that.
  *
  * Conventions shared by every entry point
