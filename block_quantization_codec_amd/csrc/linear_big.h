@@ -559,20 +559,12 @@ struct LinBig {
 };
 
 template <bool GRAD, int BITS, int PA, int PB, int MT, LinMode MODE>
-__global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1 : 2) void linear_big_kernel(
-    LinArgs p) {
+__device__ __forceinline__ void linear_big_tile(const LinArgs &p, const LinPlace &place,
+                                                uint8_t (*tiles)[LinBig<GRAD, BITS, PA, PB, MT>::kBytes]) {
     using L = LinBig<GRAD, BITS, PA, PB, MT>;
-    __shared__ __attribute__((aligned(128))) uint8_t tiles[L::kBufs][L::kBytes];
-
     const int lane = threadIdx.x & (kWave - 1), w = wave_in_block();
     const int q = lane >> 4;
     const int64_t c_len = GRAD ? p.n_out : p.n_in, len = GRAD ? p.n_in : p.n_out;
-    LinPlace place;
-    if constexpr (MODE == LinMode::grouped) {
-        if (!group_place_tail<BITS, 2>(p, L::kRows, place)) return;
-    } else {
-        place = lin_place(p, L::kRows);
-    }
     const int64_t m0 = place.m0, wave_col = place.col * kTileCols + w * 64, col = wave_col + (lane & 15) * 4;
     const typename L::At at = L::place(p, m0, wave_col);
 
@@ -749,6 +741,30 @@ __global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1
             store4<MODE == LinMode::grouped ? kTileCols : 0>(p, len, row, col, v, place.split);
         }
     }
+}
+
+template <bool GRAD, int BITS, int PA, int PB, int MT, LinMode MODE>
+__global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1 : 2) void linear_big_kernel(
+    LinArgs p) {
+    using L = LinBig<GRAD, BITS, PA, PB, MT>;
+    __shared__ __attribute__((aligned(128))) uint8_t tiles[L::kBufs][L::kBytes];
+    LinPlace place;
+    if constexpr (MODE == LinMode::grouped) {
+        if (!group_place_tail<BITS, 2>(p, L::kRows, place)) return;
+        // A group's last tile is half empty or more as often as not. 16 groups of 300 rows, int4, 11008 x
+        // 4096: 612 us so, 636 with 256-row tiles alone (a step's codes cost as much in either).
+        if constexpr (MT == 16) {
+            using S = LinBig<GRAD, BITS, PA, PB, 8>;
+            static_assert(S::kBufs * S::kBytes <= L::kBufs * L::kBytes);
+            if (p.rows - place.m0 <= S::kRows) {
+                linear_big_tile<GRAD, BITS, PA, PB, 8, MODE>(p, place, reinterpret_cast<uint8_t(*)[S::kBytes]>(&tiles[0][0]));
+                return;
+            }
+        }
+    } else {
+        place = lin_place(p, L::kRows);
+    }
+    linear_big_tile<GRAD, BITS, PA, PB, MT, MODE>(p, place, tiles);
 }
 
 template <LinMode MODE, bool GRAD, int BITS, int PA, int PB, int MT>
