@@ -1,6 +1,6 @@
 // The tiled products on 8-bit codes, a matrix for each group of rows: dx = dy W.
 // 4096 rows over 8 matrices of 11008 x 4096 with unequal shares: 407 us, 14 of them the join.
-// Matrix instructions bound it; each group's last tile is half empty.
+// Matrix instructions and the codes' conversion bound it; last tiles are not full.
 #include "linear_big.h"
 
 namespace zpp {
