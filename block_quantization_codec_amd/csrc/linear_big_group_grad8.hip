@@ -1,5 +1,5 @@
 // The tiled products on 8-bit codes, a matrix for each group of rows: dx = dy W.
-// 4096 rows over 8 matrices of 11008 x 4096 with unequal shares: 407 us, 14 of them the join.
+// 4096 rows over 8 matrices of 11008 x 4096 with unequal shares: 394 to 414 us, 14 of them the join.
 // Matrix instructions and the codes' conversion bound it; last tiles are not full.
 #include "linear_big.h"
 
