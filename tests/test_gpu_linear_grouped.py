@@ -236,6 +236,43 @@ def test_a_captured_pass_replays_with_new_groups(z):
             at = min(at + c, rows)
 
 
+def test_a_replay_takes_the_parts_that_its_groups_leave(z):
+    """One captured pass, whose groups leave from no tile to nearly a round of them for parts; bad offsets too."""
+    g = gen(14)
+    e, n, k, rows = 4, 1024, 16384, 900
+    codes, scales, w = weights(g, e * n, k, 4, 128, lambda m: torch.ones(m, device="cuda"))
+    w = w.view(e, n, k)
+    dy, o = torch.zeros(rows, n, dtype=BF, device="cuda"), ascending([225] * e)
+    dx = torch.empty(rows, k, dtype=BF, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        z.linear_grouped_grad(dy, o, codes, scales, 4, 128, k, out=dx)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z.linear_grouped_grad(dy, o, codes, scales, 4, 128, k, out=dx)
+    for counts in ([225] * e, [900, 0, 0, 0], [0, 0, 0, 1], [256, 256, 256, 132], [1, 0, 300, 2], [0] * e, [64] * e):
+        dy.copy_(torch.randint(-4, 5, dy.shape, generator=g, device="cuda"))
+        o.copy_(ascending(counts))
+        dx.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for i, c in enumerate(counts):
+            assert torch.equal(dx[at:at + c], (dy[at:at + c].double() @ w[i]).to(BF)), (counts, i)
+            at += c
+        assert bool((dx[at:] == 9).all()), counts
+    o.copy_(torch.tensor([700, -5, 2_000_000_000, 30, 890], dtype=torch.int32))
+    graph.replay()  # rows of no group or of two hold what they hold; nothing outside is touched
+    torch.cuda.synchronize()
+    o.copy_(ascending([225] * e))
+    graph.replay()
+    torch.cuda.synchronize()
+    for i in range(e):
+        here = slice(225 * i, 225 * i + 225)
+        assert torch.equal(dx[here], (dy[here].double() @ w[i]).to(BF))
+
+
 def test_on_a_stream_that_is_behind(z):
     g = gen(8)
     n, k = 4160, 256
