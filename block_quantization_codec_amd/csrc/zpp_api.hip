@@ -570,9 +570,8 @@ zpp_status zpp_linear_adapters_grad(const void *dy, int32_t dy_dtype, int64_t dy
     if (bits != 8 && bits != 4) return ZPP_ERR_ARG;
     if (!is_linear_size(rows, out_features, in_features) || !ad.sizes(out_features, in_features)) return ZPP_ERR_ARG;
     if (!is_pow2_block(block) || out_features * in_features % block != 0) return ZPP_ERR_ARG;
-    if (!is_stride(dy_stride, rows, out_features) || !is_stride(x_stride, rows, in_features) ||
-        !is_stride(dx_stride, rows, in_features))
-        return ZPP_ERR_ARG;
+    if (!is_stride(dy_stride, rows, out_features) || !is_stride(dx_stride, rows, in_features)) return ZPP_ERR_ARG;
+    if (x && !is_stride(x_stride, rows, in_features)) return ZPP_ERR_ARG;
     if (rows == 1) dx_stride = in_features;
     const int64_t need = zpp::linear_adapters_workspace(true, dy_dtype == ZPP_FP32, dy_stride, dx_dtype == ZPP_FP32,
                                                         rows, out_features, in_features, adapters, rank);

@@ -429,8 +429,8 @@ zpp_status zpp_linear_adapters(const void *x, int32_t x_dtype, int64_t x_stride,
  * inputs give the same bits. An adapter without rows gets zeros.
  *
  *   dy        in   rows of out_features elements of dy_dtype, as in zpp_linear_blocks_grad
- *   x         in   rows of in_features elements of dy_dtype, 16-B aligned, x_stride (any) between rows, as in the
- *                  forward pass; may be NULL without da
+ *   x         in   rows of in_features elements of dy_dtype, 16-B aligned, x_stride (any of in_features or more)
+ *                  between rows, as in the forward pass; may be NULL without da; its stride is then ignored
  *   reduced   in   as the forward pass wrote it; may be NULL without db
  *   a, b, ab_dtype, adapters, rank, ids, scaling
  *             in   as in the forward pass

@@ -76,6 +76,14 @@ def test_grad_argument_errors(z):
     assert _grad(z, **nothing) == z.ZPP_OK
 
 
+def test_grad_without_x_takes_any_stride_of_it(z):
+    for xs in (0, -1, 120, 1 << 41):
+        # past the arguments: dx on dy is what is refused
+        assert _grad(z, x=None, da=None, xs=xs, dx=A) == z.ZPP_ERR_OVERLAP, xs
+        assert _grad(z, da=None, xs=xs, dx=A) == z.ZPP_ERR_ARG, xs
+        assert _grad(z, x=None, xs=xs) == z.ZPP_ERR_NULL, xs
+
+
 def test_workspace_is_asked_for_and_checked(z):
     w = z.zpp_linear_adapters_workspace
     need = w(0, 1, 8192, 1, 16, 8192, 8192, 2, 64)
