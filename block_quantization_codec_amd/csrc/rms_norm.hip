@@ -178,8 +178,8 @@ __device__ __forceinline__ void quantize_chunks(const RmsArgs &p, int64_t row, c
     }
 }
 
-// HOLD: the weights stay in registers over the rows (else they are read again for each).
-template <bool F32, bool WHOLE, int T, int N, bool HOLD, bool QUANT>
+// The weights stay in registers over the rows.
+template <bool F32, bool WHOLE, int T, int N, bool QUANT>
 __global__ __launch_bounds__(group(T)) void rms_kernel(RmsArgs p) {
     using H = Held<F32, WHOLE, T, N>;
     constexpr int V = H::V;
@@ -190,20 +190,17 @@ __global__ __launch_bounds__(group(T)) void rms_kernel(RmsArgs p) {
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kUnits + (kUnits > 1 ? wave_in_block() : 0);
     if (kUnits > 1 && unit >= p.rows) return;
     const float inv = 1.0f / static_cast<float>(p.width);
-    float w[HOLD ? N : 1][V];
+    float w[N][V];
     H x, next, next_res;
     auto fetch = [&](int64_t r) {
         next.load(p.x, r * p.x_stride, p.width);
         if (p.res) next_res.load(p.res, r * p.res_stride, p.width);
     };
     fetch(unit);
-    if constexpr (HOLD) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            load_w<V, WHOLE>(p.weight, p.w_f32, H::column(i) < p.width ? H::column(i) : 0, p.width, 1.0f, w[i]);
-    }
+    for (int i = 0; i < N; ++i)
+        load_w<V, WHOLE>(p.weight, p.w_f32, H::column(i) < p.width ? H::column(i) : 0, p.width, 1.0f, w[i]);
     for (int64_t r = unit; r < p.rows; r += p.units) {
-        if constexpr (!HOLD) asm volatile("" ::: "memory");  // the weights' loads stay in the loop
         x = next;
         if (p.res) {
 #pragma unroll
@@ -229,11 +226,9 @@ __global__ __launch_bounds__(group(T)) void rms_kernel(RmsArgs p) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int64_t c = H::column(i);
-            constexpr int one = HOLD ? 1 : 0, own = QUANT ? 1 : 0;
-            if constexpr (!HOLD)
-                load_w<V, WHOLE>(p.weight, p.w_f32, c < p.width ? c : 0, p.width, 1.0f, w[0]);
+            constexpr int own = QUANT ? 1 : 0;
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[own * i][j] = x.at(i, j) * rstd * w[one * i][j];
+            for (int j = 0; j < V; ++j) y[own * i][j] = x.at(i, j) * rstd * w[i][j];
             if (p.y && c < p.width) store_v<F32, V, WHOLE>(p.y, r * p.y_stride + c, p.width - c, y[own * i]);
         }
         if constexpr (QUANT) quantize_chunks<T, N, V>(p, r, y, maxima);
@@ -471,15 +466,15 @@ hipError_t launch_rms(RmsArgs p, hipStream_t stream) {
         kernel<<<static_cast<unsigned>(p.units / units_of_group), threads, 0, stream>>>(p);
     };
     if (h <= 512)
-        go(rms_kernel<F32, WHOLE, 64, 8 / V, true, QUANT>, 4, 256, 8192);
+        go(rms_kernel<F32, WHOLE, 64, 8 / V, QUANT>, 4, 256, 8192);
     else if (h <= 2048)
-        go(rms_kernel<F32, WHOLE, 256, 8 / V, true, QUANT>, 1, 256, 2048);
+        go(rms_kernel<F32, WHOLE, 256, 8 / V, QUANT>, 1, 256, 2048);
     else if (h <= 4096)
-        go(rms_kernel<F32, WHOLE, 256, 16 / V, true, QUANT>, 1, 256, 4096);
+        go(rms_kernel<F32, WHOLE, 256, 16 / V, QUANT>, 1, 256, 4096);
     else if (h <= 8192)
-        go(rms_kernel<F32, WHOLE, 512, 16 / V, true, QUANT>, 1, 512, 2048);
+        go(rms_kernel<F32, WHOLE, 512, 16 / V, QUANT>, 1, 512, 2048);
     else
-        go(rms_kernel<F32, WHOLE, 1024, 16 / V, true, QUANT>, 1, 1024, 512);
+        go(rms_kernel<F32, WHOLE, 1024, 16 / V, QUANT>, 1, 1024, 512);
     return hipGetLastError();
 }
 
