@@ -695,19 +695,32 @@ __global__ __launch_bounds__(kBlockThreads) void adapter_rows_join_kernel(const 
     }
 }
 
-// Whether there are as many sums as the GPU holds of these waves, or too few rows to share out
-// (4 rows with 4 adapters of rank 64, 8192 x 8192: 54 us for the backward pass in place of 73).
-bool rows_alone(int64_t rows, int64_t tiles, int64_t adapters, int64_t rank) {
-    return rows <= 128 || tiles * adapters * ceil_div(rank, 64) >= 2048;
-}
+// How a call's sums are shared out: a wave each (alone), or a workgroup each with the rows in parts, as
+// many as give 256 workgroups, of 8 chunks of 64 rows or more.
+//
+// The estimated time decides, in microseconds: rounds of the waves (2048) or workgroups (256) that the GPU
+// holds at once, times the chunks that a wave walks, at 0.26 a chunk and 3.3 more if all of its rows are the
+// adapter's, and 5 to begin and to join. Alone against shared, bf16, measured: 4096 rows of 8192 and 8192 columns, one
+// adapter of rank 64, 214 us against 50, 16 of them 77 against 147, 128 of rank 16 250 against 887; 8192 and 28672
+// columns, one of rank 256, 434 against 296 with 4096 rows, 63 against 86 with 512; 192 rows of 8192 and 8192, one of
+// rank 64, 16.1 against 12.5, four 11.8 against 33.5. Of 70 such cases the estimate was wrong in two, by 3 and 4%.
+struct RowsPlan {
+    bool alone;
+    int64_t splits;  // parts of the rows
+};
 
-// Parts of the rows: as many as give 256 workgroups, of 8 chunks of 64 rows or more.
-int64_t rows_splits(int64_t rows, int64_t tiles, int64_t adapters, int64_t rank) {
-    if (rows_alone(rows, tiles, adapters, rank)) return 1;
-    const int64_t chunks = ceil_div(rows, 64), others = tiles * adapters * ceil_div(rank, 64);
-    const int64_t want = std::max<int64_t>(256 / std::max<int64_t>(others, 1), 1);
+RowsPlan rows_plan(int64_t rows, int64_t tiles, int64_t adapters, int64_t rank) {
+    const int64_t chunks = ceil_div(rows, 64), sums = tiles * adapters * ceil_div(rank, 64);
+    const int64_t want = std::max<int64_t>(256 / sums, 1);
     const int64_t each = std::max<int64_t>(ceil_div(ceil_div(chunks, want), kRowWaves) * kRowWaves, kRowWaves);
-    return std::max<int64_t>(ceil_div(chunks, each), 1);
+    const int64_t splits = std::max<int64_t>(ceil_div(chunks, each), 1);
+    const double chunk_us = 0.26 + 3.3 / static_cast<double>(adapters);
+    auto time = [&](int64_t rounds, int64_t walked) {
+        return static_cast<double>(rounds) * (static_cast<double>(walked) * chunk_us + 5);
+    };
+    if (time(ceil_div(sums, 2048), chunks) <= time(ceil_div(sums * splits, 256), ceil_div(chunks, kRowWaves * splits)))
+        return RowsPlan{true, 1};
+    return RowsPlan{false, splits};
 }
 
 int64_t align16(int64_t bytes) { return (bytes + 15) & ~INT64_C(15); }
@@ -728,7 +741,7 @@ hipError_t launch_down_any(bool grad, const void *x, bool x_f32, int64_t x_strid
 }
 
 int64_t rows_workspace(int64_t rows, int64_t n_out, int64_t n_in, int64_t adapters, int64_t rank) {
-    const int64_t splits = rows_splits(rows, ceil_div(n_in, 64) + ceil_div(n_out, 64), adapters, rank);
+    const int64_t splits = rows_plan(rows, ceil_div(n_in, 64) + ceil_div(n_out, 64), adapters, rank).splits;
     return splits > 1 ? align16(splits * adapters * rank * n_in * 4) + align16(splits * adapters * rank * n_out * 4) : 0;
 }
 
@@ -738,12 +751,12 @@ hipError_t launch_adapter_rows(const void *x, int64_t x_stride, const float *up,
                                void *workspace, hipStream_t stream) {
     RowsCall p{};
     // planned for both, so that each comes out the same without the other
-    const int64_t tiles = ceil_div(n_in, 64) + ceil_div(n_out, 64);
-    p.splits = static_cast<int>(rows_splits(rows, tiles, adapters, rank));
+    const RowsPlan plan = rows_plan(rows, ceil_div(n_in, 64) + ceil_div(n_out, 64), adapters, rank);
+    p.splits = static_cast<int>(plan.splits);
     p.split_chunks = ceil_div(ceil_div(rows, 64), p.splits);
     float *second = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
                                               align16(p.splits * adapters * rank * n_in * 4));
-    const bool alone = rows_alone(rows, tiles, adapters, rank);
+    const bool alone = plan.alone;
     const int64_t columns = alone ? 64 * kAloneWaves : 64;
     p.of[0] = RowsArgs{x, x_stride, n_in, up, da, static_cast<float *>(workspace), da ? ceil_div(n_in, columns) : 0};
     p.of[1] = RowsArgs{dy, dy_stride, n_out, reduced, db, second, db ? ceil_div(n_out, columns) : 0};

@@ -210,6 +210,15 @@ def test_many_tiles_and_split_sums(z, rows, n, k, kind, types):
     Case(9, rows, n, k, 4, 32, 3, 64, kind, xt, wt, False, z).check_real(dtype)
 
 
+@pytest.mark.parametrize("rows,n,k,adapters,rank,kind", [(2100, 24640, 8224, 1, 256, "null"), (192, 4128, 4096, 4, 64, "any"),
+                                                         (150, 4096, 4128, 4, 16, "runs"), (192, 1000, 512, 4, 64, "any"),
+                                                         (1600, 2080, 2080, 32, 16, "any")])
+def test_gradients_of_adapters_by_waves_and_by_workgroups(z, rows, n, k, adapters, rank, kind):
+    """Sizes on either side of the estimate that shares the adapters' gradients out: many sums and many rows, few
+    sums and few rows."""
+    Case(rows, rows, n, k, 4, 32, adapters, rank, kind, BF, BF, True, z).check_whole(F32)
+
+
 def test_without_scaling_and_in_more_dimensions(z):
     c = Case(2, 12, 96, 128, 4, 32, 3, 16, "any", BF, BF, True, z, scaled=False)
     c.check_whole(BF)
