@@ -172,6 +172,55 @@ def test_offsets_that_do_not_ascend_stay_in_bounds(z, grad):
         assert not bool((big[32:-32] == 77).all())
 
 
+@pytest.mark.parametrize("types", [(BF, BF), (BF, F32), (F32, F32)], ids=["bb", "bf", "ff"])
+@pytest.mark.parametrize("grad", [False, True], ids=["y", "dx"])
+def test_no_element_of_a_non_finite_row_is_finite(z, grad, types):
+    """Each of the rows by itself, and every element: a code of zero makes a NaN of an infinity."""
+    g = gen(15)
+    n, k = 96, 160
+    codes, scales, _ = weights(g, 3 * n, k, 4, 32, lambda m: torch.ones(m, device="cuda"))
+    f = z.linear_grouped_grad if grad else z.linear_grouped
+    for counts in ([2, 3, 1], [30, 70, 100], [300, 10, 90]):
+        rows, o = sum(counts), ascending(counts)
+        a = torch.randint(-4, 5, (rows, n if grad else k), generator=g, device="cuda").to(types[0])
+        for row, value in ((1, float("inf")), (counts[0], float("-inf")), (rows - 1, float("nan"))):
+            bad = a.clone()
+            bad[row, 7] = value
+            got = f(bad, o, codes, scales, 4, 32, k if grad else n, dtype=types[1])
+            finite = torch.isfinite(got.float())
+            assert not bool(finite[row].any()), (counts, row)
+            assert bool(finite[:row].all()) and bool(finite[row + 1:].all()), (counts, row)
+
+
+@pytest.mark.parametrize("grad", [False, True], ids=["y", "dx"])
+def test_results_after_offsets_that_do_not_ascend(z, grad):
+    """A call with such offsets leaves nothing behind: the next one's results are its own, in a buffer filled anew."""
+    g = gen(16)
+    n, k = 96, 128
+    codes, scales, w = weights(g, 4 * n, k, 4, 32, lambda m: torch.ones(m, device="cuda"))
+    w = w.view(4, n, k)
+    f = z.linear_grouped_grad if grad else z.linear_grouped
+    need = max(z.zpp_linear_grouped_workspace(int(grad), z.ZPP_BF16, n if grad else k, z.ZPP_BF16, r, 4, n, k)
+               for r in (5, 100, 600))
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    for rows in (5, 100, 600):
+        a = torch.randint(-4, 5, (rows, n if grad else k), generator=g, device="cuda").to(BF)
+        big = torch.empty(rows + 64, k if grad else n, dtype=BF, device="cuda")
+        for bad in ([0, rows, 0, rows, rows], [-5, 3, 1 << 30, -(1 << 31), (1 << 31) - 1], [rows, 0, 0, 0, 0]):
+            big.fill_(77)
+            f(a, torch.tensor(bad, dtype=torch.int32).cuda(), codes, scales, 4, 32, k if grad else n, out=big[32:-32],
+              workspace=ws)
+            big.fill_(77)
+            o = [0, 1, 2, 3, rows - 1]
+            f(a, torch.tensor(o, dtype=torch.int32).cuda(), codes, scales, 4, 32, k if grad else n, out=big[32:-32],
+              workspace=ws)
+            want = torch.full_like(big, 77)
+            for i in range(4):
+                m = w[i] if grad else w[i].t()
+                want[32 + o[i]:32 + o[i + 1]] = (a[o[i]:o[i + 1]].double() @ m).to(BF)
+            assert torch.equal(big, want), (rows, bad)
+
+
 def test_many_groups(z):
     """4096 weights: the offsets are read in many runs of 64."""
     g = gen(5)
