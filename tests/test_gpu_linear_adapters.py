@@ -280,6 +280,41 @@ def test_non_finite_adapters_and_rows_stay_their_own(z, rows, wt):
     assert torch.equal(da2[[0, 2]], da[[0, 2]]) and torch.equal(db2[[0, 2]], db[[0, 2]])
 
 
+@pytest.mark.parametrize("rows", [2, 4, 40, 100, 300, 600])
+@pytest.mark.parametrize("wt", [BF, F32], ids=["bf16", "f32"])
+def test_what_is_not_finite_reaches_all_that_it_enters(z, rows, wt):
+    """And nothing else: every element that the formulas make of an infinity or a NaN (a factor of zero makes a
+    NaN), in the adapter's rows and gradients, and in a row of x or dy that holds one."""
+    c = Case(17, rows, 96, 160, 4, 32, 3, 16, "runs" if rows == 600 else "any", BF, wt, True, z)
+    c.ids[0], c.ids[1] = 1, 2
+    c.at = dense(z, c.ids, rows, 3)
+    _, t = c.forward(None)
+    own = (c.at == 1)[:, None]
+
+    def lost(got, want):
+        assert torch.equal(~torch.isfinite(got.float()), want.expand(got.shape))
+
+    a, b = c.a.clone(), c.b.clone()
+    c.a[1, 3, 5], c.b[1, 7, 2] = float("inf"), float("nan")
+    y2, t2 = c.forward(None)
+    dx2, da2, db2 = c.backward(t, None)
+    lost(y2, own)
+    lost(t2, own & (torch.arange(16, device="cuda") == 3))
+    lost(dx2, own)
+    # u is lost at rank 2, so that rank of the adapter's gradient is; dB has finite factors alone
+    lost(da2, (torch.arange(3, device="cuda") == 1)[:, None, None] & (torch.arange(16, device="cuda") == 2)[:, None])
+    lost(db2, torch.zeros(1, dtype=torch.bool, device="cuda"))
+    c.a, c.b = a, b
+    first, of_its = (torch.arange(rows, device="cuda") == 0)[:, None], (torch.arange(3, device="cuda") == 1)[:, None, None]
+    c.x[0, 5], c.dy[0, 7] = float("inf"), float("nan")
+    y2, t2 = c.forward(None)
+    dx2, da2, db2 = c.backward(t, None)
+    for got in (y2, t2, dx2):
+        lost(got, first)
+    lost(da2, of_its)  # u of row 0 is
+    lost(db2, of_its & (torch.arange(96, device="cuda") == 7)[:, None])
+
+
 def test_no_rows_and_adapters_without_rows(z):
     c = Case(5, 40, 96, 128, 4, 32, 5, 16, "one", BF, BF, True, z)
     _, t = c.forward(None)
