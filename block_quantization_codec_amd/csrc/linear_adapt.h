@@ -7,14 +7,17 @@
 // a pass of its own would read and write the result again, and round it twice.
 //
 // Rows of a tile may have different adapters. In tiles of many rows up to four bf16
-// adapters are multiplied in turn, low set to zero in the rows that have another; if
-// a sum is not finite, and in tiles of more adapters or of few rows, the rows of each
-// adapter are gathered and multiplied by themselves, so that nothing of an adapter,
-// not its infinities or NaNs either, reaches another's rows.
+// adapters are multiplied in turn, low set to zero in the rows that have another. Zero
+// times an infinity or a NaN is a NaN, so each adapter's elements are looked at as they are
+// loaded: if one that only some of the tile's rows have holds such an element in the
+// wave's columns, and in tiles of more adapters, of binary32 ones or of few rows, the
+// rows of each adapter are gathered and multiplied by themselves. So nothing of an adapter
+// reaches another's rows. (Nor does a sum that overflows: it is its own row's.)
 //
 // Precision: low is binary32 and enters as bf16 parts, like binary32 activations:
-// two of them (16 bits: off by 2^-17, against the 2^-9 of a bf16 result) from
-// bf16 to bf16, three otherwise; a bf16 adapter is one part, a binary32 one three.
+// two of them from bf16 to bf16 (16 bits: the first leaves less than 2^-7 of low, and the
+// second's rounding at most 2^-16 of it, against the 2^-8 of a bf16 result), three
+// otherwise; a bf16 adapter is one part, a binary32 one three.
 #pragma once
 
 #include "linear_device.h"

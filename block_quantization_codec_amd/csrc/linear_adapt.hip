@@ -13,7 +13,7 @@
 // contraction (rows). Rows without an adapter get low = 0 and are in no sum.
 //
 // Sums are binary32; bf16 factors are exact, binary32 ones enter as three bf16
-// parts (low, where everything else is bf16, as two: linear_adapt.h).
+// parts (low, in the sums of bf16 rows for bf16 adapters, as two, off by 2^-16: linear_adapt.h).
 #include <algorithm>
 
 #include "linear_adapt.h"

@@ -398,7 +398,7 @@ int64_t zpp_linear_grouped_workspace(int32_t grad, int32_t in_dtype, int64_t in_
  * The sum is rounded once, to y_dtype. What is said of zpp_linear_blocks holds for x, the
  * codes, y, their strides and the first product's precision. Adapters enter exactly,
  * `reduced` is binary32; where x, y and the adapters are all ZPP_BF16, it enters the
- * second product with 16 bits or more. Nothing of an adapter, not its infinities or NaNs
+ * second product with 16 bits or more (off by at most 2^-16 of itself). Nothing of an adapter, not its infinities or NaNs
  * either, reaches rows that do not name it.
  *
  *   a         in   adapters x rank x in_features elements of ab_dtype, 16-B aligned, without gaps
@@ -426,7 +426,9 @@ zpp_status zpp_linear_adapters(const void *x, int32_t x_dtype, int64_t x_stride,
  *   db[g][n][r] = sum over the rows m of adapter g of dy[m][n] * reduced[m][r]
  *
  * Sums are binary32, in an order fixed by the sizes and the ids, and rounded once: the same
- * inputs give the same bits. An adapter without rows gets zeros.
+ * inputs give the same bits. An adapter without rows gets zeros. Where dy and the adapters are
+ * ZPP_BF16, u and `reduced` enter da and db with 16 bits (off by at most 2^-16 of themselves), and
+ * u enters dx so where dx is ZPP_BF16 too; otherwise in full.
  *
  *   dy        in   rows of out_features elements of dy_dtype, as in zpp_linear_blocks_grad
  *   x         in   rows of in_features elements of dy_dtype, 16-B aligned, x_stride (any of in_features or more)
