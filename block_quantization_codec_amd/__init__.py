@@ -610,7 +610,8 @@ def linear_grouped(x, offsets, codes, scales, bits: int, block: int, out_feature
     codes, and scales, lie one behind the other. ``offsets`` is an ascending int32
     device tensor of one element more than there are weights. Rows before its first
     element and from its last on are in no group: in ``out`` they stay as they are
-    (in a new tensor they are unspecified)."""
+    (in a new tensor they are unspecified). From bf16 to bf16, weights may be rounded to
+    bf16 (past 64 rows a weight on average, and in the gradient past 64 rows)."""
     if stream is not None:
         return _under(stream, linear_grouped, x, offsets, codes, scales, bits, block, out_features, dtype, out, workspace)
     return _linear("zpp_linear_grouped", 0, x, codes, scales, bits, block, out_features, dtype, out, workspace, stream,
@@ -671,7 +672,7 @@ def linear_adapters(x, codes, scales, bits: int, block: int, out_features: int, 
     where each row's A = a[g], B = b[g] and s = ``scaling[g]`` (1 without) are those of g = ``ids`` of the row.
     ``a`` is [adapters, rank, in_features] and ``b`` [adapters, out_features, rank], of one dtype, the rank a
     multiple of 8; ``ids`` has an int32 for each row, and a row whose number is no adapter's has none
-    (None: every row has adapter 0).
+    (None: every row has adapter 0). From bf16 to bf16, W may be rounded to bf16 (past 64 rows, also in the gradient).
     Returns (y, reduced): reduced float32 [rows..., rank] is s * x @ A.T, as :func:`linear_adapters_grad` takes it.
     Autograd does not see the call, as with :func:`linear`. ``workspace``, if given, is a device tensor of at least
     ``zpp_linear_adapters_workspace`` bytes."""

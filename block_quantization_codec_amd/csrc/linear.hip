@@ -45,6 +45,7 @@ struct Plan {
     int64_t rows; // rows of one launch
     int64_t groups; // and groups
     int join_steps; // groups in tiles: what a round's parts cost, in steps (linear_tile.h)
+    int parts;      // tiles: of the operands (linear_big.h, launch_linear_big_as)
 };
 
 // Rows of tiles that `rows` rows make; in groups, each has a last tile of its own, on
@@ -76,10 +77,11 @@ double mid_time(bool in_f32, int mt, int64_t tiles, int64_t splits, int64_t spli
 // What a tiled call takes, in microseconds, with workgroups of mt rows of 16
 // and the contraction in `splits` parts: rounds of workgroups over the CUs
 // times steps times a step's time, and the join. A step takes, with the
-// operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3), measured at
+// operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3, 1 and 2), measured at
 // 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
 double step_time(int parts, int mt) {
-    static constexpr double step_us[3][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0}};
+    static constexpr double step_us[4][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0},
+                                             {1.15, 1.40, 0, 0}};
     return step_us[parts][mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3];
 }
 
@@ -136,7 +138,15 @@ void bound_launch(Plan &p, int64_t groups, int64_t col_tiles) {
 // 45; 200 of 4096 x 11008 int8, 131 against 115.
 //
 // Rows in groups (groups > 0) take the same kernels but the stream of few rows.
-Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t groups, int64_t n_out, int64_t n_in) {
+//
+// From bf16 to bf16, tiles multiply by weights rounded to bf16: an error of the size of the result's
+// own rounding, and with few results the two add up unevenly (to 1.4 times the result's rounding
+// on average, to 2.1 times in a call of one row). So gradients of up to kMidRows rows, in groups or with adapters, take
+// the weights in two parts, off by 2^-16; forward, as many rows multiply by exact codes. It costs, int4: one row of
+// 8192 x 8192 with an adapter 56 us in place of 51, 8 rows over 8 matrices of 11008 x 4096 127 in place of 104;
+// 2048 rows over 64 of those would take 861 in place of 607.
+Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t groups, int64_t n_out, int64_t n_in,
+               bool adapted) {
     Plan p{};
     // rows of one matrix, as far as the sizes say
     const int64_t each_rows = groups == 0 ? rows : ceil_div(rows, std::min(rows, groups));
@@ -169,10 +179,11 @@ Plan make_plan(bool grad, bool in_f32, bool out_f32, int64_t rows, int64_t group
     p.way = Way::tile;
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     const int64_t col_tiles = ceil_div(len, 256), steps = ceil_div(c_len, 64);
-    const int parts = in_f32 ? 2 : out_f32 ? 1 : 0;
+    const bool few = grad && rows <= kMidRows && (groups > 0 || adapted);
+    const int parts = p.parts = in_f32 ? 2 : out_f32 ? 1 : few ? 3 : 0;
     double least = 0;
     for (const int mt : {16, 8, 4, 1}) {
-        if (mt == 16 && parts > 0) continue;
+        if (step_time(parts, mt) == 0) continue;
         if (groups > 0) {
             int join_steps;
             const double t = group_time(parts, mt, rows, groups, len, steps, join_steps);
@@ -337,9 +348,9 @@ int64_t packed_bytes(const Plan &p, bool in_f32, int64_t rows, int64_t c_len) {
 }  // namespace
 
 int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int64_t rows, int64_t groups,
-                         int64_t n_out, int64_t n_in) {
+                         int64_t n_out, int64_t n_in, bool adapted) {
     if (rows == 0) return 0;
-    const Plan p = make_plan(grad, in_f32, out_f32, rows, groups, n_out, n_in);
+    const Plan p = make_plan(grad, in_f32, out_f32, rows, groups, n_out, n_in, adapted);
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     int64_t bytes = needs_pack(p, in_f32, lda, c_len) ? packed_bytes(p, in_f32, rows, c_len) : 0;
     if (p.splits > 1) bytes += p.splits * std::min(rows, p.rows) * ((len + 3) & ~INT64_C(3)) * 4;
@@ -354,7 +365,7 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
                          int64_t groups, const void *codes, const float *scales, int bits, int64_t n_out, int64_t n_in,
                          int log2b, void *out, bool out_f32, int64_t ldo, void *workspace, hipStream_t stream,
                          const LinAdapters *ad, const float *low) {
-    const Plan plan = make_plan(grad, in_f32, out_f32, rows, groups, n_out, n_in);
+    const Plan plan = make_plan(grad, in_f32, out_f32, rows, groups, n_out, n_in, ad != nullptr);
     const int64_t c_len = grad ? n_out : n_in, len = grad ? n_in : n_out;
     const bool pack = needs_pack(plan, in_f32, lda, c_len);
     for (int64_t r0 = 0; r0 < rows; r0 += plan.rows) {
@@ -401,7 +412,7 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
         }
         p.row_tiles = ceil_div(p.rows, 16 * std::max(plan.mt, 1));
         p.col_tiles = plan.way == Way::mid ? ceil_div(n_out, 64 * kMidTiles) : ceil_div(len, 256);
-        const int parts = in_f32 ? 2 : out_f32 ? 1 : 0;
+        const int parts = plan.parts;
         if (groups > 0) {
             for (int64_t g0 = 0; g0 < groups; g0 += plan.groups) {
                 LinArgs q = p;

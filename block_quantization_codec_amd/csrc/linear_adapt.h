@@ -15,9 +15,9 @@
 // reaches another's rows. (Nor does a sum that overflows: it is its own row's.)
 //
 // Precision: low is binary32 and enters as bf16 parts, like binary32 activations:
-// two of them from bf16 to bf16 (16 bits: the first leaves less than 2^-7 of low, and the
-// second's rounding at most 2^-16 of it, against the 2^-8 of a bf16 result), three
-// otherwise; a bf16 adapter is one part, a binary32 one three.
+// two of them where the product takes activations and weights as one each, from bf16 to bf16
+// (16 bits: the first leaves less than 2^-7 of low, and the second's rounding at most 2^-16 of it,
+// against the 2^-8 of a bf16 result), three otherwise; a bf16 adapter is one part, a binary32 one three.
 #pragma once
 
 #include "linear_device.h"

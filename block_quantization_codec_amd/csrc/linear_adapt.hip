@@ -796,7 +796,7 @@ int64_t linear_adapters_workspace(bool grad, bool in_f32, int64_t lda, bool out_
                                   int64_t n_in, int64_t adapters, int64_t rank) {
     int64_t most = 0;
     if (rows > 0)
-        most = std::max(linear_workspace(grad, in_f32, lda, out_f32, rows, 0, n_out, n_in),
+        most = std::max(linear_workspace(grad, in_f32, lda, out_f32, rows, 0, n_out, n_in, true),
                         down_workspace(rows, grad ? n_out : n_in, adapters, rank));
     if (!grad) return align16(most);
     // low of the backward pass, then what one step after the other uses

@@ -29,7 +29,8 @@
 // of the results' norm in place of 1.7e-3. That is one product in place of the
 // three that a caller gets by asking for binary32 results: weights are three parts
 // of RN(code * s) where input or result is binary32 (forward, bf16 to binary32
-// takes exact codes instead, linear_mid.h). Sums are binary32 throughout.
+// takes exact codes instead, linear_mid.h), and two of it in the gradients of few rows that
+// linear.hip says. Sums are binary32 throughout.
 //
 // A step is taken in two halves of 32 indices (one matrix instruction deep).
 // With 256 rows a wave has the SIMD to itself (256 sums a lane), so nothing but
@@ -125,7 +126,7 @@ struct LinBig {
     // Buffers of activations: up to 8, within 144 KB of LDS (72 KB where two
     // workgroups share a CU). Sets of codes in registers.
     static constexpr int kBufs = PA == 3 ? (MT == 8 ? 3 : MT == 4 ? 4 : 8) : MT >= 8 ? 4 : 8;
-    static constexpr int kDepth = MT >= 8 || (PB == 3 && MT == 4) ? 2 : 4;
+    static constexpr int kDepth = MT >= 8 || (PB > 1 && MT == 4) ? 2 : 4;
 
     // Codes of 16 indices of a lane's 4 columns; scales of the 4 columns (y),
     // or of index (lane & 15) in both 32-column halves (dx).
@@ -347,7 +348,7 @@ struct LinBig {
     static __device__ __forceinline__ void pack(const Part &f, B &b) {
         constexpr int t = GRAD ? X % 4 : X / 4, d = GRAD ? X / 4 : X % 4;
         uint32_t w[PB];
-        to_parts<PB>(f.f[0], f.f[1], w);
+        low_parts<PB>(f.f[0], f.f[1], w);
 #pragma unroll
         for (int i = 0; i < PB; ++i) b[i][t][d] = w[i];
     }
@@ -384,7 +385,7 @@ struct LinBig {
     // pair k of parts.
     template <int T0, int T1, int K, class F>
     static __device__ __forceinline__ void products_from(const A &a, const B &b, f32x4 (&acc)[4], F &&after) {
-        // pairs in order: (2,0) (1,1) (1,0) (0,2) (0,1) (0,0) of three and three parts, (0,2) (0,1) (0,0) of one and three
+        // pairs in order: (2,0) (1,1) (1,0) (0,2) (0,1) (0,0) of three and three parts, the last three of one and three
         constexpr int pairs = PA == 3 ? 6 : PB;
         if constexpr (K < pairs) {
             constexpr int i = PA == 1 ? 0 : K == 0 ? 2 : K < 3 ? 1 : 0;
@@ -458,6 +459,7 @@ struct LinBig {
         } else {
             products<0, 4>(a[M % kRing], b, acc[M], [&](auto k) {
                 if constexpr (k.value < 3) piece<HN, k.value, x0, x1>(raw, s, bn, f, scale);
+                if constexpr (PB == 2 && k.value == 1) piece<HN, 2, x0, x1>(raw, s, bn, f, scale);
             });
         }
         if constexpr (M + 1 < MT) rows_from<HN, M + 1>(here, then, b, raw, s, bn, a, scale, acc, before);
@@ -744,7 +746,7 @@ __device__ __forceinline__ void linear_big_tile(const LinArgs &p, const LinPlace
 }
 
 template <bool GRAD, int BITS, int PA, int PB, int MT, LinMode MODE>
-__global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB == 3 && MT >= 4) ? 1 : 2) void linear_big_kernel(
+__global__ __launch_bounds__(kBlockThreads, MT == 16 || (PB > 1 && MT >= 4) ? 1 : 2) void linear_big_kernel(
     LinArgs p) {
     using L = LinBig<GRAD, BITS, PA, PB, MT>;
     __shared__ __attribute__((aligned(128))) uint8_t tiles[L::kBufs][L::kBytes];
@@ -774,7 +776,7 @@ hipError_t launch_linear_big_one(const LinArgs &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// parts 0: bf16 to bf16; 1: bf16 to binary32; 2: binary32 activations. mt is the plan's.
+// parts 0: bf16 to bf16; 1: bf16 to binary32; 2: binary32 activations; 3: bf16 to bf16, few rows. mt is the plan's.
 template <LinMode MODE, bool GRAD, int BITS>
 hipError_t launch_linear_big_as(const LinArgs &p, int parts, int mt, hipStream_t stream) {
     if (parts == 2) {
@@ -788,6 +790,11 @@ hipError_t launch_linear_big_as(const LinArgs &p, int parts, int mt, hipStream_t
             if (mt == 4) return launch_linear_big_one<MODE, GRAD, BITS, 1, 3, 4>(p, stream);
             return launch_linear_big_one<MODE, GRAD, BITS, 1, 3, 1>(p, stream);
         }
+    }
+    if constexpr (GRAD && MODE != LinMode::one) {
+        if (parts == 3)
+            return mt == 4 ? launch_linear_big_one<MODE, GRAD, BITS, 1, 2, 4>(p, stream)
+                           : launch_linear_big_one<MODE, GRAD, BITS, 1, 2, 1>(p, stream);
     }
     if (mt == 16) return launch_linear_big_one<MODE, GRAD, BITS, 1, 1, 16>(p, stream);
     if (mt == 8) return launch_linear_big_one<MODE, GRAD, BITS, 1, 1, 8>(p, stream);

@@ -51,7 +51,7 @@ hipError_t launch_linear(bool grad, const void *a, bool in_f32, int64_t lda, int
                          int log2b, void *out, bool out_f32, int64_t ldo, void *workspace, hipStream_t stream,
                          const LinAdapters *ad = nullptr, const float *low = nullptr);
 int64_t linear_workspace(bool grad, bool in_f32, int64_t lda, bool out_f32, int64_t rows, int64_t groups,
-                         int64_t n_out, int64_t n_in);
+                         int64_t n_out, int64_t n_in, bool adapted = false);
 
 // reduced: [rows][rank], s x A^T of each row's adapter. da and db may be null.
 hipError_t launch_linear_adapters(const void *x, bool in_f32, int64_t x_stride, int64_t rows, const void *codes,

@@ -368,7 +368,8 @@ int64_t zpp_linear_blocks_workspace(int32_t grad, int32_t in_dtype, int64_t in_s
  *   block           in   block size B; divides out_features * in_features
  *   workspace_bytes in   at least zpp_linear_grouped_workspace(...) (ZPP_ERR_ARG otherwise)
  * Everything else is as in zpp_linear_blocks: types, strides, precision (where that speaks of more than 64 rows:
- * where rows / groups is more than 64), and rows that hold infinite or NaN elements.
+ * where rows / groups is more than 64), and rows that hold infinite or NaN elements. But in the gradient of up to 64
+ * rows, all groups together, weights enter with 16 bits or more (off by at most 2^-16) from ZPP_BF16 to ZPP_BF16 too.
  */
 zpp_status zpp_linear_grouped(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, const int32_t *offsets,
                               int64_t groups, const void *codes, const float *scales, int32_t bits,
@@ -428,7 +429,9 @@ zpp_status zpp_linear_adapters(const void *x, int32_t x_dtype, int64_t x_stride,
  * Sums are binary32, in an order fixed by the sizes and the ids, and rounded once: the same
  * inputs give the same bits. An adapter without rows gets zeros. Where dy and the adapters are
  * ZPP_BF16, u and `reduced` enter da and db with 16 bits (off by at most 2^-16 of themselves), and
- * u enters dx so where dx is ZPP_BF16 too; otherwise in full.
+ * u enters dx so where dx is ZPP_BF16 too and there are more than 64 rows; otherwise in full. Weights enter dx
+ * as in zpp_linear_blocks_grad, but of up to 64 rows from ZPP_BF16 to ZPP_BF16 with 16 bits or more (off by at most
+ * 2^-16), not as bf16.
  *
  *   dy        in   rows of out_features elements of dy_dtype, as in zpp_linear_blocks_grad
  *   x         in   rows of in_features elements of dy_dtype, 16-B aligned, x_stride (any of in_features or more)

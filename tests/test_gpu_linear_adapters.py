@@ -327,6 +327,27 @@ def test_no_rows_and_adapters_without_rows(z):
     assert bool((da == 0).all()) and bool((db == 0).all())
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("wt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 2, 5, 16, 40, 64])
+def test_few_rows_have_the_results_own_rounding_alone(z, rows, wt, bits):
+    """From bf16 to bf16: up to 64 rows, weights enter with 16 bits or more, not as bf16, forward and back."""
+    for n, k, adapters, rank, kind in ((200, 416, 3, 16, "any"), (2752, 1152, 2, 24, "runs"), (67, 1056, 1, 8, "null")):
+        c = Case(19, rows, n, k, bits, 32, adapters, rank, kind, BF, wt, False, z)
+        y, t = c.forward(None)
+        dx, _, _ = c.backward(t, None)
+        for got, x, w, m, m2 in ((y, c.x, c.w.t(), c.a, c.b.transpose(1, 2)), (dx, c.dy, c.w, c.b.transpose(1, 2), c.a)):
+            low, mags_l = c.low(x, m)
+            want = x.double() @ w + c.up(low, m2)
+            # as in check_real, with a weight's second part off by half a step of 2^-8 of what the first leaves, 2^-8
+            # in its binade: 2^-16, and low's likewise
+            mags, mags_m = x.double().abs() @ w.abs(), c.up(low.abs(), m2.abs())
+            tol = mags * ((w.shape[0] + 16) * U + 2.0 ** -16) + mags_m * ((rank + w.shape[0] // 64 + 16) * U + 2.0 ** -16) + \
+                c.up(mags_l * (w.shape[0] + 16) * U, m2.abs()) + want.abs() * 2.0 ** -8
+            off = (got.double() - want).abs()
+            assert bool((off <= tol * (1 + 2.0 ** -7)).all()), (n, k, (off / tol).max().item())
+
+
 def test_gradients_against_differences(z):
     """The gradients' products with directions, against differences of the forward formula in 64 bits: it is
     bilinear in A and B and linear in x, so central differences are exact there but for rounding."""

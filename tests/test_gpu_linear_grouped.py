@@ -124,6 +124,34 @@ def test_one_group_gives_what_one_weight_gives_within_its_roundings(z, grad):
                 at += c
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("grad", [False, True], ids=["y", "dx"])
+def test_few_rows_have_the_results_own_rounding_alone(z, grad, bits):
+    """From bf16 to bf16: weights enter with 16 bits or more, not as bf16, up to 64 rows a group, back up to 64 rows
+    a call."""
+    g = gen(18)
+    for counts in ([1], [0, 1, 2], [5, 0, 3, 9], [16] * 4, [64]) if grad else ([1], [5, 0, 3, 9], [60, 100, 2, 30], [64] * 3):
+        for n, k, block in ((632, 448, 128), (1000, 224, 32), (4992, 96, 32), (67, 1056, 32)):
+            w = torch.randn(len(counts) * n, k, generator=g, device="cuda") * 0.02
+            codes, scales = z.quantize(w, block, bits)
+            w = z.dequantize(codes, scales, bits, len(counts) * n * k, block, dtype=F32).double().view(-1, n, k)
+            a = torch.randn(sum(counts), n if grad else k, generator=g, device="cuda").to(BF)
+            f = z.linear_grouped_grad if grad else z.linear_grouped
+            got = f(a, ascending(counts), codes, scales, bits, block, k if grad else n).double()
+            at = 0
+            for i, c in enumerate(counts):
+                m = w[i] if grad else w[i].t()
+                x = a[at:at + c].double()
+                want, mags = x @ m, x.abs() @ m.abs()
+                # each of the binary32 sums' additions 2^-24 of the magnitudes, and as much for code times scale; a
+                # weight's second part half a step of 2^-8 of what the first leaves, 2^-8 in its binade: 2^-16; the
+                # result half a step of bf16
+                tol = mags * ((m.shape[0] + 8) * 2.0 ** -24 + 2.0 ** -16) + want.abs() * 2.0 ** -8
+                off = (got[at:at + c] - want).abs()
+                assert bool((off <= tol * (1 + 2.0 ** -7)).all()), (counts, n, k, (off / tol).max().item())
+                at += c
+
+
 @pytest.mark.parametrize("grad", [False, True], ids=["y", "dx"])
 def test_non_finite_rows_stay_their_own(z, grad):
     g = gen(2)
