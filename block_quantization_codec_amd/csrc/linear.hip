@@ -78,10 +78,11 @@ double mid_time(bool in_f32, int mt, int64_t tiles, int64_t splits, int64_t spli
 // and the contraction in `splits` parts: rounds of workgroups over the CUs
 // times steps times a step's time, and the join. A step takes, with the
 // operands' parts (rows of the table: 1 and 1, 1 and 3, 3 and 3, 1 and 2), measured at
-// 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights:
+// 128 to 4096 rows of 8192 x 8192 and 11008 x 4096 weights (1 and 2: 1.27 and 1.43 times as long as
+// 1 and 1, 16 and 64 rows of 8192 x 65536):
 double step_time(int parts, int mt) {
     static constexpr double step_us[4][4] = {{0.92, 1.05, 1.10, 1.60}, {1.50, 1.90, 3.20, 0}, {1.60, 3.20, 4.80, 0},
-                                             {1.15, 1.40, 0, 0}};
+                                             {1.17, 1.50, 0, 0}};
     return step_us[parts][mt == 1 ? 0 : mt == 4 ? 1 : mt == 8 ? 2 : 3];
 }
 
